@@ -41,7 +41,7 @@ CSRC = os.path.join(ROOT, "moe_grouped_gemm_tiles_amd", "csrc")
 # Sources whose change invalidates a traffic record, per kernel family.
 KERNEL_SOURCES = {
     "gemm": ["dg_kernels.hpp", "dg_api.hip", "dg_common.hpp"],
-    "quant": ["dg_quant.hip", "dg_common.hpp"],
+    "quant": ["dg_quant.hip", "dg_cast.hpp", "dg_common.hpp"],
     "mqa": ["dg_mqa.hip", "dg_common.hpp"],
 }
 
