@@ -318,6 +318,127 @@ dg_status dg_per_block_cast_to_fp8(const void* w, int64_t ldw, dg_dtype w_dtype,
                                    void* sf, int ue8m0, int n, int k, hipStream_t stream);
 
 /*
+ * Residual addition, RMS norm and the per-token FP8 cast in one pass: what
+ * stands before a GEMM or an expert layer of a decoder block.
+ *   (The pages leave the cast and its fusion with what precedes it to the
+ *   caller, [README] "Interfaces > Notices".)
+ * Per row, in FP32: s = x + residual; r = 1 / sqrt(mean(s^2) + eps);
+ * v = s * r * weight; then v is cast as by dg_per_token_cast_to_fp8 (the sum s
+ * is rounded to dtype only where it is stored; the norm is of the unrounded s).
+ *
+ * x             [m, k], dtype BF16 or FP32, row stride ldx; all row-major operands
+ *               of this call have 16-byte aligned rows and a stride >= k.
+ * residual      optional [m, k], same dtype; given exactly when residual_out is.
+ * residual_out  [m, k], same dtype: s.  May equal residual or x (in place).
+ * weight        [k], BF16 or FP32 (weight_dtype), 16-B aligned.
+ * q, sf         the codes [m, k] (row stride ldq, ldq % 8 == 0) and the transposed
+ *               scales, FP32 [k/128][ld_sf] or (ue8m0 != 0) packed words
+ *               [ceil(k/512)][ld_sf], as in dg_per_token_cast_to_fp8.
+ * y             optional [m, k], dtype: v itself (for a router, or training).
+ * rstd          optional FP32 [m]: r, for dg_rms_norm_backward.
+ * An Inf or NaN in v is kept: the block's scale is not finite (UE8M0: 255) and
+ * so is what the pair stands for.
+ * eps >= 0; k % 128 != 0 or k > 16384 -> DG_ERROR_NOT_SUPPORTED; m or k == 0 ->
+ * DG_SUCCESS.
+ */
+dg_status dg_add_rms_norm_cast_to_fp8(const void* x, int64_t ldx, const void* residual, int64_t ld_residual,
+                                      void* residual_out, int64_t ld_residual_out, dg_dtype dtype,
+                                      const void* weight, dg_dtype weight_dtype, float eps, void* q, int64_t ldq,
+                                      void* sf, int64_t ld_sf, int ue8m0, void* y, int64_t ldy, float* rstd, int m,
+                                      int k, hipStream_t stream);
+
+/*
+ * Gradient of the norm above (the cast passes its gradient through unchanged).
+ * With xhat = s * rstd and g = dy * weight, in FP32:
+ *   dx = rstd * (g - xhat * mean(g * xhat)) + dresidual      (of x and of residual alike)
+ *   dw (+)= sum over rows of dy * xhat
+ *
+ * dy, s        [m, k], dtype; s is the stored sum (residual_out, or x where there
+ *              was no residual), rstd the forward's.
+ * dresidual    optional [m, k], dtype: the gradient that reached residual_out.
+ * dx           [m, k], dtype; may equal dy or dresidual.
+ * dw           FP32 [k], 16-B aligned; accumulate_dw != 0 adds to it, else it is
+ *              overwritten (m == 0: with zeros).
+ * workspace    dg_get_rms_norm_backward_workspace_size(m, k) bytes, 256-byte
+ *              aligned, any contents; nothing is kept in it between calls.
+ * The result is the same bits every time (partial sums in a fixed order).
+ * Sizes and errors as above.
+ */
+dg_status dg_rms_norm_backward(const void* dy, int64_t ld_dy, const void* s, int64_t ld_s, dg_dtype dtype,
+                               const void* weight, dg_dtype weight_dtype, const float* rstd, const void* dresidual,
+                               int64_t ld_dresidual, void* dx, int64_t ld_dx, float* dw, int accumulate_dw, int m,
+                               int k, void* workspace, size_t workspace_bytes, hipStream_t stream);
+size_t dg_get_rms_norm_backward_workspace_size(int m, int k);
+
+/*
+ * A whole gated expert layer for a few tokens (MoE decode): routing, both
+ * products, the activation and the weighted sum over a token's experts, in two
+ * launches.  For token t and j < top_k with e = topk_ids[t][j] in [0, num_experts):
+ *   h = x[t] @ w13[e]^T,   a = silu(h[0..inter)) * h[inter..2*inter),
+ *   out[t] = sum over such j of topk_weights[t][j] * (a_j @ w2[e]^T).
+ * The weights of the experts that have tokens are read once per 512 / top_k
+ * tokens: this is the form for batches of that size; larger ones belong to the
+ * grouped GEMMs above.  a is rounded to BF16 between the products.
+ *
+ * x             E4M3 [m, hidden], row stride ldx (a multiple of 16), 16-B aligned.
+ * sfx           FP32 [hidden/128][ld_sfx], ld_sfx >= m, ld_sfx % 4 == 0 (as sfa).
+ * w13           E4M3 [num_experts, 2*inter, hidden] contiguous: gate rows, then up rows.
+ * sf13          FP32 [num_experts][2*inter/128][hidden/128] contiguous.
+ * w2            E4M3 [num_experts, hidden, inter] contiguous.
+ * sf2           FP32 [num_experts][hidden/128][inter/128] contiguous.
+ * topk_ids      DEVICE int32 [m, top_k] contiguous; an id outside [0, num_experts)
+ *               is no expert of this device and adds nothing (its weight is not read).
+ * topk_weights  FP32 [m, top_k] contiguous.
+ * out           BF16 [m, hidden], row stride ld_out (a multiple of 8), 16-B aligned.
+ *               Every row is written; a token without an expert here gets zeros.
+ * workspace     dg_get_moe_workspace_size(m, top_k, inter) bytes, 256-byte aligned,
+ *               any contents (a of every token and slot).
+ * hidden % 128 != 0, inter % 128 != 0, inter == 0, top_k or num_experts == 0, top_k > 64 or
+ * num_experts > 1024 -> DG_ERROR_NOT_SUPPORTED; m or hidden == 0 -> DG_SUCCESS.
+ * The _ue8m0 form takes packed scale words, as the UE8M0 GEMMs do: sfx
+ * [ceil(hidden/512)][ld_sfx], sf13 [num_experts][2*inter/128][ceil(hidden/512)],
+ * sf2 [num_experts][hidden/128][ceil(inter/512)].
+ */
+dg_status dg_fp8_moe_few_tokens(const void* x, int64_t ldx, const float* sfx, int64_t ld_sfx, const void* w13,
+                                const float* sf13, const void* w2, const float* sf2, const int32_t* topk_ids,
+                                const float* topk_weights, void* out, int64_t ld_out, int m, int top_k,
+                                int num_experts, int hidden, int inter, void* workspace, size_t workspace_bytes,
+                                hipStream_t stream);
+dg_status dg_fp8_moe_few_tokens_ue8m0(const void* x, int64_t ldx, const int32_t* sfx, int64_t ld_sfx, const void* w13,
+                                      const int32_t* sf13, const void* w2, const int32_t* sf2,
+                                      const int32_t* topk_ids, const float* topk_weights, void* out, int64_t ld_out,
+                                      int m, int top_k, int num_experts, int hidden, int inter, void* workspace,
+                                      size_t workspace_bytes, hipStream_t stream);
+size_t dg_get_moe_workspace_size(int m, int top_k, int inter);
+
+/*
+ * Global norm over many gradient tensors, and clipping by it:
+ *   norm = sqrt(sum over all tensors of g^2),
+ *   out  = g * min(1, max_norm / (norm + 1e-6)).
+ * Squares are summed in FP64.  With a norm that is not finite the factor is
+ * what the formula gives (0 for Inf, NaN for NaN); look at *norm.
+ *
+ * grads, out    HOST arrays of num_tensors descriptors (read before the call
+ *               returns); data is a device pointer aligned to its type only.  out
+ *               == NULL clips in place (then nothing is written where the factor is
+ *               1); else out[i] has grads[i]'s numel and dtype and each out[i] is
+ *               that gradient itself or overlaps none of them.
+ * max_norm      >= 0; with infinity the factor is 1 whatever the norm (in place the
+ *               call then only measures it).
+ * norm          DEVICE FP32 [1].
+ * workspace     dg_get_clip_workspace_size() bytes, 256-byte aligned, any contents.
+ * Two launches per 128 tensors; the same bits every time.
+ */
+typedef struct {
+  void* data;
+  int64_t numel;
+  dg_dtype dtype;
+} dg_tensor;
+dg_status dg_clip_grad_norm(const dg_tensor* grads, const dg_tensor* out, int num_tensors, float max_norm, float* norm,
+                            void* workspace, size_t workspace_bytes, hipStream_t stream);
+size_t dg_get_clip_workspace_size(void);
+
+/*
  * Weighted-ReLU MQA logits (the lightning-indexer scoring kernel, non-paged).
  *   [README] "V3.2 MQA kernels for the indexer": for query i and each key j
  *   in [ks[i], ke[i]),

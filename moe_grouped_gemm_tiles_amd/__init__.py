@@ -17,6 +17,13 @@ as mirrored on the page "Weight gradient kernels for dense and MoE models #95":
   (the caller's FP8 cast, writing the scale layouts the GEMMs take)
 * ``fp8_mqa_logits(q, (kv, kv_sf), weights, ks, ke, clean_logits, out)``
   (README "V3.2 MQA kernels for the indexer")
+* ``add_rms_norm_cast_to_fp8(x, weight, eps, q, sf, residual, residual_out, y, rstd)``
+  (residual addition, RMS norm and the per-token cast in one pass) and its
+  gradient ``rms_norm_backward(dy, s, weight, rstd, dx, dw, dresidual)``
+* ``fp8_moe_few_tokens((x, sfx), (w13, sf13), (w2, sf2), topk_ids, topk_weights, out)``
+  (a whole gated expert layer for a few tokens, two launches)
+* ``clip_grad_norm(grads, max_norm, norm, out)`` (global norm over many tensors
+  and clipping by it; ``tensor_list`` keeps the descriptors between calls)
 * ``get_mk_alignment_for_contiguous_layout()``, ``get_sf_aligned_size(mn)``,
   ``set_num_cus(n)`` / ``get_num_cus()``, ``get_workspace_size(m, n, k)`` and
   ``alloc_workspace(m, n, k)``
@@ -60,6 +67,16 @@ __all__ = [
     "per_token_cast_to_fp8",
     "per_block_cast_to_fp8",
     "fp8_mqa_logits",
+    "add_rms_norm_cast_to_fp8",
+    "rms_norm_backward",
+    "alloc_rms_norm_backward_workspace",
+    "fp8_moe_few_tokens",
+    "get_moe_workspace_size",
+    "alloc_moe_workspace",
+    "clip_grad_norm",
+    "alloc_clip_workspace",
+    "TensorList",
+    "tensor_list",
     "transform_sf_into_required_layout",
     "get_mn_major_tma_aligned_tensor",
     "get_mn_major_tma_aligned_packed_ue8m0_tensor",
@@ -87,6 +104,8 @@ _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _i32 = ctypes.c_int
 _sz = ctypes.c_size_t
+
+_f = ctypes.c_float
 
 _SIGNATURES = {
     "dg_fp8_gemm_nt": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _i64, _i32,
@@ -116,6 +135,18 @@ _SIGNATURES = {
     "dg_per_token_cast_to_fp8": (_i32, [_vp, _i64, _i32, _vp, _i64, _vp, _i64, _i32, _i32, _i32, _vp]),
     "dg_per_block_cast_to_fp8": (_i32, [_vp, _i64, _i32, _vp, _i64, _vp, _i32, _i32, _i32, _vp]),
     "dg_fp8_mqa_logits": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _i32, _vp]),
+    "dg_add_rms_norm_cast_to_fp8": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _i32, _f, _vp, _i64, _vp, _i64,
+                                           _i32, _vp, _i64, _vp, _i32, _i32, _vp]),
+    "dg_rms_norm_backward": (_i32, [_vp, _i64, _vp, _i64, _i32, _vp, _i32, _vp, _vp, _i64, _vp, _i64, _vp, _i32,
+                                    _i32, _i32, _vp, _sz, _vp]),
+    "dg_get_rms_norm_backward_workspace_size": (_sz, [_i32, _i32]),
+    "dg_fp8_moe_few_tokens": (_i32, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64,
+                                     _i32, _i32, _i32, _i32, _i32, _vp, _sz, _vp]),
+    "dg_fp8_moe_few_tokens_ue8m0": (_i32, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64,
+                                           _i32, _i32, _i32, _i32, _i32, _vp, _sz, _vp]),
+    "dg_get_moe_workspace_size": (_sz, [_i32, _i32, _i32]),
+    "dg_clip_grad_norm": (_i32, [_vp, _vp, _i32, _f, _vp, _vp, _sz, _vp]),
+    "dg_get_clip_workspace_size": (_sz, []),
     "dg_transform_sf_into_required_layout": (_i32, [_vp, _vp, _i32, _i32, _i32, _i64, _i32, _vp]),
     "dg_get_mk_alignment_for_contiguous_layout": (_i32, []),
     "dg_get_sf_aligned_size": (_i64, [_i64]),
@@ -494,6 +525,206 @@ def fp8_mqa_logits(q: torch.Tensor, kv_pair, weights: torch.Tensor, ks: torch.Te
                                _stream(out))
     _check(st)
     return out
+
+
+def _rows(t: torch.Tensor, like: torch.Tensor, name: str):
+    """(pointer, row stride) of a 2-D operand with like's shape, dtype and device."""
+    if t.dtype != like.dtype or t.device != like.device or t.shape != like.shape or not _unit_last_stride(t):
+        raise ValueError(f"{name} must match the input's shape, dtype and device and be contiguous in its last "
+                         "dimension")
+    return t.data_ptr(), _ld(t, 0, 16 // t.element_size())
+
+
+def _norm_weight(weight: torch.Tensor, x: torch.Tensor) -> int:
+    if weight.dtype not in _DTYPES or weight.device != x.device or weight.shape != (x.shape[1],) \
+            or not weight.is_contiguous():
+        raise ValueError("weight must be a contiguous bfloat16 or float32 tensor [K] on the input's device")
+    return _DTYPES[weight.dtype]
+
+
+def _scratch(workspace: torch.Tensor | None, size: int, device: torch.device, name: str = "workspace"):
+    """(tensor to keep alive, pointer, bytes) of a workspace with any contents; without one, a
+    fresh one from torch's allocator (its blocks are at least 512-byte aligned)."""
+    if workspace is None:
+        workspace = torch.empty(size, dtype=torch.uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor on the output's device")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def add_rms_norm_cast_to_fp8(x: torch.Tensor, weight: torch.Tensor, eps: float, q: torch.Tensor, sf: torch.Tensor,
+                             residual: torch.Tensor | None = None, residual_out: torch.Tensor | None = None,
+                             y: torch.Tensor | None = None, rstd: torch.Tensor | None = None):
+    """s = x + residual, v = s / sqrt(mean(s^2) + eps) * weight, and v's per-token FP8 cast in one
+    pass: x [M, K] -> q E4M3 [M, K], sf FP32 [K/128, ld >= M] or packed UE8M0 int32 [ceil(K/512), ld]
+    (the GEMMs' a operand), residual_out = s (may be residual itself).  Optional outputs: y = v in
+    x's dtype, rstd FP32 [M] for ``rms_norm_backward``."""
+    lib = load_library()
+    dt, ue = _cast_args(x, q, sf)
+    m, k = x.shape
+    wdt = _norm_weight(weight, x)
+    if sf.dim() != 2 or sf.shape[0] != _sf_rows(k, ue) or sf.shape[1] < m:
+        raise ValueError(f"sf shape {tuple(sf.shape)} does not fit x {tuple(x.shape)}")
+    if q.device != x.device or sf.device != x.device:
+        raise ValueError("q and sf must be on x's device")
+    if (residual is None) != (residual_out is None):
+        raise ValueError("residual and residual_out go together")
+    res, ldr = _rows(residual, x, "residual") if residual is not None else (None, 0)
+    ro, ldro = _rows(residual_out, x, "residual_out") if residual_out is not None else (None, 0)
+    yp, ldy = _rows(y, x, "y") if y is not None else (None, 0)
+    if rstd is not None and (rstd.dtype != torch.float32 or rstd.device != x.device or rstd.shape != (m,)
+                             or not rstd.is_contiguous()):
+        raise ValueError("rstd must be a contiguous float32 tensor [M] on x's device")
+    st = lib.dg_add_rms_norm_cast_to_fp8(
+        x.data_ptr(), _ld(x, 0, 16 // x.element_size()), res, ldr, ro, ldro, dt, weight.data_ptr(), wdt, eps,
+        q.data_ptr(), _ld(q, 0, 8), sf.data_ptr(), _ld(sf, 0, 4), ue, yp, ldy,
+        rstd.data_ptr() if rstd is not None else None, m, k, _stream(x))
+    _check(st)
+    return q, sf
+
+
+def alloc_rms_norm_backward_workspace(m: int, k: int, device=None) -> torch.Tensor:
+    """A workspace for ``rms_norm_backward`` of [m, k] inputs (any contents)."""
+    size = int(load_library().dg_get_rms_norm_backward_workspace_size(m, k))
+    return torch.empty(size, dtype=torch.uint8, device=device if device is not None else torch.cuda.current_device())
+
+
+def rms_norm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, dx: torch.Tensor,
+                      dw: torch.Tensor, dresidual: torch.Tensor | None = None, accumulate: bool = False,
+                      workspace: torch.Tensor | None = None):
+    """Gradient of the norm of ``add_rms_norm_cast_to_fp8``: dy [M, K] (of v), s the stored sum, rstd
+    the forward's -> dx (of x and of residual alike; dresidual, the gradient that reached
+    residual_out, is added) and dw FP32 [K] (overwritten, or added to with ``accumulate``).
+    dx may be dy or dresidual itself."""
+    lib = load_library()
+    if dy.dtype not in _DTYPES or not dy.is_cuda or dy.dim() != 2 or not _unit_last_stride(dy):
+        raise TypeError("dy must be a 2-D bfloat16 or float32 GPU tensor, contiguous in its last dimension")
+    m, k = dy.shape
+    wdt = _norm_weight(weight, dy)
+    for t, shape, nm in ((rstd, (m,), "rstd"), (dw, (k,), "dw")):
+        if t.dtype != torch.float32 or t.device != dy.device or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{nm} must be a contiguous float32 tensor {list(shape)} on dy's device")
+    sp, lds = _rows(s, dy, "s")
+    dxp, lddx = _rows(dx, dy, "dx")
+    dr, lddr = _rows(dresidual, dy, "dresidual") if dresidual is not None else (None, 0)
+    ws, wsp, wsb = _scratch(workspace, lib.dg_get_rms_norm_backward_workspace_size(m, k), dy.device)
+    st = lib.dg_rms_norm_backward(dy.data_ptr(), _ld(dy, 0, 16 // dy.element_size()), sp, lds, _DTYPES[dy.dtype],
+                                  weight.data_ptr(), wdt, rstd.data_ptr(), dr, lddr, dxp, lddx, dw.data_ptr(),
+                                  bool(accumulate), m, k, wsp, wsb, _stream(dy))
+    _check(st)
+    return dx, dw
+
+
+def get_moe_workspace_size(m: int, top_k: int, inter: int) -> int:
+    """Bytes of workspace ``fp8_moe_few_tokens`` needs for m tokens."""
+    return int(load_library().dg_get_moe_workspace_size(m, top_k, inter))
+
+
+def alloc_moe_workspace(m: int, top_k: int, inter: int, device=None) -> torch.Tensor:
+    """A workspace for ``fp8_moe_few_tokens`` with up to m tokens (any contents)."""
+    size = get_moe_workspace_size(m, top_k, inter)
+    return torch.empty(size, dtype=torch.uint8, device=device if device is not None else torch.cuda.current_device())
+
+
+def fp8_moe_few_tokens(x_pair, w13_pair, w2_pair, topk_ids: torch.Tensor, topk_weights: torch.Tensor,
+                       out: torch.Tensor, workspace: torch.Tensor | None = None):
+    """A whole gated expert layer for a few tokens: x E4M3 [M, H], w13 E4M3 [E, 2I, H] (gate rows,
+    then up rows), w2 E4M3 [E, H, I], their scales in the GEMMs' layouts (FP32, or all packed UE8M0
+    int32), topk_ids int32 [M, top_k] (ids outside [0, E) add nothing), topk_weights FP32
+    [M, top_k] -> out BF16 [M, H]."""
+    lib = load_library()
+    x, sfx = x_pair
+    w13, sf13 = w13_pair
+    w2, sf2 = w2_pair
+    for t, nm in ((x, "x"), (w13, "w13"), (w2, "w2")):
+        _fp8(t, nm)
+    ue = _sf(sfx, sf13)
+    if _sf(sfx, sf2) != ue:
+        raise TypeError("all scales must be float32, or all int32 (packed UE8M0)")
+    for t, nm in ((w13, "w13"), (w2, "w2"), (sf13, "sf13"), (sf2, "sf2"), (topk_ids, "topk_ids"),
+                  (topk_weights, "topk_weights")):
+        _dense_contig(t, nm)
+    if topk_ids.dtype != torch.int32 or topk_weights.dtype != torch.float32:
+        raise TypeError("topk_ids must be int32 and topk_weights float32")
+    if out.dtype != torch.bfloat16 or not _unit_last_stride(out):
+        raise TypeError("out must be a bfloat16 tensor, contiguous in its last dimension")
+    for t in (x, sfx, w13, sf13, w2, sf2, topk_ids, topk_weights):
+        if t.device != out.device:
+            raise ValueError("all operands must be on out's device")
+    m, h = x.shape
+    e, i2, _ = w13.shape
+    i = i2 // 2
+    top_k = topk_ids.shape[1]
+    if w13.shape != (e, 2 * i, h) or w2.shape != (e, h, i) or topk_ids.shape != (m, top_k) \
+            or topk_weights.shape != (m, top_k) or out.shape != (m, h):
+        raise ValueError(f"shape mismatch: x {tuple(x.shape)}, w13 {tuple(w13.shape)}, w2 {tuple(w2.shape)}, "
+                         f"topk_ids {tuple(topk_ids.shape)}, out {tuple(out.shape)}")
+    rows = _sf_rows(h, ue)
+    if sfx.dim() != 2 or sfx.shape[0] != rows or sfx.shape[1] < m or sf13.shape != (e, 2 * i // 128, rows) \
+            or sf2.shape != (e, h // 128, _sf_rows(i, ue)):
+        raise ValueError("scale shape mismatch")
+    ws, wsp, wsb = _scratch(workspace, lib.dg_get_moe_workspace_size(m, top_k, i), out.device)
+    fn = lib.dg_fp8_moe_few_tokens_ue8m0 if ue else lib.dg_fp8_moe_few_tokens
+    st = fn(x.data_ptr(), _ld(x, 0, 16), sfx.data_ptr(), _ld(sfx, 0, 4), w13.data_ptr(), sf13.data_ptr(),
+            w2.data_ptr(), sf2.data_ptr(), topk_ids.data_ptr(), topk_weights.data_ptr(), out.data_ptr(),
+            _ld(out, 0, 8), m, top_k, e, h, i, wsp, wsb, _stream(out))
+    _check(st)
+    return out
+
+
+class _Tensor(ctypes.Structure):
+    """dg_tensor of the C ABI."""
+    _fields_ = [("data", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int)]
+
+
+class TensorList:
+    """The descriptors of a list of contiguous BF16 / FP32 tensors on one GPU, made once and kept
+    as long as the tensors themselves (it holds references to them)."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        self.device = self.tensors[0].device if self.tensors else None
+        self.table = (_Tensor * max(1, len(self.tensors)))()
+        for d, t in zip(self.table, self.tensors):
+            if t.dtype not in _DTYPES or not t.is_cuda:
+                raise TypeError("tensors must be bfloat16 or float32 GPU tensors")
+            if t.device != self.device or not t.is_contiguous():
+                raise ValueError("tensors must be contiguous and on one device")
+            d.data, d.numel, d.dtype = t.data_ptr(), t.numel(), _DTYPES[t.dtype]
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def tensor_list(tensors) -> TensorList:
+    """A ``TensorList`` for ``clip_grad_norm``."""
+    return TensorList(tensors)
+
+
+def alloc_clip_workspace(device=None) -> torch.Tensor:
+    """A workspace for ``clip_grad_norm`` (any contents)."""
+    size = int(load_library().dg_get_clip_workspace_size())
+    return torch.empty(size, dtype=torch.uint8, device=device if device is not None else torch.cuda.current_device())
+
+
+def clip_grad_norm(grads, max_norm: float, norm: torch.Tensor, out=None, workspace: torch.Tensor | None = None):
+    """norm[0] = sqrt(sum of all squares) and out = grads * min(1, max_norm / (norm + 1e-6)); without
+    ``out`` in place.  grads and out: lists of tensors, or a ``TensorList`` kept between calls."""
+    lib = load_library()
+    grads = grads if isinstance(grads, TensorList) else TensorList(grads)
+    if norm.dtype != torch.float32 or not norm.is_cuda or norm.numel() != 1:
+        raise TypeError("norm must be a float32 GPU tensor with one element")
+    if len(grads) and grads.device != norm.device:
+        raise ValueError("grads must be on norm's device")
+    if out is not None:
+        out = out if isinstance(out, TensorList) else TensorList(out)
+        if len(out) != len(grads) or (len(out) and out.device != norm.device):
+            raise ValueError("out must have as many tensors as grads, on norm's device")
+    ws, wsp, wsb = _scratch(workspace, lib.dg_get_clip_workspace_size(), norm.device)
+    st = lib.dg_clip_grad_norm(grads.table, out.table if out is not None else None, len(grads), max_norm,
+                               norm.data_ptr(), wsp, wsb, _stream(norm))
+    _check(st)
+    return norm
 
 
 def transform_sf_into_required_layout(sf: torch.Tensor, ue8m0: bool = False) -> torch.Tensor:

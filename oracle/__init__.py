@@ -20,6 +20,9 @@ What it computes, written out plainly in FP64 with numpy:
 * the weighted-ReLU MQA logits of the indexer (``mqa.py``);
 * the scale-factor layout transform: per-row scales to the transposed,
   aligned FP32 form or the packed UE8M0 form (``layout.py``);
+* RMS norm with the residual's addition and its gradient (``norm.py``), the
+  gated expert layer (``moe.py``), global gradient norm and clipping
+  (``clip.py``);
 * the acceptance check (``check.py``).
 
 Sources, by page title and section:
@@ -67,4 +70,7 @@ from .kgrouped import k_offsets, ref_k_grouped  # noqa: F401
 from .quant import e4m3_encode_rne, quant_per_token, quant_per_block  # noqa: F401
 from .mqa import ref_mqa_logits  # noqa: F401
 from .layout import transform_sf  # noqa: F401
+from .norm import ref_add_rms_norm, ref_rms_norm_backward  # noqa: F401
+from .moe import ref_moe  # noqa: F401
+from .clip import ref_clip  # noqa: F401
 from .check import tolerance_report, assert_close, TOL_REL, TOL_RMS, TOL_COS  # noqa: F401

@@ -1,0 +1,167 @@
+"""GPU parity of the global gradient norm and clipping against the oracle
+(``oracle/clip.py``).  The squares are summed in FP64 and the norm is rounded
+once to FP32 (2^-24); the factor takes two more FP32 roundings and each product
+one: 2^-22 relative for the norm, 2^-21 for FP32 results, half a BF16 ulp (2^-8 of
+the value) more for BF16 ones."""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():  # pragma: no cover - GPU only
+    import moe_grouped_gemm_tiles_amd as dg
+    from tests._gpu_harness import note, to_dev
+
+DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
+
+
+def _grads(sizes, dtypes, seed, scale=1.0):
+    rng = np.random.default_rng(seed)
+    return [to_dev((scale * rng.standard_normal(n)).astype(np.float32)).to(DT[d]) for n, d in zip(sizes, dtypes)]
+
+
+def _check(grads, max_norm, norm, out, what=""):
+    want, scaled = oracle.ref_clip([g.double().cpu().numpy() for g in grads], max_norm)
+    assert abs(float(norm) - want) <= 2.0 ** -22 * want, f"{what}: norm {float(norm)} {want}"
+    for i, (o, s) in enumerate(zip(out, scaled)):
+        tol = 2.0 ** -21 if o.dtype == torch.float32 else 2.0 ** -8 + 2.0 ** -20
+        assert (np.abs(o.double().cpu().numpy() - s) <= tol * np.abs(s) + 1e-38).all(), f"{what}: tensor {i}"
+
+
+def _norm():
+    return torch.full((1,), -1.0, device="cuda:0")
+
+
+SIZES = [
+    [1], [7], [8], [8191, 8192, 8193], [0, 5, 0, 0, 3, 0], [100000, 1, 17, 65536 * 4 + 3],
+    [33] * 127, [40] * 128, [9] * 300, [3_000_001],
+]
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16", "mixed"])
+@pytest.mark.parametrize("sizes", SIZES, ids=lambda s: f"{len(s)}x{max(s)}")
+def test_clip_sizes(sizes, kind):
+    dtypes = [kind if kind != "mixed" else ("bf16", "fp32")[i % 2] for i in range(len(sizes))]
+    grads = _grads(sizes, dtypes, 700 + len(sizes))
+    out = [torch.full_like(g, float("nan")) for g in grads]
+    norm = _norm()
+    dg.clip_grad_norm(grads, 0.5, norm, out=out)
+    _check(grads, 0.5, norm, out, "out of place")
+    mine = [g.clone() for g in grads]
+    dg.clip_grad_norm(mine, 0.5, norm)
+    _check(grads, 0.5, norm, mine, "in place")
+    for a, b in zip(mine, out):
+        assert torch.equal(a, b)
+
+
+def test_clip_not_needed():
+    """A norm below the limit: the same bits, also out of place."""
+    grads = _grads([1000, 3], ["fp32", "bf16"], 710, scale=1e-3)
+    out = [torch.zeros_like(g) for g in grads]
+    norm = _norm()
+    dg.clip_grad_norm(grads, 100.0, norm, out=out)
+    _check(grads, 100.0, norm, out)
+    for g, o in zip(grads, out):
+        assert torch.equal(g, o)
+    mine = [g.clone() for g in grads]
+    dg.clip_grad_norm(mine, math.inf, norm)
+    assert all(torch.equal(a, b) for a, b in zip(mine, grads))
+
+
+@pytest.mark.parametrize("shift_in", range(4))
+@pytest.mark.parametrize("shift_out", [0, 1, 4])
+def test_clip_unaligned_tensors(shift_in, shift_out):
+    """Tensors that start anywhere: views into one flat buffer, the neighbours untouched."""
+    for dtype in ("fp32", "bf16"):
+        flat = _grads([20000], [dtype], 720 + shift_in)[0]
+        dst = torch.full_like(flat, 7.0)
+        grads = [flat[shift_in:shift_in + 9001], flat[9100 + shift_in:9103 + shift_in]]
+        out = [dst[shift_out:shift_out + 9001], dst[9200 + shift_out:9203 + shift_out]]
+        norm = _norm()
+        dg.clip_grad_norm(grads, 1.0, norm, out=out)
+        _check(grads, 1.0, norm, out, f"{dtype} {shift_in} {shift_out}")
+        kept = torch.ones(20000, dtype=torch.bool, device="cuda:0")
+        kept[shift_out:shift_out + 9001] = False
+        kept[9200 + shift_out:9203 + shift_out] = False
+        assert (dst[kept] == 7.0).all()
+
+
+def test_clip_large_and_small_values():
+    """Squares past FP32's range, and below it: the FP64 sum holds them."""
+    for scale in (1e25, 1e-30):
+        grads = _grads([5000, 77], ["fp32", "fp32"], 730, scale=scale)
+        out = [torch.empty_like(g) for g in grads]
+        norm = _norm()
+        dg.clip_grad_norm(grads, 1.0, norm, out=out)
+        _check(grads, 1.0, norm, out, f"scale {scale}")
+
+
+def test_clip_norm_not_finite():
+    grads = _grads([100, 100], ["fp32", "fp32"], 740)
+    grads[1][3] = math.inf
+    out = [torch.empty_like(g) for g in grads]
+    norm = _norm()
+    dg.clip_grad_norm(grads, 1.0, norm, out=out)
+    assert math.isinf(float(norm)) and (out[0] == 0).all() and math.isnan(float(out[1][3]))
+    grads[1][3] = math.nan
+    dg.clip_grad_norm(grads, 1.0, norm, out=out)
+    assert math.isnan(float(norm)) and torch.isnan(out[0]).all()
+    kept = [g.clone() for g in grads]
+    dg.clip_grad_norm(grads, math.inf, norm)  # only measured
+    assert math.isnan(float(norm)) and torch.equal(grads[0], kept[0])
+
+
+def test_clip_no_tensors_and_all_zero():
+    norm = _norm()
+    dg.clip_grad_norm([], 1.0, norm)
+    assert float(norm) == 0.0
+    z = [torch.zeros(5, device="cuda:0")]
+    dg.clip_grad_norm(z, 0.0, norm)
+    assert float(norm) == 0.0 and (z[0] == 0).all()
+
+
+def test_clip_repeatable_on_another_stream_and_in_a_graph():
+    grads = _grads([50000, 3, 70001], ["fp32", "bf16", "bf16"], 750)
+    out = [torch.empty_like(g) for g in grads]
+    ws, norm = dg.alloc_clip_workspace(), _norm()
+    lists = dg.tensor_list(grads), dg.tensor_list(out)
+    dg.clip_grad_norm(lists[0], 0.7, norm, out=lists[1], workspace=ws)
+    want = [o.clone() for o in out] + [norm.clone()]
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        dg.clip_grad_norm(lists[0], 0.7, norm, out=lists[1], workspace=ws)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out + [norm], want))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        dg.clip_grad_norm(lists[0], 0.7, norm, out=lists[1], workspace=ws)
+    for _ in range(4):
+        for o in out:
+            o.zero_()
+        ws.fill_(0xFF)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out + [norm], want))
+        dg.clip_grad_norm([o.clone() for o in out], 0.1, torch.empty(1, device="cuda:0"))
+
+
+def test_clip_large():
+    """256 MiB in three tensors (FP64 reference on the GPU)."""
+    gen = torch.Generator(device="cuda:0").manual_seed(760)
+    grads = [torch.randn(n, device="cuda:0", generator=gen) for n in (40_000_001, 25_000_000, 2_000_000)]
+    out = [torch.empty_like(g) for g in grads]
+    norm = _norm()
+    dg.clip_grad_norm(grads, 1.0, norm, out=out)
+    want = math.sqrt(sum(float(g.double().square().sum()) for g in grads))
+    assert abs(float(norm) - want) <= 2.0 ** -22 * want
+    for g, o in zip(grads, out):
+        ref = g.double() / (want + 1e-6)
+        assert bool(((o.double() - ref).abs() <= 2.0 ** -21 * ref.abs()).all())
+    note(f"norm {float(norm)}")

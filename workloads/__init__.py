@@ -25,6 +25,7 @@ from .gen import (  # noqa: F401
     gen_k_grouped,
     gen_quant_input,
     gen_mqa,
+    gen_moe,
     DENSE_SWEEP,
     workload,
     WORKLOAD_NAMES,

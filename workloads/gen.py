@@ -318,6 +318,48 @@ def gen_mqa(s: int, s_kv: int, h: int, d: int, seed: int, ranges: str = "causal"
     return dict(kind="mqa", s=s, s_kv=s_kv, h=h, d=d, q=q, kv=kv, sf=sf, w=w, ks=ks, ke=ke)
 
 
+def gen_moe(m: int, experts: int, top_k: int, hidden: int, inter: int, seed: int, scale_fmt: str = "fp32",
+            routed: int | None = None, poison: bool = False):
+    """Inputs of the few-token expert layer.
+
+    Draw order: x, W13 and W2 of each expert, routing.  x ~ N(0,1) quantised per
+    (row, 128), weights ~ N(0, 1/K) per 128x128 block; each token goes to top_k
+    distinct experts of ``routed`` (default ``experts``), ids past the local
+    ones becoming -1 (and some of them other out-of-range values); weights
+    softmax-normalised.  ``poison``: experts without a token get NaN codes and
+    NaN scales, slots without an expert here a NaN weight.
+    """
+    rng = np.random.default_rng(seed)
+    pow2 = scale_fmt == "ue8m0"
+    routed = experts if routed is None else routed
+    x, sx = quantize_per_row_block(_draw(rng, (m, hidden)), pow2)
+    sfx = sf_to_mn_major(sx)
+    w13 = np.empty((experts, 2 * inter, hidden), np.uint8)
+    w2 = np.empty((experts, hidden, inter), np.uint8)
+    sf13 = np.empty((experts, 2 * inter // SF_BLOCK, hidden // SF_BLOCK), np.float32)
+    sf2 = np.empty((experts, hidden // SF_BLOCK, inter // SF_BLOCK), np.float32)
+    for e in range(experts):
+        w13[e], sf13[e] = quantize_per_block(_draw(rng, (2 * inter, hidden)) / np.float32(np.sqrt(hidden)), pow2)
+        w2[e], sf2[e] = quantize_per_block(_draw(rng, (hidden, inter)) / np.float32(np.sqrt(inter)), pow2)
+    score = rng.random((m, routed))
+    ids = np.argsort(-score, axis=1)[:, :top_k].astype(np.int32)
+    far = np.array([-1, experts, 2 ** 31 - 1, -2 ** 31], np.int32)
+    ids = np.where(ids < experts, ids, far[rng.integers(0, 4, ids.shape)])
+    w = np.exp(_draw(rng, (m, top_k)))
+    w = (w / w.sum(1, keepdims=True)).astype(np.float32)
+    if poison:
+        idle = np.setdiff1d(np.arange(experts), ids)
+        w13[idle], w2[idle] = 0x7F, 0xFF
+        sf13[idle] = sf2[idle] = np.nan if not pow2 else 1.0
+        w[(ids < 0) | (ids >= experts)] = np.nan
+    if pow2:
+        cols = np.zeros((hidden // SF_BLOCK, sfx.shape[1]), np.float32) + 1.0
+        cols[:, :m] = sx.T
+        sfx, sf13, sf2 = pack_ue8m0(cols, 0), pack_ue8m0(sf13, 2), pack_ue8m0(sf2, 2)
+    return dict(kind="moe", m=m, experts=experts, top_k=top_k, hidden=hidden, inter=inter, scale_fmt=scale_fmt, x=x,
+                sfx=sfx, w13=w13, sf13=sf13, w2=w2, sf2=sf2, ids=ids, weights=w)
+
+
 # (N, K) pairs and M values of the dense sweep; case i = m_index * 5 + nk_index, seed 100 + i.
 DENSE_SWEEP_NK = [(2112, 7168), (24576, 1536), (7168, 16384), (4096, 7168), (7168, 2048)]
 DENSE_SWEEP_M = [64, 128, 4096]
