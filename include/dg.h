@@ -72,7 +72,7 @@ typedef enum {
   DG_ERROR_INVALID_VALUE = 1,  /* null/misaligned pointer, bad stride, negative size, bad enum */
   DG_ERROR_NOT_SUPPORTED = 2,  /* valid but unsupported: K % 128 != 0, contiguous M % 128 != 0 */
   DG_ERROR_LAUNCH_FAILED = 3,  /* a HIP call failed; hipGetLastError() text via dg_last_hip_error */
-  DG_ERROR_WORKSPACE = 4,      /* split-K workspace NULL, misaligned or smaller than dg_get_workspace_size */
+  DG_ERROR_WORKSPACE = 4,      /* workspace NULL, misaligned or smaller than the entry point's size function says */
   DG_ERROR_SCRATCH_LIMIT = 5   /* dg_fp8_gemm_nt_noalloc: the call needs more than the library's fixed scratch */
 } dg_status;
 

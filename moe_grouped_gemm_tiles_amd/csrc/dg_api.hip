@@ -715,8 +715,8 @@ const char* dg_status_string(dg_status s) {
       return "DG_ERROR_SCRATCH_LIMIT: the call needs more split-K scratch than the allocation-free entry point "
              "holds (16 MiB of partial tiles); use dg_fp8_gemm_nt with a workspace";
     case DG_ERROR_WORKSPACE:
-      return "DG_ERROR_WORKSPACE: the split-K workspace is missing, not 256-byte aligned or smaller than "
-             "dg_get_workspace_size(m, n, k)";
+      return "DG_ERROR_WORKSPACE: the workspace is missing, not 256-byte aligned or smaller than the entry point's "
+             "size function says (dense GEMMs: dg_get_workspace_size(m, n, k))";
   }
   return "DG_UNKNOWN_STATUS";
 }

@@ -9,8 +9,28 @@
 // Backward, with xhat = s * rstd and g = dy * w:
 //     dx = rstd * (g - xhat * mean(g * xhat)) + dresidual,   dw = sum over rows of dy * xhat
 // (the cast passes its gradient through unchanged).
+//
+// Both are bound by HBM: every operand is read once and every result written
+// once, a row staying in registers from its loads to its stores.  What that
+// takes on this chip (a plain device copy reaches 5.0 to 6.1 TB/s):
+//   * the next row's loads are in flight while a row is reduced, cast and stored,
+//     and nothing in between waits for them: no branch stands around a memory
+//     access (buffer descriptors drop what is out of range), and lanes exchange
+//     values on the VALU (DPP, permlane swaps), not through LDS;
+//   * accesses past the L2s' capacity are streaming: with them 33280 x 7168 BF16
+//     takes 363 us, without 448 us (before the prefetch);
+//   * workgroups run through memory together.  With one or two rows per workgroup
+//     the forward takes 276 us, with 4 297 us, with 16 336 us: the more regions are
+//     being read at once, the less HBM delivers.  The backward, whose workgroups
+//     persist to keep their column sums, is best with at most one per CU and a
+//     few MiB of rows in flight: 208 workgroups 316 us, 256 331 us, 512 354 us,
+//     1024 357 us;
+//   * FP32 rows are split so that every load instruction reads 256 adjacent bytes per
+//     16 lanes: 29000 x 4096 backward 343 -> 306 us, 4099 x 4096 forward 34 -> 29.5 us.
+// 33280 x 7168 BF16 now: forward 276 us, 6.07 TB/s; backward 316 us, 6.05 TB/s.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "dg.h"
@@ -23,47 +43,226 @@ namespace norm {
 
 using namespace dg::cast;
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
 constexpr int kMaxThreads = 512;
 constexpr int kMaxChunks = 4;                        // 8-value chunks a thread holds
 constexpr int kMaxK = 8 * kMaxChunks * kMaxThreads;  // 16384
+constexpr uint32_t kNowhere = 0xffffffffu;           // a buffer offset past every operand: the access is dropped
 
-// BF16 bits of a float, round to nearest even (NaN stays NaN), two to a word.
-__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  const bf16x2 v = {(__bf16)a, (__bf16)b};
-  return __builtin_bit_cast(uint32_t, v);
+// Rows go through buffer descriptors of exactly their length: lanes past the
+// row's end load zeros and store nothing, and an operand that is not there is a
+// descriptor of length 0.  So the row loop has no branch around a memory access,
+// and the compiler can count what is in flight: with branches it has to wait for
+// everything before each use.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
 }
 
+// Cache policy of the row accesses: 2 marks them as streaming (not kept in the
+// caches), 0 does not.
+template <bool NT>
+constexpr int kPolicy = NT ? 2 : 0;
+
+// Where a thread's eight values of chunk ch lie in a row, in elements: BF16 rows
+// give it eight adjacent ones (16 bytes), FP32 rows four in each half of the
+// 128-value block, so that 16 lanes always read 256 adjacent bytes.
 template <bool BF16>
-__device__ __forceinline__ void store8(void* p, const float (&v)[8]) {
+__device__ __forceinline__ uint32_t place(int ch, int half) {
+  return BF16 ? ch * 8 + half * 4 : (ch >> 4) * 128 + half * 64 + (ch & 15) * 4;
+}
+
+// Raw bits of a thread's chunks of one row.
+template <bool BF16, int C>
+struct Raw {
+  u32x4 d[C][BF16 ? 1 : 2];
+};
+
+template <bool BF16, bool NT, int C>
+__device__ __forceinline__ void load_row(__amdgpu_buffer_rsrc_t r, int tid, int nt, Raw<BF16, C>& o) {
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int h = 0; h < (BF16 ? 1 : 2); ++h)
+      o.d[c][h] = __builtin_amdgcn_raw_buffer_load_b128(r, place<BF16>(c * nt + tid, h) * (BF16 ? 2 : 4), 0, kPolicy<NT>);
+}
+
+template <bool BF16, int C>
+__device__ __forceinline__ void unpack(const Raw<BF16, C>& o, int c, float (&v)[8]) {
   if constexpr (BF16) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]),
-                                              bf16_pair(v[6], v[7]));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(o.d[c][0][i] << 16);
+      v[2 * i + 1] = __uint_as_float(o.d[c][0][i] & 0xffff0000u);
+    }
   } else {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    *(reinterpret_cast<float4*>(p) + 1) = make_float4(v[4], v[5], v[6], v[7]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(o.d[c][i >> 2][i & 3]);
   }
 }
 
-// Eight values of the norm's weight (chunk ch of the row).
-__device__ __forceinline__ void load_weight(const uint8_t* w, int bf16, int ch, float (&v)[8]) {
-  if (bf16) load8<true>(w + (int64_t)ch * 16, v);
-  else load8<false>(w + (int64_t)ch * 32, v);
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  const bf16x2 v = {(__bf16)a, (__bf16)b};  // round to nearest even
+  return __builtin_bit_cast(uint32_t, v);
+}
+
+// Eight values of chunk ch, laid out as rows of type BF16, to FP32 memory.
+template <bool BF16, bool NT>
+__device__ __forceinline__ void store8_fp32(__amdgpu_buffer_rsrc_t r, int ch, const float (&v)[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const u32x4 o = {__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]), __float_as_uint(v[4 * h + 2]),
+                     __float_as_uint(v[4 * h + 3])};
+    __builtin_amdgcn_raw_buffer_store_b128(o, r, place<BF16>(ch, h) * 4, 0, kPolicy<NT>);
+  }
+}
+
+// Eight values of chunk ch to a row, rounded to the row's type.
+template <bool BF16, bool NT>
+__device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t r, int ch, const float (&v)[8]) {
+  if constexpr (BF16) {
+    const u32x4 o = {bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])};
+    __builtin_amdgcn_raw_buffer_store_b128(o, r, ch * 16, 0, kPolicy<NT>);
+  } else {
+    store8_fp32<false, NT>(r, ch, v);
+  }
+}
+
+// A thread's chunks of the norm's weight (BF16 or FP32), as FP32, laid out as rows of type BF16.
+template <bool BF16, int C>
+__device__ __forceinline__ void load_weight(const uint8_t* w, int bf16, int k, int tid, int nt, float (&v)[C][8]) {
+  const __amdgpu_buffer_rsrc_t r = make_rsrc(w, (uint32_t)k * (bf16 ? 2 : 4));
+  if (bf16) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const u32x2 o = __builtin_amdgcn_raw_buffer_load_b64(r, place<BF16>(c * nt + tid, h) * 2, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          v[c][4 * h + 2 * i] = __uint_as_float(o[i] << 16);
+          v[c][4 * h + 2 * i + 1] = __uint_as_float(o[i] & 0xffff0000u);
+        }
+      }
+  } else {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const u32x4 o = __builtin_amdgcn_raw_buffer_load_b128(r, place<BF16>(c * nt + tid, h) * 4, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[c][4 * h + i] = __uint_as_float(o[i]);
+      }
+  }
+}
+
+// Lane permutations on the VALU: 0xB1 and 0x4E swap neighbours and pairs in
+// each four lanes, 0x141 and 0x140 mirror eight and sixteen.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __uint_as_float(dpp<CTRL>(__float_as_uint(v)));
+}
+
+// Largest of 16 adjacent lanes.
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+  v = max(v, dpp<0xB1>(v));
+  v = max(v, dpp<0x4E>(v));
+  v = max(v, dpp<0x141>(v));
+  return max(v, dpp<0x140>(v));
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+  v += dpp<0xB1>(v);
+  v += dpp<0x4E>(v);
+  v += dpp<0x141>(v);
+  v += dpp<0x140>(v);
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
 // Sum over the workgroup, the same on every thread and in a fixed order.
-// `slot` holds one float per wave; calls in turn use different slots, so one
-// barrier per call is enough.
+// `slot` holds one float per wave (zeros past the last); calls in turn use
+// different slots, so one barrier per call is enough.
+constexpr int kSlots = kMaxThreads / 64;
 __device__ __forceinline__ float block_sum(float v, float* slot) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
-  const int waves = blockDim.x >> 6;
-  if (waves == 1) return v;
+  v = wave_sum(v);
+  if (blockDim.x == 64) return v;
   if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
   __syncthreads();
-  float t = 0.f;
-  for (int i = 0; i < waves; ++i) t += slot[i];
-  return t;
+  float t[kSlots];
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) t[i] = slot[i];
+#pragma unroll
+  for (int d = 1; d < kSlots; d *= 2)
+#pragma unroll
+    for (int i = 0; i < kSlots; i += 2 * d) t[i] += t[i + d];
+  return t[0];
+}
+
+// Codes of eight values of a block whose amax has the bits `amax` (compared as
+// an unsigned integer, so that a NaN is the largest).  The common case takes
+// amax / 448 and x / s with the steps of the correctly rounded division
+// (dg_cast.hpp), written so that a zero keeps its sign and without a clamp:
+// |x / s| <= 448 * (1 + 2^-23), which rounds to 448.  Zero blocks and scales
+// outside the range of those steps take the general form, and a block with an
+// Inf or NaN keeps it: its scale is not finite, and neither are the codes of
+// such elements.
+__device__ __forceinline__ float quotient(float x, float s, float y) {
+  const float q0 = x * y;
+  const float q1 = __builtin_fmaf(-__builtin_fmaf(s, q0, -x), y, q0);
+  return __builtin_fmaf(-__builtin_fmaf(s, q1, -x), y, q1);
+}
+
+template <bool UE8M0>
+__device__ __forceinline__ u32x2 codes8(const float (&v)[8], uint32_t amax, float& s, uint32_t& byte) {
+  const float a = __uint_as_float(amax);
+  const float t = quotient(a, kE4M3Max, 1.0f / kE4M3Max);
+  if (plain_div_range(t)) {
+    float y[8];
+    if constexpr (UE8M0) {
+      byte = (__float_as_uint(t) + 0x7fffffu) >> 23;  // the exponent, one more unless t is a power of two
+      s = __uint_as_float(byte << 23);
+      const float inv = __uint_as_float((254 - byte) << 23);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = v[i] * inv;
+    } else {
+      byte = 0;
+      s = t;
+      const float r = refined_recip(s);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = quotient(v[i], s, r);
+    }
+    int lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+    int hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[4], y[5], 0, false);
+    lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], lo, true);
+    hi = __builtin_amdgcn_cvt_pk_fp8_f32(y[6], y[7], hi, true);
+    return u32x2{(uint32_t)lo, (uint32_t)hi};
+  }
+  if (amax >= 0x7f800000u) {
+    byte = 255;
+    s = amax > 0x7f800000u ? __builtin_nanf("") : __builtin_inff();
+    u32x2 c = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i >> 2] |= (fabsf(v[i]) < __builtin_inff() ? 0u : 0x7fu) << (8 * (i & 3));
+    return c;
+  }
+  if constexpr (UE8M0) {
+    byte = ue8m0_byte(a);
+    s = ue8m0_value(byte);
+  } else {
+    byte = 0;
+    s = fp32_scale(a);
+  }
+  const uint2 c = quant8<UE8M0>(v, s);
+  return u32x2{c.x, c.y};
 }
 
 struct FwdParams {
@@ -72,115 +271,105 @@ struct FwdParams {
   uint8_t* res_out;
   const uint8_t* w;
   uint8_t* q;
-  void* sf;
+  uint8_t* sf;
   uint8_t* y;
   float* rstd;
-  int64_t ldx, ldr, ldro, ldq, ld_sf, ldy;  // bytes, except ld_sf (words)
+  int64_t ldx, ldr, ldro, ldq, ld_sf, ldy;  // bytes
   float eps;
   int m, k, rows_per_wg;
   int w_bf16;
 };
 
-// Codes of eight values of a block whose amax bits are `amax` (as an unsigned
-// integer, so that a NaN is the largest).  A block with an Inf or NaN keeps it:
-// its scale is not finite, and neither are its NaN elements' codes.
-template <bool UE8M0>
-__device__ __forceinline__ uint2 codes8(const float (&v)[8], uint32_t amax, float& s, uint32_t& byte) {
-  if (amax >= 0x7f800000u) {
-    byte = 255;
-    s = amax > 0x7f800000u ? __builtin_nanf("") : __builtin_inff();
-    uint2 c = make_uint2(0, 0);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t nan = !(fabsf(v[i]) < __builtin_inff());
-      (i < 4 ? c.x : c.y) |= (nan ? 0x7fu : 0u) << (8 * (i & 3));
-    }
-    return c;
-  }
-  const float a = __uint_as_float(amax);
-  if constexpr (UE8M0) {
-    byte = ue8m0_byte(a);
-    s = ue8m0_value(byte);
-  } else {
-    byte = 0;
-    s = fp32_scale(a);
-  }
-  return quant8<UE8M0>(v, s);
-}
-
-// One workgroup takes rows_per_wg rows in turn; a thread holds chunks
-// c * blockDim + tid of eight values of a row, so 16 adjacent lanes hold one
-// 128-value block and a wave four adjacent ones (one packed UE8M0 word).
-template <bool BF16, bool UE8M0, int C>
+// One workgroup takes rows_per_wg rows in turn, the next row's operands being
+// loaded while a row is worked on; a thread holds chunks c * blockDim + tid of
+// eight values of a row, so 16 adjacent lanes hold one 128-value block and a
+// wave four adjacent ones (one packed UE8M0 word).
+template <bool BF16, bool UE8M0, bool NT, int C>
 __global__ void __launch_bounds__(kMaxThreads) fwd_kernel(const FwdParams p) {
-  __shared__ float s_sum[2][2][kMaxThreads / 64];  // [scaled again][row parity]
+  __shared__ float s_sum[2][2][kSlots];  // [scaled again][row parity]
   constexpr int ES = BF16 ? 2 : 4;
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 63;
   const int chunks = p.k >> 3;
+  const uint32_t bytes = (uint32_t)p.k * ES, res_bytes = p.res != nullptr ? bytes : 0;
   const int row0 = blockIdx.x * p.rows_per_wg;
   const int row1 = min(row0 + p.rows_per_wg, p.m);
+  if (tid < 4 * kSlots) (&s_sum[0][0][0])[tid] = 0.f;
+  float w[C][8];
+  load_weight<BF16, C>(p.w, p.w_bf16, p.k, tid, nt, w);
+  Raw<BF16, C> x, r;
+  load_row<BF16, NT, C>(make_rsrc(p.x + row0 * p.ldx, bytes), tid, nt, x);
+  load_row<BF16, NT, C>(make_rsrc(p.res + row0 * p.ldr, res_bytes), tid, nt, r);
+  const float inv_k = 1.0f / (float)p.k;
+  __syncthreads();
   for (int row = row0; row < row1; ++row) {
+    const __amdgpu_buffer_rsrc_t ro = make_rsrc(p.res_out + row * p.ldro, res_bytes);
     float v[C][8];
     float ss = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int ch = c * nt + tid;
-      if (ch >= chunks) continue;
-      load8<BF16>(p.x + row * p.ldx + (int64_t)ch * 8 * ES, v[c]);
-      if (p.res != nullptr) {
-        float r[8];
-        load8<BF16>(p.res + row * p.ldr + (int64_t)ch * 8 * ES, r);
+      float t[8];
+      unpack<BF16, C>(x, c, v[c]);
+      unpack<BF16, C>(r, c, t);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[c][i] += r[i];
-        store8<BF16>(p.res_out + row * p.ldro + (int64_t)ch * 8 * ES, v[c]);
+      for (int i = 0; i < 8; ++i) {
+        v[c][i] += t[i];
+        ss = __builtin_fmaf(v[c][i], v[c][i], ss);
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss += v[c][i] * v[c][i];
     }
+    if (row + 1 < row1) {
+      load_row<BF16, NT, C>(make_rsrc(p.x + (row + 1) * p.ldx, bytes), tid, nt, x);
+      load_row<BF16, NT, C>(make_rsrc(p.res + (row + 1) * p.ldr, res_bytes), tid, nt, r);
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) store8<BF16, NT>(ro, c * nt + tid, v[c]);
     ss = block_sum(ss, s_sum[0][row & 1]);
-    float rstd = 1.0f / sqrtf(ss / (float)p.k + p.eps);
+    float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, inv_k, p.eps));
     if (!(ss >= 0x1p-100f && ss < __builtin_inff())) {
       // squares past FP32's range on either side (the same branch on every thread): again, scaled
-      const float c = ss < 1.0f ? 0x1p60f : 0x1p-64f;
+      const float f = ss < 1.0f ? 0x1p60f : 0x1p-64f;
       ss = 0.f;
 #pragma unroll
-      for (int j = 0; j < C; ++j) {
-        if (j * nt + tid >= chunks) continue;
+      for (int c = 0; c < C; ++c)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss += (v[j][i] * c) * (v[j][i] * c);
-      }
+        for (int i = 0; i < 8; ++i) ss += (v[c][i] * f) * (v[c][i] * f);
       ss = block_sum(ss, s_sum[1][row & 1]);
-      rstd = (float)(1.0 / sqrt((double)ss / ((double)c * (double)c) / p.k + (double)p.eps));
+      rstd = (float)(1.0 / sqrt((double)ss / ((double)f * (double)f) / p.k + (double)p.eps));
     }
-    if (p.rstd != nullptr && tid == 0) p.rstd[row] = rstd;
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(rstd), make_rsrc(p.rstd + row, p.rstd != nullptr ? 4 : 0),
+                                          tid == 0 ? 0 : kNowhere, 0, 0);
+    const __amdgpu_buffer_rsrc_t ry = make_rsrc(p.y + row * p.ldy, p.y != nullptr ? bytes : 0);
+    const __amdgpu_buffer_rsrc_t rq = make_rsrc(p.q + row * p.ldq, (uint32_t)p.k);
+    const __amdgpu_buffer_rsrc_t rs = make_rsrc(p.sf + (int64_t)row * 4, 0xfffffffeu);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int ch = c * nt + tid;
-      if (c * nt + (tid & ~63) >= chunks) continue;  // a wave past the row's end; its last blocks may be too
       uint32_t amax = 0;
-      if (ch < chunks) {
-        float w[8];
-        load_weight(p.w, p.w_bf16, ch, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          v[c][i] = v[c][i] * rstd * w[i];
-          amax = max(amax, __float_as_uint(v[c][i]) & 0x7fffffffu);
-        }
-        if (p.y != nullptr) store8<BF16>(p.y + row * p.ldy + (int64_t)ch * 8 * ES, v[c]);
+      for (int i = 0; i < 8; ++i) {
+        v[c][i] = v[c][i] * rstd * w[c][i];
+        amax = max(amax, __float_as_uint(v[c][i]) & 0x7fffffffu);
       }
-#pragma unroll
-      for (int off = 8; off >= 1; off >>= 1) amax = max(amax, (uint32_t)__shfl_xor((int)amax, off, 16));
-      float s = 1.0f;
-      uint32_t byte = 127;
-      if (ch < chunks) {
-        *reinterpret_cast<uint2*>(p.q + row * p.ldq + (int64_t)ch * 8) = codes8<UE8M0>(v[c], amax, s, byte);
+      store8<BF16, NT>(ry, ch, v[c]);
+      amax = max16(amax);
+      float s;
+      uint32_t byte;
+      const u32x2 q = codes8<UE8M0>(v[c], amax, s, byte);
+      if constexpr (BF16) {
+        __builtin_amdgcn_raw_buffer_store_b64(q, rq, ch * 8, 0, kPolicy<NT>);
+      } else {
+        __builtin_amdgcn_raw_buffer_store_b32(q[0], rq, place<false>(ch, 0), 0, kPolicy<NT>);
+        __builtin_amdgcn_raw_buffer_store_b32(q[1], rq, place<false>(ch, 1), 0, kPolicy<NT>);
       }
       if constexpr (UE8M0) {
-        const uint32_t b1 = __shfl((int)byte, 16), b2 = __shfl((int)byte, 32), b3 = __shfl((int)byte, 48);
-        if (lane == 0)
-          static_cast<uint32_t*>(p.sf)[(int64_t)(ch >> 6) * p.ld_sf + row] = byte | b1 << 8 | b2 << 16 | b3 << 24;
+        byte = ch < chunks ? byte : 127u;
+        const uint32_t word = __builtin_amdgcn_readlane(byte, 0) | __builtin_amdgcn_readlane(byte, 16) << 8 |
+                              __builtin_amdgcn_readlane(byte, 32) << 16 | __builtin_amdgcn_readlane(byte, 48) << 24;
+        __builtin_amdgcn_raw_buffer_store_b32(
+            word, rs, lane == 0 && ch < chunks ? (uint32_t)(ch >> 6) * (uint32_t)p.ld_sf : kNowhere, 0, 0);
       } else {
-        if ((lane & 15) == 0 && ch < chunks) static_cast<float*>(p.sf)[(int64_t)(ch >> 4) * p.ld_sf + row] = s;
+        __builtin_amdgcn_raw_buffer_store_b32(
+            __float_as_uint(s), rs, (lane & 15) == 0 && ch < chunks ? (uint32_t)(ch >> 4) * (uint32_t)p.ld_sf : kNowhere,
+            0, 0);
       }
     }
   }
@@ -199,105 +388,136 @@ struct BwdParams {
   int w_bf16;
 };
 
-// One workgroup takes rows blockIdx, blockIdx + gridDim, ... and keeps its sum
-// of dy * xhat per column in registers; it leaves that as one row of `part`.
-template <bool BF16, int C>
-__global__ void __launch_bounds__(kMaxThreads) bwd_kernel(const BwdParams p) {
-  __shared__ float s_sum[2][kMaxThreads / 64];
+// One workgroup takes rows blockIdx, blockIdx + gridDim, ... (the next row's
+// operands in flight) and keeps its sum of dy * xhat per column in registers;
+// it leaves that as one row of `part`.
+template <bool BF16, bool NT, int C>
+__global__ void __launch_bounds__(kMaxThreads) 
+bwd_kernel(const BwdParams p) {
+  __shared__ float s_sum[2][kSlots];
   constexpr int ES = BF16 ? 2 : 4;
   const int tid = threadIdx.x, nt = blockDim.x;
-  const int chunks = p.k >> 3;
-  float dw[C][8];
+  const uint32_t bytes = (uint32_t)p.k * ES, res_bytes = p.dres != nullptr ? bytes : 0;
+  if (tid < 2 * kSlots) (&s_sum[0][0])[tid] = 0.f;
+  float w[C][8], dw[C][8];
+  load_weight<BF16, C>(p.w, p.w_bf16, p.k, tid, nt, w);
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[c][i] = 0.f;
+  Raw<BF16, C> dy, s, dr;
+  int row = blockIdx.x;
+  float rstd = p.rstd[row];
+  constexpr bool kAhead = BF16 || C < 4;  // (else the next row's operands would not fit in registers)
+  if (kAhead) {
+    load_row<BF16, NT, C>(make_rsrc(p.dy + row * p.lddy, bytes), tid, nt, dy);
+    load_row<BF16, NT, C>(make_rsrc(p.s + row * p.lds, bytes), tid, nt, s);
+    load_row<BF16, NT, C>(make_rsrc(p.dres + row * p.lddres, res_bytes), tid, nt, dr);
+  }
   const float inv_k = 1.0f / (float)p.k;
-  int turn = 0;
-  for (int row = blockIdx.x; row < p.m; row += gridDim.x, turn ^= 1) {
-    const float rstd = p.rstd[row];
-    float g[C][8], xh[C][8];
+  __syncthreads();
+  for (int turn = 0; row < p.m; turn ^= 1) {
+    if (!kAhead) {
+      load_row<BF16, NT, C>(make_rsrc(p.dy + row * p.lddy, bytes), tid, nt, dy);
+      load_row<BF16, NT, C>(make_rsrc(p.s + row * p.lds, bytes), tid, nt, s);
+      load_row<BF16, NT, C>(make_rsrc(p.dres + row * p.lddres, res_bytes), tid, nt, dr);
+    }
+    float g[C][8], xh[C][8], d[C][8];
     float dot = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int ch = c * nt + tid;
-      if (ch >= chunks) continue;
-      load8<BF16>(p.dy + row * p.lddy + (int64_t)ch * 8 * ES, g[c]);
-      load8<BF16>(p.s + row * p.lds + (int64_t)ch * 8 * ES, xh[c]);
-      float w[8];
-      load_weight(p.w, p.w_bf16, ch, w);
+      unpack<BF16, C>(dy, c, g[c]);
+      unpack<BF16, C>(s, c, xh[c]);
+      unpack<BF16, C>(dr, c, d[c]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         xh[c][i] *= rstd;
-        dw[c][i] += g[c][i] * xh[c][i];
-        g[c][i] *= w[i];
-        dot += g[c][i] * xh[c][i];
+        dw[c][i] = __builtin_fmaf(g[c][i], xh[c][i], dw[c][i]);
+        g[c][i] *= w[c][i];
+        dot = __builtin_fmaf(g[c][i], xh[c][i], dot);
+      }
+    }
+    const float r = rstd;
+    const int here = row;
+    row += gridDim.x;
+    if (row < p.m) {
+      rstd = p.rstd[row];
+      if (kAhead) {
+        load_row<BF16, NT, C>(make_rsrc(p.dy + row * p.lddy, bytes), tid, nt, dy);
+        load_row<BF16, NT, C>(make_rsrc(p.s + row * p.lds, bytes), tid, nt, s);
+        load_row<BF16, NT, C>(make_rsrc(p.dres + row * p.lddres, res_bytes), tid, nt, dr);
       }
     }
     dot = block_sum(dot, s_sum[turn]) * inv_k;
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.dx + here * p.lddx, bytes);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int ch = c * nt + tid;
-      if (ch >= chunks) continue;
-      float d[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) d[i] = rstd * (g[c][i] - xh[c][i] * dot);
-      if (p.dres != nullptr) {
-        float r[8];
-        load8<BF16>(p.dres + row * p.lddres + (int64_t)ch * 8 * ES, r);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] += r[i];
-      }
-      store8<BF16>(p.dx + row * p.lddx + (int64_t)ch * 8 * ES, d);
+      for (int i = 0; i < 8; ++i) d[c][i] = __builtin_fmaf(r, __builtin_fmaf(-xh[c][i], dot, g[c][i]), d[c][i]);
+      store8<BF16, NT>(rx, c * nt + tid, d[c]);
     }
   }
+  const __amdgpu_buffer_rsrc_t rp = make_rsrc(p.part + (int64_t)blockIdx.x * p.k, (uint32_t)p.k * 4);
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int ch = c * nt + tid;
-    if (ch < chunks) store8<false>(p.part + (int64_t)blockIdx.x * p.k + (int64_t)ch * 8, dw[c]);
-  }
+  for (int c = 0; c < C; ++c) store8_fp32<BF16, false>(rp, c * nt + tid, dw[c]);
 }
 
 constexpr int kDwCols = 32;  // columns of one workgroup of the column sum
+constexpr int kDwRows = 128;  // rows it takes at a time
 
-// dw[col] (+)= sum over rows of part[row][col]: eight lanes take 32 columns of
-// a row, 32 rows at a time, and the 32 sums of a column are added in order.
-__global__ void __launch_bounds__(256) dw_kernel(const float* part, int rows, int k, float* dw, int accumulate) {
-  __shared__ float t[32][kDwCols];
+// dw[col] (+)= sum over rows of part[row][col]: eight lanes take 32 columns of a
+// row, and the sums of the 128 row classes are added in a fixed order.
+__global__ void __launch_bounds__(kDwRows * 8) dw_kernel(const float* part, int rows, int k, float* dw,
+                                                         int accumulate) {
+  __shared__ float t[kDwRows][kDwCols];
   const int tid = threadIdx.x, r = tid >> 3, c4 = (tid & 7) * 4;
   const int col = blockIdx.x * kDwCols + c4;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = r; i < rows; i += 32) {
+  for (int i = r; i < rows; i += kDwRows) {
     const float4 v = *reinterpret_cast<const float4*>(part + (int64_t)i * k + col);
     a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
   }
   *reinterpret_cast<float4*>(&t[r][c4]) = a;
   __syncthreads();
-  if (tid < kDwCols) {
-    float sum = 0.f;
+  // 32 threads per column, four classes each, then across them
+  const int c = tid >> 5, g = tid & 31;
+  float sum = (t[g][c] + t[g + 32][c]) + (t[g + 64][c] + t[g + 96][c]);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) sum += t[i][tid];
-    float* o = dw + blockIdx.x * kDwCols + tid;
+  for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 32);
+  if (g == 0) {
+    float* o = dw + blockIdx.x * kDwCols + c;
     *o = accumulate ? *o + sum : sum;
   }
 }
 
-// Threads and chunks per thread for rows of k values.
+// Threads and chunks per thread for rows of k values: as many threads as there
+// are chunks, up to 512.
 struct Shape {
   int threads, chunks;
 };
-Shape shape_for(int k, int want_chunks) {
+Shape shape_for(int k) {
   const int n = k / 8;
-  int c = want_chunks;
-  while (c < kMaxChunks && (n + c - 1) / c > kMaxThreads) c *= 2;
-  const int threads = ((n + c - 1) / c + 63) / 64 * 64;
-  return {threads, c};
+  int c = 1;
+  while ((n + c - 1) / c > kMaxThreads) c *= 2;
+  return {((n + c - 1) / c + 63) / 64 * 64, c};
 }
 
-// Workgroups of the backward's row loop: each leaves a row of partial sums.
-int bwd_grid(int m) {
-  constexpr int kMost = 1024;
-  return m < kMost ? m : kMost;
+// Rows one workgroup of the forward takes in turn: one where a row keeps a CU's
+// load queue busy by itself, more for shorter rows (256 columns: 357 us for a
+// million rows with 8, 427 us with 1) and for the longest, whose workgroups fill a CU
+// alone and need the prefetch (14560 x 16384: 298 us with 4, 318 us with 1).
+int fwd_rows(int m, int k) {
+  const int rows = k > 8192 ? 4 : k > 4096 ? 1 : k > 512 ? 2 : 8;
+  return std::max(1, std::min(rows, m / 2048));
+}
+
+// Workgroups of the backward's row loop, each of which leaves a row of partial sums:
+// 208 for rows of 4096 values and more, in proportion for shorter ones (2048 columns,
+// 77000 rows: 206 us with 448, 224 us with 336; 384 columns, 600000 rows: 320 us with
+// 2240, 435 us with 1024), and no more than one for two rows.
+int bwd_grid(int m, int k) {
+  const int most = 208 * std::max(1, 4096 / k);
+  return std::min(most, (m + 1) / 2);
 }
 
 inline bool aligned_to(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -307,22 +527,36 @@ inline bool rows_ok(const void* p, int64_t ld, int64_t es, int k) {
   return p != nullptr && aligned_to(p, 16) && ld >= k && (ld * es) % 16 == 0;
 }
 
-template <bool BF16, bool UE8M0>
+// Operands past the L2s' 32 MiB are marked as streaming; smaller ones stay for whoever
+// reads them next.  (2048 x 7168 BF16 forward, 103 MB: 21.0 us streaming, 22.8 us not.)
+bool streams(int64_t bytes) { return bytes > (int64_t)32 << 20; }
+
+template <bool BF16, bool UE8M0, bool NT>
 void launch_fwd(const FwdParams& p, Shape s, dim3 grid, hipStream_t stream) {
   switch (s.chunks) {
-    case 1: hipLaunchKernelGGL((fwd_kernel<BF16, UE8M0, 1>), grid, dim3(s.threads), 0, stream, p); break;
-    case 2: hipLaunchKernelGGL((fwd_kernel<BF16, UE8M0, 2>), grid, dim3(s.threads), 0, stream, p); break;
-    default: hipLaunchKernelGGL((fwd_kernel<BF16, UE8M0, 4>), grid, dim3(s.threads), 0, stream, p); break;
+    case 1: hipLaunchKernelGGL((fwd_kernel<BF16, UE8M0, NT, 1>), grid, dim3(s.threads), 0, stream, p); break;
+    case 2: hipLaunchKernelGGL((fwd_kernel<BF16, UE8M0, NT, 2>), grid, dim3(s.threads), 0, stream, p); break;
+    default: hipLaunchKernelGGL((fwd_kernel<BF16, UE8M0, NT, 4>), grid, dim3(s.threads), 0, stream, p); break;
   }
 }
+template <bool BF16, bool UE8M0>
+void launch_fwd(const FwdParams& p, Shape s, bool nt, dim3 grid, hipStream_t stream) {
+  if (nt) launch_fwd<BF16, UE8M0, true>(p, s, grid, stream);
+  else launch_fwd<BF16, UE8M0, false>(p, s, grid, stream);
+}
 
-template <bool BF16>
+template <bool BF16, bool NT>
 void launch_bwd(const BwdParams& p, Shape s, dim3 grid, hipStream_t stream) {
   switch (s.chunks) {
-    case 1: hipLaunchKernelGGL((bwd_kernel<BF16, 1>), grid, dim3(s.threads), 0, stream, p); break;
-    case 2: hipLaunchKernelGGL((bwd_kernel<BF16, 2>), grid, dim3(s.threads), 0, stream, p); break;
-    default: hipLaunchKernelGGL((bwd_kernel<BF16, 4>), grid, dim3(s.threads), 0, stream, p); break;
+    case 1: hipLaunchKernelGGL((bwd_kernel<BF16, NT, 1>), grid, dim3(s.threads), 0, stream, p); break;
+    case 2: hipLaunchKernelGGL((bwd_kernel<BF16, NT, 2>), grid, dim3(s.threads), 0, stream, p); break;
+    default: hipLaunchKernelGGL((bwd_kernel<BF16, NT, 4>), grid, dim3(s.threads), 0, stream, p); break;
   }
+}
+template <bool BF16>
+void launch_bwd(const BwdParams& p, Shape s, bool nt, dim3 grid, hipStream_t stream) {
+  if (nt) launch_bwd<BF16, true>(p, s, grid, stream);
+  else launch_bwd<BF16, false>(p, s, grid, stream);
 }
 
 dg_status launch_status() {
@@ -356,27 +590,28 @@ dg_status dg_add_rms_norm_cast_to_fp8(const void* x, int64_t ldx, const void* re
   if (weight == nullptr || !aligned_to(weight, 16)) return DG_ERROR_INVALID_VALUE;
   if (q == nullptr || !aligned_to(q, 8) || ldq < k || ldq % 8 != 0) return DG_ERROR_INVALID_VALUE;
   if (sf == nullptr || !aligned_to(sf, 16) || ld_sf < m || ld_sf % 4 != 0) return DG_ERROR_INVALID_VALUE;
+  if (ld_sf > (int64_t)0xfffffff0 / 4 / (k / 128)) return DG_ERROR_NOT_SUPPORTED;  // 32-bit offsets into sf
   if (!aligned_to(rstd, 4)) return DG_ERROR_INVALID_VALUE;
   FwdParams p{static_cast<const uint8_t*>(x), static_cast<const uint8_t*>(residual),
               static_cast<uint8_t*>(residual_out), static_cast<const uint8_t*>(weight), static_cast<uint8_t*>(q),
-              sf, static_cast<uint8_t*>(y), rstd, ldx * es, ld_residual * es, ld_residual_out * es, ldq, ld_sf,
-              ldy * es, eps, m, k, 1, weight_dtype == DG_DTYPE_BF16};
-  const Shape s = shape_for(k, m < 1024 ? 1 : 4);
-  p.rows_per_wg = m < 8192 ? 1 : 4;
+              static_cast<uint8_t*>(sf), static_cast<uint8_t*>(y), rstd, ldx * es, ld_residual * es, ld_residual_out * es, ldq, ld_sf * 4,
+              ldy * es, eps, m, k, fwd_rows(m, k), weight_dtype == DG_DTYPE_BF16};
+  const Shape s = shape_for(k);
+  const bool nt = streams((int64_t)m * k * (es * (residual != nullptr ? 3 : 1) + 1));
   const dim3 grid((m + p.rows_per_wg - 1) / p.rows_per_wg);
   if (dtype == DG_DTYPE_BF16) {
-    if (ue8m0) launch_fwd<true, true>(p, s, grid, stream);
-    else launch_fwd<true, false>(p, s, grid, stream);
+    if (ue8m0) launch_fwd<true, true>(p, s, nt, grid, stream);
+    else launch_fwd<true, false>(p, s, nt, grid, stream);
   } else {
-    if (ue8m0) launch_fwd<false, true>(p, s, grid, stream);
-    else launch_fwd<false, false>(p, s, grid, stream);
+    if (ue8m0) launch_fwd<false, true>(p, s, nt, grid, stream);
+    else launch_fwd<false, false>(p, s, nt, grid, stream);
   }
   return launch_status();
 }
 
 size_t dg_get_rms_norm_backward_workspace_size(int m, int k) {
   if (m <= 0 || k <= 0 || k % 128 != 0 || k > norm::kMaxK) return 0;
-  return (size_t)norm::bwd_grid(m) * (size_t)k * sizeof(float);
+  return (size_t)norm::bwd_grid(m, k) * (size_t)k * sizeof(float);
 }
 
 dg_status dg_rms_norm_backward(const void* dy, int64_t ld_dy, const void* s, int64_t ld_s, dg_dtype dtype,
@@ -390,7 +625,7 @@ dg_status dg_rms_norm_backward(const void* dy, int64_t ld_dy, const void* s, int
   if (k % 128 != 0 || k > kMaxK) return DG_ERROR_NOT_SUPPORTED;
   if (k == 0) return DG_SUCCESS;
   if (dw == nullptr || !aligned_to(dw, 16)) return DG_ERROR_INVALID_VALUE;
-  const int grid = bwd_grid(m);
+  const int grid = m > 0 ? bwd_grid(m, k) : 0;
   if (m > 0) {
     const int64_t es = dtype == DG_DTYPE_BF16 ? 2 : 4;
     if (!rows_ok(dy, ld_dy, es, k) || !rows_ok(s, ld_s, es, k) || !rows_ok(dx, ld_dx, es, k))
@@ -405,13 +640,14 @@ dg_status dg_rms_norm_backward(const void* dy, int64_t ld_dy, const void* s, int
                       static_cast<const uint8_t*>(weight), static_cast<const uint8_t*>(dresidual), rstd,
                       static_cast<uint8_t*>(dx), static_cast<float*>(workspace), ld_dy * es, ld_s * es,
                       ld_dresidual * es, ld_dx * es, m, k, weight_dtype == DG_DTYPE_BF16};
-    const Shape sh = shape_for(k, 4);
-    if (dtype == DG_DTYPE_BF16) launch_bwd<true>(p, sh, dim3(grid), stream);
-    else launch_bwd<false>(p, sh, dim3(grid), stream);
+    const Shape sh = shape_for(k);
+    const bool nt = streams((int64_t)m * k * es * (dresidual != nullptr ? 4 : 3));
+    if (dtype == DG_DTYPE_BF16) launch_bwd<true>(p, sh, nt, dim3(grid), stream);
+    else launch_bwd<false>(p, sh, nt, dim3(grid), stream);
     const dg_status st = launch_status();
     if (st != DG_SUCCESS) return st;
   }
-  hipLaunchKernelGGL(dw_kernel, dim3(k / kDwCols), dim3(256), 0, stream, static_cast<const float*>(workspace), grid, k,
+  hipLaunchKernelGGL(dw_kernel, dim3(k / kDwCols), dim3(kDwRows * 8), 0, stream, static_cast<const float*>(workspace), grid, k,
                      dw, accumulate_dw != 0);
   return launch_status();
 }

@@ -54,7 +54,7 @@ def test_norm_gradient_refusals(lib):
                 dict(lddx=100), dict(dres=P, lddres=100), dict(dres=P + 2, lddres=512)):
         assert _grad(lib, **bad) == INVALID, bad
     need = lib.dg_get_rms_norm_backward_workspace_size(64, 512)
-    assert need == 64 * 512 * 4
+    assert 512 * 4 <= need <= 64 * 512 * 4 and need % (512 * 4) == 0  # one row of partial sums per workgroup
     for bad in (dict(ws=None), dict(ws=P + 16), dict(wsb=need - 1)):
         assert _grad(lib, **bad) == WORKSPACE, bad
     assert _grad(lib, k=0) == 0
