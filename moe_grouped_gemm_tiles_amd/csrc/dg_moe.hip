@@ -1,3 +1,12 @@
+#ifndef UPD
+#define UPD 2
+#endif
+#ifndef UPG
+#define UPG 2
+#endif
+#ifndef RH
+#define RH 6144
+#endif
 // dg_moe.hip -- a whole gated expert layer for a few tokens in two kernels, on
 // gfx950.
 //
@@ -31,6 +40,7 @@
 // further grid rows), so there is no planning kernel and no host work.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "dg.h"
@@ -44,13 +54,14 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
 constexpr int kPairs = 512;       // (token, slot) pairs a workgroup plans for
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 64;
 constexpr int kUpWaves = 4;
-constexpr int kDownWaves = 8;
 
 struct Params {
   const uint8_t* x;
@@ -73,24 +84,24 @@ struct Params {
 // place in `order` and, in `order`, the pairs (token in chunk * top_k + slot).
 // Pairs whose id is outside [0, experts) are in no list.
 struct Plan {
-  int16_t id[kPairs];
   uint16_t order[kPairs];
   uint16_t expert[kPairs];
   uint16_t start[kPairs + 1];
   int touched;
 };
 
-// Sorts the chunk's pairs by expert.  `count` holds kMaxExperts words of
-// scratch.  The order of an expert's own pairs depends on timing, but no
+// Sorts the chunk's pairs by expert; id[pair] becomes the pair's expert or -1.
+// `count` holds kMaxExperts words of scratch.  The order of an expert's own pairs depends on timing, but no
 // result does: a pair's place only says which MFMA column computes it.
-__device__ __forceinline__ void make_plan(const Params& p, int t0, int pairs, Plan& plan, uint32_t* count) {
+__device__ __forceinline__ void make_plan(const Params& p, int t0, int pairs, Plan& plan, int16_t* id,
+                                          uint32_t* count) {
   const int tid = threadIdx.x, nt = blockDim.x;
   for (int e = tid; e < p.experts; e += nt) count[e] = 0;
   __syncthreads();
   for (int i = tid; i < pairs; i += nt) {
     const int e = p.ids[(int64_t)t0 * p.top_k + i];
     const bool ok = e >= 0 && e < p.experts;
-    plan.id[i] = (int16_t)(ok ? e : -1);
+    id[i] = (int16_t)(ok ? e : -1);
     if (ok) atomicAdd(&count[e], 1u);
   }
   __syncthreads();
@@ -122,7 +133,7 @@ __device__ __forceinline__ void make_plan(const Params& p, int t0, int pairs, Pl
   }
   __syncthreads();
   for (int i = tid; i < pairs; i += nt) {
-    const int e = plan.id[i];
+    const int e = id[i];
     if (e >= 0) plan.order[atomicAdd(&count[e], 1u)] = (uint16_t)i;
   }
   __syncthreads();
@@ -132,30 +143,76 @@ __device__ __forceinline__ void make_plan(const Params& p, int t0, int pairs, Pl
 __device__ __forceinline__ float e8m0(uint32_t byte) {
   return byte == 255 ? __builtin_nanf("") : __uint_as_float(byte == 0 ? 0x00400000u : byte << 23);
 }
+// Scale of K block kb from the word that holds it (FP32, or four packed bytes).
 template <bool UE8M0>
-__device__ __forceinline__ float row_scale(const void* sf, int64_t ld, int64_t row, int kb) {
-  if constexpr (UE8M0)
-    return e8m0((static_cast<const uint32_t*>(sf)[(int64_t)(kb >> 2) * ld + row] >> (8 * (kb & 3))) & 255);
-  else
-    return static_cast<const float*>(sf)[(int64_t)kb * ld + row];
+__device__ __forceinline__ float scale_of(uint32_t word, int kb) {
+  return UE8M0 ? e8m0((word >> (8 * (kb & 3))) & 255) : __uint_as_float(word);
 }
-// Scale of K block kb in row block nb of a weight with nkb K blocks.
 template <bool UE8M0>
-__device__ __forceinline__ float block_scale(const void* sf, int64_t nb, int nkb, int kb) {
-  if constexpr (UE8M0)
-    return e8m0((static_cast<const uint32_t*>(sf)[nb * ((nkb + 3) >> 2) + (kb >> 2)] >> (8 * (kb & 3))) & 255);
+__device__ __forceinline__ int words(int nkb) { return UE8M0 ? (nkb + 3) >> 2 : nkb; }
+template <bool UE8M0>
+__device__ __forceinline__ int word_of(int kb) { return UE8M0 ? kb >> 2 : kb; }
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes, 0x00020000);
+}
+// The same from an address that is the same on every lane: into scalar registers, which the asm below needs.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const void* base, uint32_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a), hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+  return make_rsrc(reinterpret_cast<const void*>(((uint64_t)hi << 32) | lo), __builtin_amdgcn_readfirstlane(bytes));
+}
+constexpr uint32_t kNowhere = 0x80000000u;  // an offset past every operand here: the load gives zeros
+
+// A wave streams its operands through a ring of stages of its own in LDS, one
+// stage per 128-K block, with direct global->LDS loads: nothing is held in
+// registers while it is on its way, and no other wave is waited for.  The loads
+// are inline asm so that the compiler, which would wait for all of them before
+// any LDS read, does not see them; they write no register.  The waits are
+// counted below: a wave's vector loads complete in order, so "at most N
+// outstanding" means that all but the last N loads have arrived, whatever
+// stores are in flight besides.  s_nop 4 covers the wait states between a
+// scalar write of m0 or of the descriptor and its use, which the compiler does
+// not add inside asm.  NT: streaming, the weights are read once.
+template <int BYTES, bool NT>
+__device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t r, uint32_t lds, uint32_t off) {
+  if constexpr (BYTES == 16 && NT)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen nt lds" : : "v"(off), "s"(r), "s"(lds)
+                 : "memory", "m0");
+  else if constexpr (BYTES == 16)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" : : "v"(off), "s"(r), "s"(lds)
+                 : "memory", "m0");
   else
-    return static_cast<const float*>(sf)[nb * nkb + kb];
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tbuffer_load_dword %0, %1, 0 offen lds" : : "v"(off), "s"(r), "s"(lds)
+                 : "memory", "m0");
+}
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
+  asm volatile("" ::: "memory");
+}
+// The wave's LDS reads have returned (their place may be loaded into again).
+__device__ __forceinline__ void wait_lds() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((0xF) | (0x3 << 14) | (0x7 << 4) | (0x0 << 8));
+  asm volatile("" ::: "memory");
 }
 
-// Operand fragment of a 16-row x 128-byte block: lane (r16, q4) takes the 16-byte
-// chunks q4 and q4 + 4 of row r16.  Both operands of an MFMA are read this way, so
-// the order of K inside the block does not matter.
-__device__ __forceinline__ i32x8 load_frag(const uint8_t* p) {
-  const i32x4 lo = *reinterpret_cast<const i32x4*>(p);
-  const i32x4 hi = *reinterpret_cast<const i32x4*>(p + 64);
+// 16-row x 128-byte tiles lie in LDS row by row, the 16-byte chunk c of row r at
+// chunk c ^ (r & 7); one load instruction brings eight whole rows.  An operand
+// fragment: lane (r16, q4) takes chunks q4 and q4 + 4 of row r16.  Both operands of
+// an MFMA are read this way, so the order of K inside a block does not matter.
+__device__ __forceinline__ i32x8 read_frag(const uint8_t* tile, int r16, int q4) {
+  const uint8_t* row = tile + r16 * 128;
+  const i32x4 lo = *reinterpret_cast<const i32x4*>(row + ((q4 ^ (r16 & 7)) << 4));
+  const i32x4 hi = *reinterpret_cast<const i32x4*>(row + (((q4 + 4) ^ (r16 & 7)) << 4));
   return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 }
+// Chunk of its row that a lane loads (row = 8 h + lane / 8).
+__device__ __forceinline__ uint32_t tile_chunk(int lane) { return ((lane & 7) ^ (lane >> 3)) << 4; }
 
 __device__ __forceinline__ f32x4 mfma_fp8(i32x8 a, i32x8 b) {
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
@@ -173,119 +230,305 @@ __device__ __forceinline__ bf16x8 widen(uint32_t lo, uint32_t hi) {
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + __expf(-g)); }
 
-// grid: (inter / 16, most touched experts, chunks).
-template <bool UE8M0>
+// Stage of the gate/up kernel: gate tile, up tile, NG token tiles, the tokens' scales
+// (one per lane), the two block scales.
+template <int NG>
+struct UpStage {
+  static constexpr int kX = 4096, kSx = kX + 2048 * NG, kSw = kSx + 256, kBytes = kSw + 256;
+  static constexpr int kLoads = 6 + 2 * NG;
+};
+
+// A unit is one touched expert's tile of 16 columns of a; workgroups take contiguous
+// ranges of units.  An expert with more than 16 * NG tokens takes several passes.
+// grid: (workgroups, chunks).
+template <bool UE8M0, int NG, int D>
 __global__ void __launch_bounds__(kUpWaves * 64) gate_up_kernel(const Params p) {
+  using S = UpStage<NG>;
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[kUpWaves * D * S::kBytes];
+  __shared__ __attribute__((aligned(16))) float red[kUpWaves * 8 * 64];
   __shared__ Plan plan;
-  __shared__ uint32_t count[kMaxExperts];
-  __shared__ float red[kUpWaves][8][64];
+  static_assert(sizeof(red) >= sizeof(uint32_t) * kMaxExperts, "the plan's scratch shares red");
   const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, q4 = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int t0 = blockIdx.z * p.tokens;
-  const int pairs = min(p.tokens, p.m - t0) * p.top_k;
-  make_plan(p, t0, pairs, plan, count);
-  const int i = blockIdx.y;
-  if (i >= plan.touched) return;
-  const int e = plan.expert[i], first = plan.start[i], n = plan.start[i + 1] - first;
-  const int col0 = blockIdx.x * 16;
-  const int nkb = p.hidden >> 7, nb = p.inter >> 7;
-  const uint8_t* wg = p.w13 + ((int64_t)e * 2 * p.inter + col0 + r16) * p.hidden + 16 * q4;
-  const uint8_t* wu = wg + (int64_t)p.inter * p.hidden;
-  const int64_t sb = (int64_t)e * 2 * nb + (col0 >> 7);
-  for (int g0 = 0; g0 < n; g0 += 16) {
-    const int pair = plan.order[first + min(g0 + r16, n - 1)];
-    const int64_t tok = t0 + pair / p.top_k;
-    const uint8_t* x = p.x + tok * p.ldx + 16 * q4;
-    f32x4 ag = {0.f, 0.f, 0.f, 0.f}, au = {0.f, 0.f, 0.f, 0.f};
-    for (int kb = wave; kb < nkb; kb += kUpWaves) {
-      const i32x8 fg = load_frag(wg + kb * 128), fu = load_frag(wu + kb * 128), fx = load_frag(x + kb * 128);
-      const float sx = row_scale<UE8M0>(p.sfx, p.ld_sfx, tok, kb);
-      const float sg = sx * block_scale<UE8M0>(p.sf13, sb, nkb, kb);
-      const float su = sx * block_scale<UE8M0>(p.sf13, sb + nb, nkb, kb);
-      const f32x4 pg = mfma_fp8(fg, fx), pu = mfma_fp8(fu, fx);
+  const int wave = uniform(tid >> 6);
+  const int t0 = blockIdx.y * p.tokens;
+  const int tokens = min(p.tokens, p.m - t0);
+  make_plan(p, t0, tokens * p.top_k, plan, reinterpret_cast<int16_t*>(ring), reinterpret_cast<uint32_t*>(red));
+  const int tiles = p.inter >> 4, nkb = p.hidden >> 7, nb = p.inter >> 7, nw = words<UE8M0>(nkb);
+  const int rounds = (nkb + kUpWaves - 1) / kUpWaves;
+  const int units = uniform(plan.touched) * tiles;
+  const int u0 = uniform((int)((int64_t)units * blockIdx.x / gridDim.x));
+  const int u1 = uniform((int)((int64_t)units * (blockIdx.x + 1) / gridDim.x));
+  if (u0 >= u1) return;
+
+  uint8_t* my_ring = ring + wave * D * S::kBytes;
+  const uint32_t my_lds = (uint32_t)uniform((int)(uintptr_t)(lds_ptr_t)my_ring);
+  const __amdgpu_buffer_rsrc_t rx = uniform_rsrc(p.x + (int64_t)t0 * p.ldx, (uint32_t)((tokens - 1) * p.ldx + p.hidden));
+  const __amdgpu_buffer_rsrc_t rsx =
+      uniform_rsrc(static_cast<const uint32_t*>(p.sfx) + t0, (uint32_t)(((nw - 1) * p.ld_sfx + tokens) * 4));
+  const uint32_t w_off = (uint32_t)(lane >> 3) * p.hidden + tile_chunk(lane);
+
+  // Where the next stage to load is: pass (expert i, tile t, first token g0), round it.
+  int li = uniform(u0 / tiles), lt = u0 - li * tiles, lg0 = 0, lit = 0, left = u1 - u0, ln = 0, slot = 0;
+  const uint8_t* lw = nullptr;
+  const uint32_t* lsw = nullptr;
+  uint32_t x_off[NG][2], sx_off;
+  auto pass = [&]() __attribute__((always_inline)) {
+    const int e = uniform((int)plan.expert[li]), first = uniform((int)plan.start[li]);
+    ln = uniform((int)plan.start[li + 1]) - first;
+    lw = p.w13 + ((int64_t)e * 2 * p.inter + lt * 16) * p.hidden;
+    lsw = static_cast<const uint32_t*>(p.sf13) + ((int64_t)e * 2 * nb + (lt >> 3)) * nw;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        ag[r] = __builtin_fmaf(pg[r], sg, ag[r]);
-        au[r] = __builtin_fmaf(pu[r], su, au[r]);
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int c = lg0 + 16 * g + 8 * h + (lane >> 3);
+        x_off[g][h] = c < ln ? (uint32_t)(plan.order[first + c] / p.top_k) * (uint32_t)p.ldx + tile_chunk(lane) : kNowhere;
       }
+    const int c = lg0 + lane;
+    sx_off = lane < 16 * NG && c < ln ? (uint32_t)(plan.order[first + c] / p.top_k) * 4 : kNowhere;
+  };
+  auto load = [&]() __attribute__((always_inline)) {
+    const int kb = wave + lit * kUpWaves;
+    const uint32_t k = kb < nkb ? (uint32_t)kb * 128 : kNowhere;
+    const uint32_t lds = (uint32_t)uniform((int)(my_lds + slot * S::kBytes));
+    const __amdgpu_buffer_rsrc_t rg = uniform_rsrc(lw, 16u * p.hidden);
+    const __amdgpu_buffer_rsrc_t ru = uniform_rsrc(lw + (int64_t)p.inter * p.hidden, 16u * p.hidden);
+    const __amdgpu_buffer_rsrc_t rsw = uniform_rsrc(lsw, (uint32_t)((nb + 1) * nw * 4));
+    to_lds<16, true>(rg, lds, w_off + k);
+    to_lds<16, true>(rg, lds + 1024, w_off + 8u * p.hidden + k);
+    to_lds<16, true>(ru, lds + 2048, w_off + k);
+    to_lds<16, true>(ru, lds + 3072, w_off + 8u * p.hidden + k);
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) to_lds<16, false>(rx, lds + S::kX + 2048 * g + 1024 * h, x_off[g][h] + k);
+    const uint32_t wd = kb < nkb ? (uint32_t)word_of<UE8M0>(kb) : kNowhere;
+    to_lds<4, false>(rsx, lds + S::kSx, kb < nkb && sx_off != kNowhere ? sx_off + wd * (uint32_t)p.ld_sfx * 4 : kNowhere);
+    to_lds<4, false>(rsw, lds + S::kSw, kb < nkb && lane < 2 ? (lane * nb * nw + wd) * 4 : kNowhere);
+    slot = slot + 1 == D ? 0 : slot + 1;
+    if (++lit < rounds) return;
+    lit = 0;
+    lg0 += 16 * NG;
+    if (lg0 >= ln) {
+      lg0 = 0;
+      --left;
+      if (++lt == tiles) lt = 0, ++li;
     }
+    if (left > 0) pass();
+  };
+  pass();
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      red[wave][r][lane] = ag[r];
-      red[wave][4 + r][lane] = au[r];
-    }
-    __syncthreads();
-    if (wave == 0 && g0 + r16 < n) {
-      __bf16 a[4];
+  for (int d = 0; d < D; ++d)
+    if (left > 0) load();
+
+  int at = 0;
+  for (int u = u0; u < u1; ++u) {
+    const int i = uniform(u / tiles), col0 = (u - i * tiles) * 16;
+    const int first = uniform((int)plan.start[i]), n = uniform((int)plan.start[i + 1]) - first;
+    for (int g0 = 0; g0 < n; g0 += 16 * NG) {
+      f32x4 ag[NG], au[NG];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        float g = red[0][r][lane], u = red[0][4 + r][lane];
+      for (int g = 0; g < NG; ++g) ag[g] = au[g] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int it = 0; it < rounds; ++it) {
+        if (left > 0) wait_loads<(D - 1) * S::kLoads>();
+        else wait_loads<0>();
+        const uint8_t* st = my_ring + at * S::kBytes;
+        const int kb = wave + it * kUpWaves;
+        const i32x8 fg = read_frag(st, r16, q4), fu = read_frag(st + 2048, r16, q4);
+        const uint32_t* sw = reinterpret_cast<const uint32_t*>(st + S::kSw);
+        const float sg = scale_of<UE8M0>(sw[0], kb), su = scale_of<UE8M0>(sw[1], kb);
 #pragma unroll
-        for (int w = 1; w < kUpWaves; ++w) {
-          g += red[w][r][lane];
-          u += red[w][4 + r][lane];
+        for (int g = 0; g < NG; ++g) {
+          if (g > 0 && g0 + 16 * g >= n) break;
+          const i32x8 fx = read_frag(st + S::kX + 2048 * g, r16, q4);
+          const float sx = scale_of<UE8M0>(reinterpret_cast<const uint32_t*>(st + S::kSx)[16 * g + r16], kb);
+          const f32x4 pg = mfma_fp8(fg, fx), pu = mfma_fp8(fu, fx);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            ag[g][r] = __builtin_fmaf(pg[r], sx * sg, ag[g][r]);
+            au[g][r] = __builtin_fmaf(pu[r], sx * su, au[g][r]);
+          }
         }
-        a[r] = (__bf16)(silu(g) * u);
+        wait_lds();
+        if (left > 0) load();
+        at = at + 1 == D ? 0 : at + 1;
       }
-      __bf16* o = p.act + ((int64_t)t0 * p.top_k + pair) * p.inter + col0 + 4 * q4;
-      typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-      *reinterpret_cast<bf16x4*>(o) = bf16x4{a[0], a[1], a[2], a[3]};
+      // the waves' sums meet group by group: red[wave][gate 0..3, up 0..3][lane]
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        if (g > 0 && g0 + 16 * g >= n) break;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          red[(wave * 8 + r) * 64 + lane] = ag[g][r];
+          red[(wave * 8 + 4 + r) * 64 + lane] = au[g][r];
+        }
+        __syncthreads();
+        if (g % kUpWaves == wave && g0 + 16 * g + r16 < n) {
+          bf16x4 a;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            float vg = 0.f, vu = 0.f;
+#pragma unroll
+            for (int k = 0; k < kUpWaves; ++k) {
+              vg += red[(k * 8 + r) * 64 + lane];
+              vu += red[(k * 8 + 4 + r) * 64 + lane];
+            }
+            a[r] = (__bf16)(silu(vg) * vu);
+          }
+          const int pair = plan.order[first + g0 + 16 * g + r16];
+          *reinterpret_cast<bf16x4*>(p.act + ((int64_t)t0 * p.top_k + pair) * p.inter + col0 + 4 * q4) = a;
+        }
+        __syncthreads();
+      }
     }
-    __syncthreads();
   }
 }
 
-// grid: (hidden / 16, chunks).  Dynamic LDS: slots * pairs * 16 floats.
-template <bool UE8M0>
-__global__ void __launch_bounds__(kDownWaves * 64) down_kernel(const Params p) {
+// Stage of the down kernel: R weight tiles, NG tiles of 16 tokens x 128 BF16 values of a,
+// the block scale.
+template <int R, int NG>
+struct DownStage {
+  static constexpr int kA = 2048 * R, kSw = kA + 4096 * NG, kBytes = kSw + 256;
+  static constexpr int kLoads = 2 * R + 4 * NG + 1;
+};
+
+// grid: (hidden / (16 * R), chunks).  Dynamic LDS: the sums, slots * pairs * 16 * R floats.
+template <bool UE8M0, int R, int NG, int W, int D>
+__global__ void __launch_bounds__(W * 64) down_kernel(const Params p) {
+  using S = DownStage<R, NG>;
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[W * D * S::kBytes];
   __shared__ Plan plan;
-  __shared__ uint32_t count[kMaxExperts];
-  extern __shared__ float sums[];  // [K range][pair][16]
+  __shared__ int16_t id[kPairs];
+  extern __shared__ __attribute__((aligned(16))) float sums[];  // [K range][pair][16 * R]
+  static_assert(sizeof(ring) >= sizeof(uint32_t) * kMaxExperts, "the plan's scratch shares the ring");
   const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, q4 = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = uniform(tid >> 6);
   const int t0 = blockIdx.y * p.tokens;
   const int tokens = min(p.tokens, p.m - t0), pairs = tokens * p.top_k;
-  make_plan(p, t0, pairs, plan, count);
-  const int col0 = blockIdx.x * 16;
-  const int nkb = p.inter >> 7;
-  // K is split into ranges until there are two pieces for each wave
-  int split = 1;
-  while (2 * split <= p.slots && 2 * split <= nkb && plan.touched * split < 2 * kDownWaves) split *= 2;
-  for (int u = wave; u < plan.touched * split; u += kDownWaves) {
-    const int i = u / split, s = u % split;
-    const int e = plan.expert[i], first = plan.start[i], n = plan.start[i + 1] - first;
-    const int kb0 = nkb * s / split, kb1 = nkb * (s + 1) / split;
-    const uint8_t* w = p.w2 + ((int64_t)e * p.hidden + col0 + r16) * p.inter + 16 * q4;
-    const int64_t sb = (int64_t)e * (p.hidden >> 7) + (col0 >> 7);
-    for (int g0 = 0; g0 < n; g0 += 16) {
-      const int pair = plan.order[first + min(g0 + r16, n - 1)];
-      const __bf16* a = p.act + ((int64_t)t0 * p.top_k + pair) * p.inter + 16 * q4;
-      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-      for (int kb = kb0; kb < kb1; ++kb) {
-        const i32x8 f = load_frag(w + kb * 128);
-        f32x4 part = {0.f, 0.f, 0.f, 0.f};
+  make_plan(p, t0, pairs, plan, id, reinterpret_cast<uint32_t*>(ring));
+  const int col0 = blockIdx.x * 16 * R;
+  const int nkb = p.inter >> 7, nw = words<UE8M0>(nkb);
+  const int touched = uniform(plan.touched);
+  // K ranges per expert: as many as balance the waves best, a piece costing two K blocks beside its own
+  int split = 1, best = 0x7fffffff;
+  for (int s = 1; s <= p.slots && s <= nkb; s *= 2) {
+    const int cost = ((touched * s + W - 1) / W) * ((nkb + s - 1) / s + 2);
+    if (cost < best) best = cost, split = s;
+  }
+  const int pieces = touched * split;
+
+  uint8_t* my_ring = ring + wave * D * S::kBytes;
+  const uint32_t my_lds = (uint32_t)uniform((int)(uintptr_t)(lds_ptr_t)my_ring);
+  const __amdgpu_buffer_rsrc_t ra =
+      uniform_rsrc(p.act + (int64_t)t0 * p.top_k * p.inter, (uint32_t)pairs * p.inter * 2);
+  const uint32_t w_off = (uint32_t)(lane >> 3) * p.inter + tile_chunk(lane);
+
+  // Where the next stage to load is: piece lu (expert, K range), first token lg0, K block lkb.
+  int lu = wave, lg0 = 0, lkb = 0, lkb0 = 0, lkb1 = 0, ln = 0, slot = 0;
+  const uint8_t* lw = nullptr;
+  const uint32_t* lsw = nullptr;
+  uint32_t a_off[NG][4];
+  auto pass = [&]() __attribute__((always_inline)) {
+    const int i = uniform(lu / split), s = lu - i * split;
+    const int e = uniform((int)plan.expert[i]), first = uniform((int)plan.start[i]);
+    ln = uniform((int)plan.start[i + 1]) - first;
+    lkb0 = lkb = uniform(nkb * s / split);
+    lkb1 = uniform(nkb * (s + 1) / split);
+    lw = p.w2 + ((int64_t)e * p.hidden + col0) * p.inter;
+    lsw = static_cast<const uint32_t*>(p.sf2) + ((int64_t)e * (p.hidden >> 7) + (col0 >> 7)) * nw;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const bf16x8 b = *reinterpret_cast<const bf16x8*>(a + kb * 128 + (c >> 1) * 64 + (c & 1) * 8);
-          part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen(f[2 * c], f[2 * c + 1]), b, part, 0, 0, 0);
-        }
-        const float sc = block_scale<UE8M0>(p.sf2, sb, nkb, kb);
+    for (int g = 0; g < NG; ++g)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(part[r], sc, acc[r]);
+      for (int h = 0; h < 4; ++h) {
+        const int row = 4 * h + (lane >> 4), c = lg0 + 16 * g + row;
+        a_off[g][h] = c < ln ? (uint32_t)plan.order[first + c] * (uint32_t)p.inter * 2 + (((lane & 15) ^ row) << 4) : kNowhere;
       }
-      if (g0 + r16 < n)
-        *reinterpret_cast<f32x4*>(&sums[((int64_t)s * pairs + pair) * 16 + 4 * q4]) = acc;
+  };
+  auto load = [&]() __attribute__((always_inline)) {
+    const uint32_t lds = (uint32_t)uniform((int)(my_lds + slot * S::kBytes));
+    const __amdgpu_buffer_rsrc_t rw = uniform_rsrc(lw, (uint32_t)(16 * R) * p.inter);
+    const __amdgpu_buffer_rsrc_t rsw = uniform_rsrc(lsw, (uint32_t)nw * 4);
+#pragma unroll
+    for (int r = 0; r < 2 * R; ++r) to_lds<16, true>(rw, lds + 1024 * r, w_off + (uint32_t)(8 * r) * p.inter + lkb * 128);
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int h = 0; h < 4; ++h) to_lds<16, false>(ra, lds + S::kA + 4096 * g + 1024 * h, a_off[g][h] + lkb * 256);
+    to_lds<4, false>(rsw, lds + S::kSw, lane == 0 ? word_of<UE8M0>(lkb) * 4 : kNowhere);
+    slot = slot + 1 == D ? 0 : slot + 1;
+    if (++lkb < lkb1) return;
+    lg0 += 16 * NG;
+    if (lg0 >= ln) lg0 = 0, lu += W;
+    if (lu < pieces) pass();
+  };
+  if (lu < pieces) pass();
+#pragma unroll
+  for (int d = 0; d < D; ++d)
+    if (lu < pieces) load();
+
+  int at = 0;
+  for (int u = wave; u < pieces; u += W) {
+    const int i = uniform(u / split), s = u - i * split;
+    const int first = uniform((int)plan.start[i]), n = uniform((int)plan.start[i + 1]) - first;
+    const int kb0 = uniform(nkb * s / split), kb1 = uniform(nkb * (s + 1) / split);
+    for (int g0 = 0; g0 < n; g0 += 16 * NG) {
+      f32x4 acc[NG][R];
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int r = 0; r < R; ++r) acc[g][r] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (lu < pieces) wait_loads<(D - 1) * S::kLoads>();
+        else wait_loads<0>();
+        const uint8_t* st = my_ring + at * S::kBytes;
+        const float f = scale_of<UE8M0>(*reinterpret_cast<const uint32_t*>(st + S::kSw), kb);
+        bf16x8 b[R][4];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const i32x8 w = read_frag(st + 2048 * r, r16, q4);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) b[r][c] = widen(w[2 * c], w[2 * c + 1]);
+        }
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          if (g > 0 && g0 + 16 * g >= n) break;
+          const uint8_t* row = st + S::kA + 4096 * g + r16 * 256;
+          bf16x8 a[4];  // K chunks in the order of the weight fragment's
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            a[c] = *reinterpret_cast<const bf16x8*>(row + (((2 * q4 + (c & 1) + 8 * (c >> 1)) ^ r16) << 4));
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            f32x4 part = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[r][c], a[c], part, 0, 0, 0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[g][r][k] = __builtin_fmaf(part[k], f, acc[g][r][k]);
+          }
+        }
+        wait_lds();
+        if (lu < pieces) load();
+        at = at + 1 == D ? 0 : at + 1;
+      }
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        if (g0 + 16 * g + r16 >= n) continue;
+        const int pair = plan.order[first + g0 + 16 * g + r16];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          *reinterpret_cast<f32x4*>(&sums[((s * pairs + pair) * R + r) * 16 + 4 * q4]) = acc[g][r];
+      }
     }
   }
   __syncthreads();
-  for (int o = tid; o < tokens * 16; o += kDownWaves * 64) {
-    const int t = o >> 4, c = o & 15;
+  for (int o = tid; o < tokens * 16 * R; o += W * 64) {
+    const int t = o / (16 * R), c = o % (16 * R);
     float v = 0.f;
     for (int j = 0; j < p.top_k; ++j) {
       const int pair = t * p.top_k + j;
-      if (plan.id[pair] < 0) continue;
+      if (id[pair] < 0) continue;
       float y = 0.f;
-      for (int s = 0; s < split; ++s) y += sums[((int64_t)s * pairs + pair) * 16 + c];
+      for (int s = 0; s < split; ++s) y += sums[(s * pairs + pair) * 16 * R + c];
       v = __builtin_fmaf(p.tw[(int64_t)(t0 + t) * p.top_k + j], y, v);
     }
     const __bf16 b = (__bf16)v;
@@ -295,7 +538,41 @@ __global__ void __launch_bounds__(kDownWaves * 64) down_kernel(const Params p) {
 
 inline bool aligned_to(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-constexpr int kSumBytes = 32 * 1024;  // LDS for the pairs' sums: kPairs * 64 bytes
+constexpr int kLds = 160 * 1024;  // LDS of a CU
+
+template <bool UE8M0, int NG, int D>
+void launch_up(const Params& p, dim3 grid, hipStream_t stream) {
+  hipLaunchKernelGGL((gate_up_kernel<UE8M0, NG, D>), grid, dim3(kUpWaves * 64), 0, stream, p);
+}
+
+// Tries R * 16 columns per workgroup; false where the sums of `pairs` pairs do not fit in LDS.
+template <bool UE8M0, int R, int NG, int W, int D>
+bool launch_down(Params p, int chunks, int pairs, hipStream_t stream) {
+  const int room = kLds - W * D * DownStage<R, NG>::kBytes - (int)sizeof(Plan) - 2 * kPairs - 1024;
+  p.slots = std::min(16, room / (pairs * 64 * R));
+  if (p.slots < 1) return false;
+  const dim3 grid(p.hidden / (16 * R), chunks);
+  hipLaunchKernelGGL((down_kernel<UE8M0, R, NG, W, D>), grid, dim3(W * 64), p.slots * pairs * 64 * R, stream, p);
+  return true;
+}
+
+template <bool UE8M0>
+void launch(const Params& p, int chunks, int pairs, hipStream_t stream) {
+  // tokens per expert if all ids are of this device: how many groups of 16 a pass takes
+  const int cus = dg_get_num_cus() > 0 ? dg_get_num_cus() : 256;
+  const int64_t units = (int64_t)std::min(pairs, p.experts) * (p.inter / 16);
+  const int each = pairs / p.experts;
+  const auto grid = [&](int per_cu) { return dim3((unsigned)std::min<int64_t>(units, (int64_t)cus * per_cu), chunks); };
+  if (each <= 8) launch_up<UE8M0, 1, UPD>(p, grid(UPG), stream);
+  else if (each <= 20) launch_up<UE8M0, 2, 2>(p, grid(2), stream);
+  else launch_up<UE8M0, 4, 2>(p, grid(1), stream);
+  const bool wide = p.hidden >= RH;
+  if (each <= 8) {
+    if (!(wide && launch_down<UE8M0, 2, 1, 8, 2>(p, chunks, pairs, stream))) launch_down<UE8M0, 1, 1, 8, 2>(p, chunks, pairs, stream);
+  } else {
+    if (!(wide && launch_down<UE8M0, 2, 2, 4, 2>(p, chunks, pairs, stream))) launch_down<UE8M0, 1, 2, 4, 2>(p, chunks, pairs, stream);
+  }
+}
 
 dg_status run(const void* x, int64_t ldx, const void* sfx, int64_t ld_sfx, const void* w13, const void* sf13,
               const void* w2, const void* sf2, const int32_t* ids, const float* tw, void* out, int64_t ld_out, int m,
@@ -312,6 +589,11 @@ dg_status run(const void* x, int64_t ldx, const void* sfx, int64_t ld_sfx, const
     if (q == nullptr || !aligned_to(q, 4)) return DG_ERROR_INVALID_VALUE;
   if (ldx < hidden || ldx % 16 != 0 || ld_out < hidden || ld_out % 8 != 0 || ld_sfx < m || ld_sfx % 4 != 0)
     return DG_ERROR_INVALID_VALUE;
+  // offsets inside a chunk of tokens are 32-bit
+  const int64_t chunk_tokens = std::min(m, kPairs / top_k);
+  if (chunk_tokens * ldx >= kNowhere || (int64_t)(hidden / 128) * ld_sfx * 4 >= kNowhere ||
+      (int64_t)32 * hidden >= kNowhere || (int64_t)kPairs * inter * 2 >= kNowhere)
+    return DG_ERROR_NOT_SUPPORTED;
   if (workspace == nullptr || !aligned_to(workspace, 256) ||
       workspace_bytes < dg_get_moe_workspace_size(m, top_k, inter))
     return DG_ERROR_WORKSPACE;
@@ -321,13 +603,8 @@ dg_status run(const void* x, int64_t ldx, const void* sfx, int64_t ld_sfx, const
   const int chunks = (m + p.tokens - 1) / p.tokens;
   if (chunks > 65535) return DG_ERROR_NOT_SUPPORTED;
   const int pairs = (m < p.tokens ? m : p.tokens) * top_k;
-  p.slots = kSumBytes / (pairs * 64);
-  const int most = pairs < experts ? pairs : experts;
-  const dim3 up(inter / 16, most, chunks), down(hidden / 16, chunks);
-  if (ue8m0) hipLaunchKernelGGL(gate_up_kernel<true>, up, dim3(kUpWaves * 64), 0, stream, p);
-  else hipLaunchKernelGGL(gate_up_kernel<false>, up, dim3(kUpWaves * 64), 0, stream, p);
-  if (ue8m0) hipLaunchKernelGGL(down_kernel<true>, down, dim3(kDownWaves * 64), kSumBytes, stream, p);
-  else hipLaunchKernelGGL(down_kernel<false>, down, dim3(kDownWaves * 64), kSumBytes, stream, p);
+  if (ue8m0) launch<true>(p, chunks, pairs, stream);
+  else launch<false>(p, chunks, pairs, stream);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? DG_SUCCESS : dg::record_hip_error(e);
 }
