@@ -1,12 +1,3 @@
-#ifndef UPD
-#define UPD 2
-#endif
-#ifndef UPG
-#define UPG 2
-#endif
-#ifndef RH
-#define RH 6144
-#endif
 // dg_moe.hip -- a whole gated expert layer for a few tokens in two kernels, on
 // gfx950.
 //
@@ -17,27 +8,38 @@
 // x, W13 and W2 are E4M3 with the GEMMs' scales (per row and 128 K for x, per
 // 128 x 128 block for the weights).  With a few tokens each touched expert's
 // weights are used for a handful of rows, so the layer is the reading of them
-// once; everything else is arranged around that.
+// once from HBM, and everything else is arranged around that.
 //
-//   * gate/up kernel: a workgroup owns 16 gate and the matching 16 up rows of
-//     one touched expert, its four waves split K, and every wave streams the
-//     rows straight into registers as the first operand of
-//     v_mfma_f32_16x16x128_f8f6f4 (one MFMA = one 128-K scale block); the
-//     expert's tokens, up to 16 per MFMA, are the second operand.  The K
-//     partial sums meet in LDS, and a is written once per (token, slot), in
-//     BF16: the second product's MFMA takes BF16, and one rounding of a to 8
-//     more bits than the E4M3 that the composed path would store costs the
-//     result no more than the rounding of the output does.
-//   * down kernel: a workgroup owns 16 output columns of all tokens; its waves
-//     take (expert, K range) pieces in turn.  E4M3 is exact in BF16, so W2
-//     fragments are converted in registers and the block scale is applied to
-//     the FP32 sum of each 128 K values.  Each (token, slot) leaves its own
-//     16 sums in LDS, and the slots are added in the order of j: no atomics,
-//     the same bits every time.
+//   * gate/up kernel: a workgroup takes 16 gate and the matching 16 up rows of a
+//     touched expert at a time (a unit), its four waves split K, and one
+//     v_mfma_f32_16x16x128_f8f6f4 covers 16 rows, 16 tokens and one 128-K scale
+//     block.  The waves' partial sums meet in LDS and a is written once per (token,
+//     slot) in BF16.  (The second product then takes BF16; the composed path would
+//     store a in E4M3, 4 bits less.  The rounding costs the result as much as the
+//     rounding of the output itself.)
+//   * down kernel: a workgroup owns 8, 16 or 32 output columns of all tokens; its
+//     waves take (expert, K range) pieces in turn.  E4M3 is exact in BF16, so W2
+//     fragments are widened in registers and the block scale is applied to the
+//     FP32 sum of each 128 K values.  Each (token, slot) leaves its own sums in
+//     LDS, and the slots are added in the order of j: no atomics on results, the
+//     same bits every time.
+//   * both kernels bring their operands with direct global->LDS loads into rings of
+//     K-block stages, one ring per wave, the next stages on their way while one is
+//     multiplied.  A load instruction brings whole 128-byte lines (8 rows), which is
+//     what lets the weights be marked as streaming: reading 235 MB of gate/up weights
+//     takes 35 us that way, 40 us unmarked; fragments loaded straight into registers, 64
+//     bytes of a line at a time, took 43 us unmarked and 50 us marked.
+//   * which tokens go to which expert is worked out by every workgroup from ids (at
+//     most kPairs (token, slot) pairs per chunk of tokens; larger batches are further
+//     grid rows), about 1.5 us, so there is no planning kernel and no host work.
 //
-// Which tokens go to which expert is worked out by every workgroup from ids
-// (at most kPairs (token, slot) pairs per chunk of tokens; larger batches are
-// further grid rows), so there is no planning kernel and no host work.
+// Measured (both kernels, weights not in any cache; reads alone reach 7.0 TB/s):
+//     1 token, 8 of 16 experts of 7168 x 2048       63 us   5.6 TB/s (36 + 22 us of kernels)
+//     9 tokens, top 8 of 64 experts of 4096 x 1024  98 us   5.8 TB/s
+//     64 tokens, top 4 of 16 experts of 7168 x 2048 142 us  4.9 TB/s (a's tiles fill the down
+//                                                   kernel's rings: fewer stages in flight)
+//     37 tokens, 32 of 128 experts of 2048 x 1408   52 us   4.4 TB/s (two launches and two
+//                                                   plans are 8 us of it)
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -62,6 +64,7 @@ constexpr int kPairs = 512;       // (token, slot) pairs a workgroup plans for
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopK = 64;
 constexpr int kUpWaves = 4;
+constexpr int kDownWaves = 16;
 
 struct Params {
   const uint8_t* x;
@@ -78,35 +81,50 @@ struct Params {
   int m, top_k, experts, hidden, inter;
   int tokens;  // tokens per chunk
   int slots;   // down kernel: most K ranges whose sums fit in LDS
+  int ring;    // down kernel: bytes of LDS for the rings
 };
 
 // The pairs of one chunk by expert: expert of the i-th touched one, its first
-// place in `order` and, in `order`, the pairs (token in chunk * top_k + slot).
+// place in `order` and, in `order`, the pairs (token in chunk, slot).
 // Pairs whose id is outside [0, experts) are in no list.
 struct Plan {
-  uint16_t order[kPairs];
+  uint16_t order[kPairs];  // token << 6 | slot
   uint16_t expert[kPairs];
   uint16_t start[kPairs + 1];
   int touched;
+  int most;  // tokens of the fullest expert
 };
 
+static_assert(kPairs <= 1 << 10 && kMaxTopK <= 64, "order[] packs a token and a slot into 16 bits");
+__device__ __forceinline__ int pair_of(const Params& p, int place) { return (place >> 6) * p.top_k + (place & 63); }
+
 // Sorts the chunk's pairs by expert; id[pair] becomes the pair's expert or -1.
-// `count` holds kMaxExperts words of scratch.  The order of an expert's own pairs depends on timing, but no
-// result does: a pair's place only says which MFMA column computes it.
+// `count` holds kMaxExperts words of scratch.  The order of an expert's own
+// pairs depends on timing, but no result does: a pair's place only says which
+// MFMA column computes it.
+template <int THREADS>
 __device__ __forceinline__ void make_plan(const Params& p, int t0, int pairs, Plan& plan, int16_t* id,
                                           uint32_t* count) {
-  const int tid = threadIdx.x, nt = blockDim.x;
-  for (int e = tid; e < p.experts; e += nt) count[e] = 0;
+  const int tid = threadIdx.x;
+  constexpr int PER = (kPairs + THREADS - 1) / THREADS;
+  int mine[PER];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int i = j * THREADS + tid;
+    const int e = i < pairs ? p.ids[(int64_t)t0 * p.top_k + i] : -1;
+    mine[j] = e >= 0 && e < p.experts ? e : -1;
+  }
+  for (int e = tid; e < p.experts; e += THREADS) count[e] = 0;
   __syncthreads();
-  for (int i = tid; i < pairs; i += nt) {
-    const int e = p.ids[(int64_t)t0 * p.top_k + i];
-    const bool ok = e >= 0 && e < p.experts;
-    id[i] = (int16_t)(ok ? e : -1);
-    if (ok) atomicAdd(&count[e], 1u);
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int i = j * THREADS + tid;
+    if (i < pairs) id[i] = (int16_t)mine[j];
+    if (mine[j] >= 0) atomicAdd(&count[mine[j]], 1u);
   }
   __syncthreads();
   if (tid < 64) {  // one wave: touched experts in order of their number, and where their pairs start
-    int touched = 0, start = 0;
+    int touched = 0, start = 0, most = 0;
     for (int e0 = 0; e0 < p.experts; e0 += 64) {
       const int e = e0 + tid;
       const int c = e < p.experts ? (int)count[e] : 0;
@@ -125,17 +143,23 @@ __device__ __forceinline__ void make_plan(const Params& p, int t0, int pairs, Pl
       }
       touched += __popcll(mask);
       start += __shfl(before, 63);
+      most = max(most, c);
     }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) most = max(most, __shfl_xor(most, off));
     if (tid == 0) {
       plan.touched = touched;
+      plan.most = most;
       plan.start[touched] = (uint16_t)start;
     }
   }
   __syncthreads();
-  for (int i = tid; i < pairs; i += nt) {
-    const int e = id[i];
-    if (e >= 0) plan.order[atomicAdd(&count[e], 1u)] = (uint16_t)i;
-  }
+#pragma unroll
+  for (int j = 0; j < PER; ++j)
+    if (mine[j] >= 0) {
+      const int pair = j * THREADS + tid, token = pair / p.top_k;
+      plan.order[atomicAdd(&count[mine[j]], 1u)] = (uint16_t)(token << 6 | (pair - token * p.top_k));
+    }
   __syncthreads();
 }
 
@@ -241,9 +265,10 @@ struct UpStage {
 // A unit is one touched expert's tile of 16 columns of a; workgroups take contiguous
 // ranges of units.  An expert with more than 16 * NG tokens takes several passes.
 // grid: (workgroups, chunks).
-template <bool UE8M0, int NG, int D>
+template <bool UE8M0, int NG>
 __global__ void __launch_bounds__(kUpWaves * 64) gate_up_kernel(const Params p) {
   using S = UpStage<NG>;
+  constexpr int D = 2;  // stages of a ring
   __shared__ __attribute__((aligned(1024))) uint8_t ring[kUpWaves * D * S::kBytes];
   __shared__ __attribute__((aligned(16))) float red[kUpWaves * 8 * 64];
   __shared__ Plan plan;
@@ -252,12 +277,13 @@ __global__ void __launch_bounds__(kUpWaves * 64) gate_up_kernel(const Params p) 
   const int wave = uniform(tid >> 6);
   const int t0 = blockIdx.y * p.tokens;
   const int tokens = min(p.tokens, p.m - t0);
-  make_plan(p, t0, tokens * p.top_k, plan, reinterpret_cast<int16_t*>(ring), reinterpret_cast<uint32_t*>(red));
+  make_plan<kUpWaves * 64>(p, t0, tokens * p.top_k, plan, reinterpret_cast<int16_t*>(ring), reinterpret_cast<uint32_t*>(red));
   const int tiles = p.inter >> 4, nkb = p.hidden >> 7, nb = p.inter >> 7, nw = words<UE8M0>(nkb);
   const int rounds = (nkb + kUpWaves - 1) / kUpWaves;
   const int units = uniform(plan.touched) * tiles;
-  const int u0 = uniform((int)((int64_t)units * blockIdx.x / gridDim.x));
-  const int u1 = uniform((int)((int64_t)units * (blockIdx.x + 1) / gridDim.x));
+  const int each = units / (int)gridDim.x, more = units - each * (int)gridDim.x;  // the first `more` take one more
+  const int u0 = uniform((int)blockIdx.x * each + min((int)blockIdx.x, more));
+  const int u1 = u0 + each + ((int)blockIdx.x < more ? 1 : 0);
   if (u0 >= u1) return;
 
   uint8_t* my_ring = ring + wave * D * S::kBytes;
@@ -268,7 +294,8 @@ __global__ void __launch_bounds__(kUpWaves * 64) gate_up_kernel(const Params p) 
   const uint32_t w_off = (uint32_t)(lane >> 3) * p.hidden + tile_chunk(lane);
 
   // Where the next stage to load is: pass (expert i, tile t, first token g0), round it.
-  int li = uniform(u0 / tiles), lt = u0 - li * tiles, lg0 = 0, lit = 0, left = u1 - u0, ln = 0, slot = 0;
+  const int i0 = uniform(u0 / tiles);
+  int li = i0, lt = u0 - i0 * tiles, lg0 = 0, lit = 0, left = u1 - u0, ln = 0, slot = 0;
   const uint8_t* lw = nullptr;
   const uint32_t* lsw = nullptr;
   uint32_t x_off[NG][2], sx_off;
@@ -282,10 +309,10 @@ __global__ void __launch_bounds__(kUpWaves * 64) gate_up_kernel(const Params p) 
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int c = lg0 + 16 * g + 8 * h + (lane >> 3);
-        x_off[g][h] = c < ln ? (uint32_t)(plan.order[first + c] / p.top_k) * (uint32_t)p.ldx + tile_chunk(lane) : kNowhere;
+        x_off[g][h] = c < ln ? (uint32_t)(plan.order[first + c] >> 6) * (uint32_t)p.ldx + tile_chunk(lane) : kNowhere;
       }
     const int c = lg0 + lane;
-    sx_off = lane < 16 * NG && c < ln ? (uint32_t)(plan.order[first + c] / p.top_k) * 4 : kNowhere;
+    sx_off = lane < 16 * NG && c < ln ? (uint32_t)(plan.order[first + c] >> 6) * 4 : kNowhere;
   };
   auto load = [&]() __attribute__((always_inline)) {
     const int kb = wave + lit * kUpWaves;
@@ -321,9 +348,9 @@ __global__ void __launch_bounds__(kUpWaves * 64) gate_up_kernel(const Params p) 
   for (int d = 0; d < D; ++d)
     if (left > 0) load();
 
-  int at = 0;
+  int at = 0, i = i0, t = u0 - i0 * tiles;
   for (int u = u0; u < u1; ++u) {
-    const int i = uniform(u / tiles), col0 = (u - i * tiles) * 16;
+    const int col0 = t * 16;
     const int first = uniform((int)plan.start[i]), n = uniform((int)plan.start[i + 1]) - first;
     for (int g0 = 0; g0 < n; g0 += 16 * NG) {
       f32x4 ag[NG], au[NG];
@@ -375,164 +402,203 @@ __global__ void __launch_bounds__(kUpWaves * 64) gate_up_kernel(const Params p) 
             }
             a[r] = (__bf16)(silu(vg) * vu);
           }
-          const int pair = plan.order[first + g0 + 16 * g + r16];
+          const int pair = pair_of(p, plan.order[first + g0 + 16 * g + r16]);
           *reinterpret_cast<bf16x4*>(p.act + ((int64_t)t0 * p.top_k + pair) * p.inter + col0 + 4 * q4) = a;
         }
         __syncthreads();
       }
     }
+    if (++t == tiles) t = 0, ++i;
   }
 }
 
-// Stage of the down kernel: R weight tiles, NG tiles of 16 tokens x 128 BF16 values of a,
-// the block scale.
-template <int R, int NG>
+// Down kernel.  A stage holds the 128-K block of RB weight rows, 4 * AL tokens x 128 BF16
+// values of a, and the block scale.
+template <int RB, int AL>
 struct DownStage {
-  static constexpr int kA = 2048 * R, kSw = kA + 4096 * NG, kBytes = kSw + 256;
-  static constexpr int kLoads = 2 * R + 4 * NG + 1;
+  static constexpr int kA = 128 * RB, kSw = kA + 1024 * AL, kBytes = kSw + 256;
+  static constexpr int kLoads = RB / 8 + AL + 1;
 };
 
-// grid: (hidden / (16 * R), chunks).  Dynamic LDS: the sums, slots * pairs * 16 * R floats.
-template <bool UE8M0, int R, int NG, int W, int D>
-__global__ void __launch_bounds__(W * 64) down_kernel(const Params p) {
-  using S = DownStage<R, NG>;
-  __shared__ __attribute__((aligned(1024))) uint8_t ring[W * D * S::kBytes];
-  __shared__ Plan plan;
-  __shared__ int16_t id[kPairs];
-  extern __shared__ __attribute__((aligned(16))) float sums[];  // [K range][pair][16 * R]
-  static_assert(sizeof(ring) >= sizeof(uint32_t) * kMaxExperts, "the plan's scratch shares the ring");
+struct DownWork {
+  int t0, pairs, col0;
+  int split;         // log2 of the K ranges per expert
+  int waves, depth;  // waves that stream, stages of their rings
+};
+
+// What the waves do between the plan and the weighted sum: wave w takes pieces (expert, K
+// range) w, w + waves, ..., each for 4 * AL of the expert's tokens at a time.
+template <bool UE8M0, int RB, int AL>
+__device__ __forceinline__ void down_stream(const Params& p, const Plan& plan, const DownWork& k, uint8_t* ring,
+                                            float* sums) {
+  using S = DownStage<RB, AL>;
+  constexpr int T = 4 * AL, R = (RB + 15) / 16, NG = (T + 15) / 16;
   const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, q4 = lane >> 4;
   const int wave = uniform(tid >> 6);
-  const int t0 = blockIdx.y * p.tokens;
-  const int tokens = min(p.tokens, p.m - t0), pairs = tokens * p.top_k;
-  make_plan(p, t0, pairs, plan, id, reinterpret_cast<uint32_t*>(ring));
-  const int col0 = blockIdx.x * 16 * R;
   const int nkb = p.inter >> 7, nw = words<UE8M0>(nkb);
-  const int touched = uniform(plan.touched);
-  // K ranges per expert: as many as balance the waves best, a piece costing two K blocks beside its own
-  int split = 1, best = 0x7fffffff;
-  for (int s = 1; s <= p.slots && s <= nkb; s *= 2) {
-    const int cost = ((touched * s + W - 1) / W) * ((nkb + s - 1) / s + 2);
-    if (cost < best) best = cost, split = s;
-  }
-  const int pieces = touched * split;
-
-  uint8_t* my_ring = ring + wave * D * S::kBytes;
+  const int pieces = uniform(plan.touched) << k.split;
+  if (wave >= k.waves) return;
+  uint8_t* my_ring = ring + wave * k.depth * S::kBytes;
   const uint32_t my_lds = (uint32_t)uniform((int)(uintptr_t)(lds_ptr_t)my_ring);
   const __amdgpu_buffer_rsrc_t ra =
-      uniform_rsrc(p.act + (int64_t)t0 * p.top_k * p.inter, (uint32_t)pairs * p.inter * 2);
+      uniform_rsrc(p.act + (int64_t)k.t0 * p.top_k * p.inter, (uint32_t)k.pairs * p.inter * 2);
   const uint32_t w_off = (uint32_t)(lane >> 3) * p.inter + tile_chunk(lane);
 
-  // Where the next stage to load is: piece lu (expert, K range), first token lg0, K block lkb.
-  int lu = wave, lg0 = 0, lkb = 0, lkb0 = 0, lkb1 = 0, ln = 0, slot = 0;
+  // Where the next stage to load is: piece lu, first token lg0, K block lkb.
+  int lu = wave, lg0 = 0, lkb = 0, lkb1 = 0, ln = 0, slot = 0;
   const uint8_t* lw = nullptr;
   const uint32_t* lsw = nullptr;
-  uint32_t a_off[NG][4];
+  uint32_t a_off[AL];
   auto pass = [&]() __attribute__((always_inline)) {
-    const int i = uniform(lu / split), s = lu - i * split;
+    const int i = lu >> k.split, s = lu - (i << k.split);
     const int e = uniform((int)plan.expert[i]), first = uniform((int)plan.start[i]);
     ln = uniform((int)plan.start[i + 1]) - first;
-    lkb0 = lkb = uniform(nkb * s / split);
-    lkb1 = uniform(nkb * (s + 1) / split);
-    lw = p.w2 + ((int64_t)e * p.hidden + col0) * p.inter;
-    lsw = static_cast<const uint32_t*>(p.sf2) + ((int64_t)e * (p.hidden >> 7) + (col0 >> 7)) * nw;
+    lkb = nkb * s >> k.split;
+    lkb1 = nkb * (s + 1) >> k.split;
+    lw = p.w2 + ((int64_t)e * p.hidden + k.col0) * p.inter;
+    lsw = static_cast<const uint32_t*>(p.sf2) + ((int64_t)e * (p.hidden >> 7) + (k.col0 >> 7)) * nw;
 #pragma unroll
-    for (int g = 0; g < NG; ++g)
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        const int row = 4 * h + (lane >> 4), c = lg0 + 16 * g + row;
-        a_off[g][h] = c < ln ? (uint32_t)plan.order[first + c] * (uint32_t)p.inter * 2 + (((lane & 15) ^ row) << 4) : kNowhere;
-      }
+    for (int h = 0; h < AL; ++h) {
+      const int row = 4 * h + (lane >> 4), c = lg0 + row;
+      a_off[h] = c < ln ? (uint32_t)pair_of(p, plan.order[first + c]) * (uint32_t)p.inter * 2 + (((lane ^ row) & 15) << 4) : kNowhere;
+    }
   };
   auto load = [&]() __attribute__((always_inline)) {
     const uint32_t lds = (uint32_t)uniform((int)(my_lds + slot * S::kBytes));
-    const __amdgpu_buffer_rsrc_t rw = uniform_rsrc(lw, (uint32_t)(16 * R) * p.inter);
+    const __amdgpu_buffer_rsrc_t rw = uniform_rsrc(lw, (uint32_t)RB * p.inter);
     const __amdgpu_buffer_rsrc_t rsw = uniform_rsrc(lsw, (uint32_t)nw * 4);
 #pragma unroll
-    for (int r = 0; r < 2 * R; ++r) to_lds<16, true>(rw, lds + 1024 * r, w_off + (uint32_t)(8 * r) * p.inter + lkb * 128);
+    for (int r = 0; r < RB / 8; ++r)
+      to_lds<16, true>(rw, lds + 1024 * r, w_off + (uint32_t)(8 * r) * p.inter + lkb * 128);
 #pragma unroll
-    for (int g = 0; g < NG; ++g)
-#pragma unroll
-      for (int h = 0; h < 4; ++h) to_lds<16, false>(ra, lds + S::kA + 4096 * g + 1024 * h, a_off[g][h] + lkb * 256);
+    for (int h = 0; h < AL; ++h) to_lds<16, false>(ra, lds + S::kA + 1024 * h, a_off[h] + lkb * 256);
     to_lds<4, false>(rsw, lds + S::kSw, lane == 0 ? word_of<UE8M0>(lkb) * 4 : kNowhere);
-    slot = slot + 1 == D ? 0 : slot + 1;
+    slot = slot + 1 == k.depth ? 0 : slot + 1;
     if (++lkb < lkb1) return;
-    lg0 += 16 * NG;
-    if (lg0 >= ln) lg0 = 0, lu += W;
+    lg0 += T;
+    if (lg0 >= ln) lg0 = 0, lu += k.waves;
     if (lu < pieces) pass();
   };
   if (lu < pieces) pass();
-#pragma unroll
-  for (int d = 0; d < D; ++d)
+  for (int d = 0; d < k.depth; ++d)
     if (lu < pieces) load();
 
   int at = 0;
-  for (int u = wave; u < pieces; u += W) {
-    const int i = uniform(u / split), s = u - i * split;
+  for (int u = wave; u < pieces; u += k.waves) {
+    const int i = u >> k.split, s = u - (i << k.split);
     const int first = uniform((int)plan.start[i]), n = uniform((int)plan.start[i + 1]) - first;
-    const int kb0 = uniform(nkb * s / split), kb1 = uniform(nkb * (s + 1) / split);
-    for (int g0 = 0; g0 < n; g0 += 16 * NG) {
+    const int kb0 = nkb * s >> k.split, kb1 = nkb * (s + 1) >> k.split;
+    for (int g0 = 0; g0 < n; g0 += T) {
       f32x4 acc[NG][R];
 #pragma unroll
       for (int g = 0; g < NG; ++g)
 #pragma unroll
         for (int r = 0; r < R; ++r) acc[g][r] = f32x4{0.f, 0.f, 0.f, 0.f};
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (lu < pieces) wait_loads<(D - 1) * S::kLoads>();
-        else wait_loads<0>();
+        if (lu >= pieces) wait_loads<0>();
+        else if (k.depth == 2) wait_loads<S::kLoads>();
+        else if (k.depth == 3) wait_loads<2 * S::kLoads>();
+        else wait_loads<3 * S::kLoads>();
         const uint8_t* st = my_ring + at * S::kBytes;
         const float f = scale_of<UE8M0>(*reinterpret_cast<const uint32_t*>(st + S::kSw), kb);
         bf16x8 b[R][4];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          const i32x8 w = read_frag(st + 2048 * r, r16, q4);
+          const i32x8 w = read_frag(st + 2048 * r, RB == 8 ? r16 & 7 : r16, q4);
 #pragma unroll
           for (int c = 0; c < 4; ++c) b[r][c] = widen(w[2 * c], w[2 * c + 1]);
         }
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
           if (g > 0 && g0 + 16 * g >= n) break;
-          const uint8_t* row = st + S::kA + 4096 * g + r16 * 256;
+          // rows past the last token held repeat earlier ones: their columns are not stored
+          const int row = 16 * g + (T - 16 * g >= 16 ? r16 : r16 & ((T & 15) - 1));
+          const uint8_t* arow = st + S::kA + row * 256;
           bf16x8 a[4];  // K chunks in the order of the weight fragment's
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            a[c] = *reinterpret_cast<const bf16x8*>(row + (((2 * q4 + (c & 1) + 8 * (c >> 1)) ^ r16) << 4));
+            a[c] = *reinterpret_cast<const bf16x8*>(arow + (((2 * q4 + (c & 1) + 8 * (c >> 1)) ^ (row & 15)) << 4));
 #pragma unroll
           for (int r = 0; r < R; ++r) {
             f32x4 part = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int c = 0; c < 4; ++c) part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[r][c], a[c], part, 0, 0, 0);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) acc[g][r][k] = __builtin_fmaf(part[k], f, acc[g][r][k]);
+            for (int j = 0; j < 4; ++j) acc[g][r][j] = __builtin_fmaf(part[j], f, acc[g][r][j]);
           }
         }
         wait_lds();
         if (lu < pieces) load();
-        at = at + 1 == D ? 0 : at + 1;
+        at = at + 1 == k.depth ? 0 : at + 1;
       }
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        if (g0 + 16 * g + r16 >= n) continue;
-        const int pair = plan.order[first + g0 + 16 * g + r16];
+        const int c = 16 * g + r16;
+        if (c >= T || g0 + c >= n || (RB == 8 && q4 >= 2)) continue;
+        const int pair = pair_of(p, plan.order[first + g0 + c]);
 #pragma unroll
         for (int r = 0; r < R; ++r)
-          *reinterpret_cast<f32x4*>(&sums[((s * pairs + pair) * R + r) * 16 + 4 * q4]) = acc[g][r];
+          *reinterpret_cast<f32x4*>(&sums[(s * k.pairs + pair) * RB + 16 * r + 4 * q4]) = acc[g][r];
       }
     }
   }
+}
+
+// grid: (hidden / RB, chunks).  Dynamic LDS: the rings, then the sums ([K range][pair][RB]).
+template <bool UE8M0, int RB>
+__global__ void __launch_bounds__(kDownWaves * 64) down_kernel(const Params p) {
+  extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+  __shared__ Plan plan;
+  __shared__ int16_t id[kPairs];
+  __shared__ float tw[kPairs];
+  static_assert(kDownWaves * 64 >= kPairs, "a thread for every pair");
+  const int tid = threadIdx.x;
+  float* sums = reinterpret_cast<float*>(lds + p.ring);
+  DownWork k;
+  k.t0 = blockIdx.y * p.tokens;
+  const int tokens = min(p.tokens, p.m - k.t0);
+  k.pairs = tokens * p.top_k;
+  k.col0 = blockIdx.x * RB;
+  const float my_tw = tid < k.pairs ? p.tw[(int64_t)k.t0 * p.top_k + tid] : 0.f;
+  make_plan<kDownWaves * 64>(p, k.t0, k.pairs, plan, id, reinterpret_cast<uint32_t*>(lds));
+  if (tid < kPairs) tw[tid] = my_tw;
+  const int nkb = p.inter >> 7, touched = uniform(plan.touched), most = uniform(plan.most);
+  // the fullest expert's tokens decide how much of a stage a takes, and with it how many
+  // waves have rings of at least two stages
+  const int al = most <= 4 ? 1 : most <= 8 ? 2 : most <= 16 ? 4 : most <= 24 ? 6 : 8;
+  const int bytes = 128 * RB + 1024 * al + 256;
+  int lw = 4;  // log2 of the waves
+  static_assert(kDownWaves == 16, "2^lw");
+  while (lw > 1 && (bytes << lw) * 2 > p.ring) --lw;
+  k.waves = 1 << lw;
+  k.depth = (bytes << lw) * 4 <= p.ring ? 4 : (bytes << lw) * 3 <= p.ring ? 3 : 2;
+  // K ranges per expert: as many as balance the waves best, a piece costing two K blocks beside its own
+  k.split = 0;
+  int best = 0x7fffffff;
+  for (int s = 0; 1 << s <= p.slots && 1 << s <= nkb; ++s) {
+    const int cost = (((touched << s) + k.waves - 1) >> lw) * (((nkb + (1 << s) - 1) >> s) + 2);
+    if (cost < best) best = cost, k.split = s;
+  }
+  switch (al) {
+    case 1: down_stream<UE8M0, RB, 1>(p, plan, k, lds, sums); break;
+    case 2: down_stream<UE8M0, RB, 2>(p, plan, k, lds, sums); break;
+    case 4: down_stream<UE8M0, RB, 4>(p, plan, k, lds, sums); break;
+    case 6: down_stream<UE8M0, RB, 6>(p, plan, k, lds, sums); break;
+    default: down_stream<UE8M0, RB, 8>(p, plan, k, lds, sums); break;
+  }
   __syncthreads();
-  for (int o = tid; o < tokens * 16 * R; o += W * 64) {
-    const int t = o / (16 * R), c = o % (16 * R);
+  for (int o = tid; o < tokens * RB; o += kDownWaves * 64) {
+    const int t = o / RB, c = o % RB;
     float v = 0.f;
     for (int j = 0; j < p.top_k; ++j) {
       const int pair = t * p.top_k + j;
       if (id[pair] < 0) continue;
       float y = 0.f;
-      for (int s = 0; s < split; ++s) y += sums[(s * pairs + pair) * 16 * R + c];
-      v = __builtin_fmaf(p.tw[(int64_t)(t0 + t) * p.top_k + j], y, v);
+      for (int s = 0; s < 1 << k.split; ++s) y += sums[(s * k.pairs + pair) * RB + c];
+      v = __builtin_fmaf(tw[pair], y, v);
     }
     const __bf16 b = (__bf16)v;
-    p.out[(int64_t)(t0 + t) * p.ld_out + col0 + c] = __builtin_bit_cast(uint16_t, b);
+    p.out[(int64_t)(k.t0 + t) * p.ld_out + k.col0 + c] = __builtin_bit_cast(uint16_t, b);
   }
 }
 
@@ -540,38 +606,37 @@ inline bool aligned_to(const void* p, uintptr_t a) { return reinterpret_cast<uin
 
 constexpr int kLds = 160 * 1024;  // LDS of a CU
 
-template <bool UE8M0, int NG, int D>
+template <bool UE8M0, int NG>
 void launch_up(const Params& p, dim3 grid, hipStream_t stream) {
-  hipLaunchKernelGGL((gate_up_kernel<UE8M0, NG, D>), grid, dim3(kUpWaves * 64), 0, stream, p);
+  hipLaunchKernelGGL((gate_up_kernel<UE8M0, NG>), grid, dim3(kUpWaves * 64), 0, stream, p);
 }
 
-// Tries R * 16 columns per workgroup; false where the sums of `pairs` pairs do not fit in LDS.
-template <bool UE8M0, int R, int NG, int W, int D>
-bool launch_down(Params p, int chunks, int pairs, hipStream_t stream) {
-  const int room = kLds - W * D * DownStage<R, NG>::kBytes - (int)sizeof(Plan) - 2 * kPairs - 1024;
-  p.slots = std::min(16, room / (pairs * 64 * R));
-  if (p.slots < 1) return false;
-  const dim3 grid(p.hidden / (16 * R), chunks);
-  hipLaunchKernelGGL((down_kernel<UE8M0, R, NG, W, D>), grid, dim3(W * 64), p.slots * pairs * 64 * R, stream, p);
-  return true;
+template <bool UE8M0, int RB>
+void launch_down(Params p, int chunks, int pairs, hipStream_t stream) {
+  const int room = (kLds - (int)sizeof(Plan) - 6 * kPairs - 512) / 1024 * 1024;
+  p.slots = std::max(1, std::min(16, 16 * 1024 / (pairs * RB * 4)));
+  const int sum_bytes = (p.slots * pairs * RB * 4 + 1023) / 1024 * 1024;
+  p.ring = room - sum_bytes;
+  const dim3 grid(p.hidden / RB, chunks);
+  hipLaunchKernelGGL((down_kernel<UE8M0, RB>), grid, dim3(kDownWaves * 64), room, stream, p);
 }
 
 template <bool UE8M0>
 void launch(const Params& p, int chunks, int pairs, hipStream_t stream) {
-  // tokens per expert if all ids are of this device: how many groups of 16 a pass takes
   const int cus = dg_get_num_cus() > 0 ? dg_get_num_cus() : 256;
   const int64_t units = (int64_t)std::min(pairs, p.experts) * (p.inter / 16);
-  const int each = pairs / p.experts;
   const auto grid = [&](int per_cu) { return dim3((unsigned)std::min<int64_t>(units, (int64_t)cus * per_cu), chunks); };
-  if (each <= 8) launch_up<UE8M0, 1, UPD>(p, grid(UPG), stream);
-  else if (each <= 20) launch_up<UE8M0, 2, 2>(p, grid(2), stream);
-  else launch_up<UE8M0, 4, 2>(p, grid(1), stream);
-  const bool wide = p.hidden >= RH;
-  if (each <= 8) {
-    if (!(wide && launch_down<UE8M0, 2, 1, 8, 2>(p, chunks, pairs, stream))) launch_down<UE8M0, 1, 1, 8, 2>(p, chunks, pairs, stream);
-  } else {
-    if (!(wide && launch_down<UE8M0, 2, 2, 4, 2>(p, chunks, pairs, stream))) launch_down<UE8M0, 1, 2, 4, 2>(p, chunks, pairs, stream);
-  }
+  // Tokens of an expert per pass: no more than 16 can come where there are no more tokens;
+  // else 32, with room for an uneven routing, until that is the average itself (pairs / experts,
+  // if all ids are of this device).  An expert with more takes further passes over its weights.
+  if (std::min(p.m, p.tokens) <= 16) launch_up<UE8M0, 1>(p, grid(2), stream);
+  else if (pairs / p.experts <= 20) launch_up<UE8M0, 2>(p, grid(2), stream);
+  else launch_up<UE8M0, 4>(p, grid(1), stream);
+  // columns per workgroup: what gives the fewest rounds over the CUs, weighted with their length
+  const auto rounds = [&](int rb) { return (int64_t)((p.hidden / rb * (int64_t)chunks + cus - 1) / cus) * rb; };
+  if (rounds(32) <= rounds(16) && rounds(32) <= rounds(8)) launch_down<UE8M0, 32>(p, chunks, pairs, stream);
+  else if (rounds(16) <= rounds(8)) launch_down<UE8M0, 16>(p, chunks, pairs, stream);
+  else launch_down<UE8M0, 8>(p, chunks, pairs, stream);
 }
 
 dg_status run(const void* x, int64_t ldx, const void* sfx, int64_t ld_sfx, const void* w13, const void* sf13,
@@ -599,7 +664,7 @@ dg_status run(const void* x, int64_t ldx, const void* sfx, int64_t ld_sfx, const
     return DG_ERROR_WORKSPACE;
   Params p{static_cast<const uint8_t*>(x), sfx, static_cast<const uint8_t*>(w13), sf13,
            static_cast<const uint8_t*>(w2), sf2, ids, tw, static_cast<__bf16*>(workspace),
-           static_cast<uint16_t*>(out), ldx, ld_sfx, ld_out, m, top_k, experts, hidden, inter, kPairs / top_k, 1};
+           static_cast<uint16_t*>(out), ldx, ld_sfx, ld_out, m, top_k, experts, hidden, inter, kPairs / top_k, 1, 0};
   const int chunks = (m + p.tokens - 1) / p.tokens;
   if (chunks > 65535) return DG_ERROR_NOT_SUPPORTED;
   const int pairs = (m < p.tokens ? m : p.tokens) * top_k;
