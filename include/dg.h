@@ -427,7 +427,8 @@ size_t dg_get_moe_workspace_size(int m, int top_k, int inter);
  *               call then only measures it).
  * norm          DEVICE FP32 [1].
  * workspace     dg_get_clip_workspace_size() bytes, 256-byte aligned, any contents.
- * Two launches per 128 tensors; the same bits every time.
+ * Two launches per 128 tensors, and one more out of place past 32 MiB; the same
+ * bits every time.  More than 4 TiB of gradients -> DG_ERROR_NOT_SUPPORTED.
  */
 typedef struct {
   void* data;

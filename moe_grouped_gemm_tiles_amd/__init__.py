@@ -189,7 +189,8 @@ def _check(status: int):
 
 
 def _stream(t: torch.Tensor) -> int:
-    return torch.cuda.current_stream(t.device).cuda_stream
+    """The current HIP stream of t's device (0.1 us; building a torch.cuda.Stream for it takes 2 us)."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _unit_last_stride(t: torch.Tensor) -> bool:
@@ -527,29 +528,71 @@ def fp8_mqa_logits(q: torch.Tensor, kv_pair, weights: torch.Tensor, ks: torch.Te
     return out
 
 
-def _rows(t: torch.Tensor, like: torch.Tensor, name: str):
-    """(pointer, row stride) of a 2-D operand with like's shape, dtype and device."""
-    if t.dtype != like.dtype or t.device != like.device or t.shape != like.shape or not _unit_last_stride(t):
-        raise ValueError(f"{name} must match the input's shape, dtype and device and be contiguous in its last "
-                         "dimension")
+def _like(t: torch.Tensor, dtype, dev: int, shape, name: str):
+    """(pointer, row stride) of a 2-D operand of the given dtype, device and shape."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        raise ValueError(f"{name} must have the input's dtype, device and shape {tuple(shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), shape[1]
+    if not _unit_last_stride(t):
+        raise ValueError(f"{name} must be contiguous in its last dimension")
     return t.data_ptr(), _ld(t, 0, 16 // t.element_size())
 
 
-def _norm_weight(weight: torch.Tensor, x: torch.Tensor) -> int:
-    if weight.dtype not in _DTYPES or weight.device != x.device or weight.shape != (x.shape[1],) \
-            or not weight.is_contiguous():
-        raise ValueError("weight must be a contiguous bfloat16 or float32 tensor [K] on the input's device")
-    return _DTYPES[weight.dtype]
+def _flat(t: torch.Tensor, dtype, dev: int, shape, name: str) -> int:
+    """Pointer of a contiguous operand of the given dtype, device and shape."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on the input's device")
+    return t.data_ptr()
 
 
-def _scratch(workspace: torch.Tensor | None, size: int, device: torch.device, name: str = "workspace"):
+def _norm_input(x: torch.Tensor, weight: torch.Tensor, name: str):
+    """(dtype, device index, shape, dtype code, pointer, row stride) of a norm's first operand, and
+    (dtype code, pointer) of its weight."""
+    dtype, dev, shape = x.dtype, x.get_device(), x.shape
+    code = _DTYPES.get(dtype)
+    if code is None or dev < 0 or len(shape) != 2:
+        raise TypeError(f"{name} must be a 2-D bfloat16 or float32 GPU tensor")
+    wcode = _DTYPES.get(weight.dtype)
+    if wcode is None:
+        raise TypeError("weight must be bfloat16 or float32")
+    ptr, ld = _like(x, dtype, dev, shape, name)
+    return dtype, dev, shape, code, ptr, ld, wcode, _flat(weight, weight.dtype, dev, shape[1:], "weight")
+
+
+def _codes(t: torch.Tensor, dev: int, shape, name: str, align: int):
+    """(pointer, row stride) of a 2-D operand of E4M3 codes."""
+    if t.dtype is not torch.float8_e4m3fn and t.dtype is not torch.uint8:
+        raise TypeError(f"{name} must be torch.float8_e4m3fn or uint8 codes, got {t.dtype}")
+    if t.get_device() != dev or t.shape != shape:
+        raise ValueError(f"{name} must be on the input's device and of shape {tuple(shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), shape[1]
+    if not _unit_last_stride(t):
+        raise ValueError(f"{name} must be K-contiguous")
+    return t.data_ptr(), _ld(t, 0, align)
+
+
+def _row_scales(sf: torch.Tensor, dev: int, m: int, k: int, name: str):
+    """(UE8M0?, pointer, row stride) of transposed row scales [K/128 (or packed words), ld >= M]."""
+    ue = sf.dtype is torch.int32
+    if not ue and sf.dtype is not torch.float32:
+        raise TypeError(f"{name} must be float32 (FP32 scales) or int32 (packed UE8M0)")
+    shape = sf.shape
+    if sf.get_device() != dev or len(shape) != 2 or shape[0] != _sf_rows(k, ue) or shape[1] < m \
+            or not _unit_last_stride(sf):
+        raise ValueError(f"{name} shape {tuple(shape)} does not fit M = {m}, K = {k}")
+    return ue, sf.data_ptr(), _ld(sf, 0, 4)
+
+
+def _scratch(workspace: torch.Tensor | None, size: int, dev: int):
     """(tensor to keep alive, pointer, bytes) of a workspace with any contents; without one, a
     fresh one from torch's allocator (its blocks are at least 512-byte aligned)."""
     if workspace is None:
-        workspace = torch.empty(size, dtype=torch.uint8, device=device)
-    elif workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor on the output's device")
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the output's device")
+    return workspace, workspace.data_ptr(), workspace.nbytes
 
 
 def add_rms_norm_cast_to_fp8(x: torch.Tensor, weight: torch.Tensor, eps: float, q: torch.Tensor, sf: torch.Tensor,
@@ -559,27 +602,26 @@ def add_rms_norm_cast_to_fp8(x: torch.Tensor, weight: torch.Tensor, eps: float, 
     pass: x [M, K] -> q E4M3 [M, K], sf FP32 [K/128, ld >= M] or packed UE8M0 int32 [ceil(K/512), ld]
     (the GEMMs' a operand), residual_out = s (may be residual itself).  Optional outputs: y = v in
     x's dtype, rstd FP32 [M] for ``rms_norm_backward``."""
-    lib = load_library()
-    dt, ue = _cast_args(x, q, sf)
-    m, k = x.shape
-    wdt = _norm_weight(weight, x)
-    if sf.dim() != 2 or sf.shape[0] != _sf_rows(k, ue) or sf.shape[1] < m:
-        raise ValueError(f"sf shape {tuple(sf.shape)} does not fit x {tuple(x.shape)}")
-    if q.device != x.device or sf.device != x.device:
-        raise ValueError("q and sf must be on x's device")
+    lib = _lib or load_library()
+    dtype, dev, shape, code, xp, ldx, wcode, wp = _norm_input(x, weight, "x")
+    m, k = shape
+    qp, ldq = _codes(q, dev, shape, "q", 8)
+    ue, sfp, ld_sf = _row_scales(sf, dev, m, k, "sf")
     if (residual is None) != (residual_out is None):
         raise ValueError("residual and residual_out go together")
-    res, ldr = _rows(residual, x, "residual") if residual is not None else (None, 0)
-    ro, ldro = _rows(residual_out, x, "residual_out") if residual_out is not None else (None, 0)
-    yp, ldy = _rows(y, x, "y") if y is not None else (None, 0)
-    if rstd is not None and (rstd.dtype != torch.float32 or rstd.device != x.device or rstd.shape != (m,)
-                             or not rstd.is_contiguous()):
-        raise ValueError("rstd must be a contiguous float32 tensor [M] on x's device")
-    st = lib.dg_add_rms_norm_cast_to_fp8(
-        x.data_ptr(), _ld(x, 0, 16 // x.element_size()), res, ldr, ro, ldro, dt, weight.data_ptr(), wdt, eps,
-        q.data_ptr(), _ld(q, 0, 8), sf.data_ptr(), _ld(sf, 0, 4), ue, yp, ldy,
-        rstd.data_ptr() if rstd is not None else None, m, k, _stream(x))
-    _check(st)
+    rp = rop = yp = rstdp = None
+    ldr = ldro = ldy = 0
+    if residual is not None:
+        rp, ldr = _like(residual, dtype, dev, shape, "residual")
+        rop, ldro = _like(residual_out, dtype, dev, shape, "residual_out")
+    if y is not None:
+        yp, ldy = _like(y, dtype, dev, shape, "y")
+    if rstd is not None:
+        rstdp = _flat(rstd, torch.float32, dev, shape[:1], "rstd")
+    st = lib.dg_add_rms_norm_cast_to_fp8(xp, ldx, rp, ldr, rop, ldro, code, wp, wcode, eps, qp, ldq, sfp, ld_sf, ue, yp,
+                                         ldy, rstdp, m, k, _stream(x))
+    if st:
+        _check(st)
     return q, sf
 
 
@@ -596,22 +638,20 @@ def rms_norm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor, r
     the forward's -> dx (of x and of residual alike; dresidual, the gradient that reached
     residual_out, is added) and dw FP32 [K] (overwritten, or added to with ``accumulate``).
     dx may be dy or dresidual itself."""
-    lib = load_library()
-    if dy.dtype not in _DTYPES or not dy.is_cuda or dy.dim() != 2 or not _unit_last_stride(dy):
-        raise TypeError("dy must be a 2-D bfloat16 or float32 GPU tensor, contiguous in its last dimension")
-    m, k = dy.shape
-    wdt = _norm_weight(weight, dy)
-    for t, shape, nm in ((rstd, (m,), "rstd"), (dw, (k,), "dw")):
-        if t.dtype != torch.float32 or t.device != dy.device or t.shape != shape or not t.is_contiguous():
-            raise ValueError(f"{nm} must be a contiguous float32 tensor {list(shape)} on dy's device")
-    sp, lds = _rows(s, dy, "s")
-    dxp, lddx = _rows(dx, dy, "dx")
-    dr, lddr = _rows(dresidual, dy, "dresidual") if dresidual is not None else (None, 0)
-    ws, wsp, wsb = _scratch(workspace, lib.dg_get_rms_norm_backward_workspace_size(m, k), dy.device)
-    st = lib.dg_rms_norm_backward(dy.data_ptr(), _ld(dy, 0, 16 // dy.element_size()), sp, lds, _DTYPES[dy.dtype],
-                                  weight.data_ptr(), wdt, rstd.data_ptr(), dr, lddr, dxp, lddx, dw.data_ptr(),
-                                  bool(accumulate), m, k, wsp, wsb, _stream(dy))
-    _check(st)
+    lib = _lib or load_library()
+    dtype, dev, shape, code, dyp, lddy, wcode, wp = _norm_input(dy, weight, "dy")
+    m, k = shape
+    sp, lds = _like(s, dtype, dev, shape, "s")
+    dxp, lddx = _like(dx, dtype, dev, shape, "dx")
+    rstdp = _flat(rstd, torch.float32, dev, shape[:1], "rstd")
+    dwp = _flat(dw, torch.float32, dev, shape[1:], "dw")
+    drp, lddr = _like(dresidual, dtype, dev, shape, "dresidual") if dresidual is not None else (None, 0)
+    ws, wsp, wsb = _scratch(workspace, 0 if workspace is not None
+                            else lib.dg_get_rms_norm_backward_workspace_size(m, k), dev)
+    st = lib.dg_rms_norm_backward(dyp, lddy, sp, lds, code, wp, wcode, rstdp, drp, lddr, dxp, lddx, dwp, accumulate, m,
+                                  k, wsp, wsb, _stream(dy))
+    if st:
+        _check(st)
     return dx, dw
 
 
@@ -632,43 +672,36 @@ def fp8_moe_few_tokens(x_pair, w13_pair, w2_pair, topk_ids: torch.Tensor, topk_w
     then up rows), w2 E4M3 [E, H, I], their scales in the GEMMs' layouts (FP32, or all packed UE8M0
     int32), topk_ids int32 [M, top_k] (ids outside [0, E) add nothing), topk_weights FP32
     [M, top_k] -> out BF16 [M, H]."""
-    lib = load_library()
+    lib = _lib or load_library()
     x, sfx = x_pair
     w13, sf13 = w13_pair
     w2, sf2 = w2_pair
-    for t, nm in ((x, "x"), (w13, "w13"), (w2, "w2")):
-        _fp8(t, nm)
-    ue = _sf(sfx, sf13)
-    if _sf(sfx, sf2) != ue:
-        raise TypeError("all scales must be float32, or all int32 (packed UE8M0)")
-    for t, nm in ((w13, "w13"), (w2, "w2"), (sf13, "sf13"), (sf2, "sf2"), (topk_ids, "topk_ids"),
-                  (topk_weights, "topk_weights")):
-        _dense_contig(t, nm)
-    if topk_ids.dtype != torch.int32 or topk_weights.dtype != torch.float32:
-        raise TypeError("topk_ids must be int32 and topk_weights float32")
-    if out.dtype != torch.bfloat16 or not _unit_last_stride(out):
-        raise TypeError("out must be a bfloat16 tensor, contiguous in its last dimension")
-    for t in (x, sfx, w13, sf13, w2, sf2, topk_ids, topk_weights):
-        if t.device != out.device:
-            raise ValueError("all operands must be on out's device")
-    m, h = x.shape
-    e, i2, _ = w13.shape
-    i = i2 // 2
-    top_k = topk_ids.shape[1]
-    if w13.shape != (e, 2 * i, h) or w2.shape != (e, h, i) or topk_ids.shape != (m, top_k) \
-            or topk_weights.shape != (m, top_k) or out.shape != (m, h):
-        raise ValueError(f"shape mismatch: x {tuple(x.shape)}, w13 {tuple(w13.shape)}, w2 {tuple(w2.shape)}, "
-                         f"topk_ids {tuple(topk_ids.shape)}, out {tuple(out.shape)}")
-    rows = _sf_rows(h, ue)
-    if sfx.dim() != 2 or sfx.shape[0] != rows or sfx.shape[1] < m or sf13.shape != (e, 2 * i // 128, rows) \
-            or sf2.shape != (e, h // 128, _sf_rows(i, ue)):
-        raise ValueError("scale shape mismatch")
-    ws, wsp, wsb = _scratch(workspace, lib.dg_get_moe_workspace_size(m, top_k, i), out.device)
+    dev = out.get_device()
+    if dev < 0 or x.dim() != 2 or w13.dim() != 3 or topk_ids.dim() != 2:
+        raise ValueError("x, topk_ids and out must be 2-D and the weights 3-D GPU tensors")
+    shape = x.shape
+    m, h = shape
+    e, i, top_k = w13.shape[0], w13.shape[1] // 2, topk_ids.shape[1]
+    xp, ldx = _codes(x, dev, shape, "x", 16)
+    ue, sfxp, ld_sfx = _row_scales(sfx, dev, m, h, "sfx")
+    sft = torch.int32 if ue else torch.float32
+    for t, nm in ((w13, "w13"), (w2, "w2")):
+        if t.dtype is not torch.float8_e4m3fn and t.dtype is not torch.uint8:
+            raise TypeError(f"{nm} must be torch.float8_e4m3fn or uint8 codes, got {t.dtype}")
+    if out.dtype is not torch.bfloat16:
+        raise TypeError("out must be a bfloat16 tensor")
+    w13p = _flat(w13, w13.dtype, dev, (e, 2 * i, h), "w13")
+    sf13p = _flat(sf13, sft, dev, (e, 2 * i // 128, _sf_rows(h, ue)), "sf13")
+    w2p = _flat(w2, w2.dtype, dev, (e, h, i), "w2")
+    sf2p = _flat(sf2, sft, dev, (e, h // 128, _sf_rows(i, ue)), "sf2")
+    idp = _flat(topk_ids, torch.int32, dev, (m, top_k), "topk_ids")
+    twp = _flat(topk_weights, torch.float32, dev, (m, top_k), "topk_weights")
+    op, ldo = _like(out, torch.bfloat16, dev, shape, "out")
+    ws, wsp, wsb = _scratch(workspace, 0 if workspace is not None else lib.dg_get_moe_workspace_size(m, top_k, i), dev)
     fn = lib.dg_fp8_moe_few_tokens_ue8m0 if ue else lib.dg_fp8_moe_few_tokens
-    st = fn(x.data_ptr(), _ld(x, 0, 16), sfx.data_ptr(), _ld(sfx, 0, 4), w13.data_ptr(), sf13.data_ptr(),
-            w2.data_ptr(), sf2.data_ptr(), topk_ids.data_ptr(), topk_weights.data_ptr(), out.data_ptr(),
-            _ld(out, 0, 8), m, top_k, e, h, i, wsp, wsb, _stream(out))
-    _check(st)
+    st = fn(xp, ldx, sfxp, ld_sfx, w13p, sf13p, w2p, sf2p, idp, twp, op, ldo, m, top_k, e, h, i, wsp, wsb, _stream(out))
+    if st:
+        _check(st)
     return out
 
 
@@ -683,12 +716,12 @@ class TensorList:
 
     def __init__(self, tensors):
         self.tensors = list(tensors)
-        self.device = self.tensors[0].device if self.tensors else None
+        self.dev = self.tensors[0].get_device() if self.tensors else -1
         self.table = (_Tensor * max(1, len(self.tensors)))()
         for d, t in zip(self.table, self.tensors):
             if t.dtype not in _DTYPES or not t.is_cuda:
                 raise TypeError("tensors must be bfloat16 or float32 GPU tensors")
-            if t.device != self.device or not t.is_contiguous():
+            if t.get_device() != self.dev or not t.is_contiguous():
                 raise ValueError("tensors must be contiguous and on one device")
             d.data, d.numel, d.dtype = t.data_ptr(), t.numel(), _DTYPES[t.dtype]
 
@@ -710,20 +743,24 @@ def alloc_clip_workspace(device=None) -> torch.Tensor:
 def clip_grad_norm(grads, max_norm: float, norm: torch.Tensor, out=None, workspace: torch.Tensor | None = None):
     """norm[0] = sqrt(sum of all squares) and out = grads * min(1, max_norm / (norm + 1e-6)); without
     ``out`` in place.  grads and out: lists of tensors, or a ``TensorList`` kept between calls."""
-    lib = load_library()
+    lib = _lib or load_library()
     grads = grads if isinstance(grads, TensorList) else TensorList(grads)
-    if norm.dtype != torch.float32 or not norm.is_cuda or norm.numel() != 1:
+    dev = norm.get_device()
+    if norm.dtype is not torch.float32 or dev < 0 or norm.numel() != 1:
         raise TypeError("norm must be a float32 GPU tensor with one element")
-    if len(grads) and grads.device != norm.device:
+    n = len(grads.tensors)
+    if n and grads.dev != dev:
         raise ValueError("grads must be on norm's device")
+    table = None
     if out is not None:
         out = out if isinstance(out, TensorList) else TensorList(out)
-        if len(out) != len(grads) or (len(out) and out.device != norm.device):
+        if len(out.tensors) != n or (n and out.dev != dev):
             raise ValueError("out must have as many tensors as grads, on norm's device")
-    ws, wsp, wsb = _scratch(workspace, lib.dg_get_clip_workspace_size(), norm.device)
-    st = lib.dg_clip_grad_norm(grads.table, out.table if out is not None else None, len(grads), max_norm,
-                               norm.data_ptr(), wsp, wsb, _stream(norm))
-    _check(st)
+        table = out.table
+    ws, wsp, wsb = _scratch(workspace, 0 if workspace is not None else lib.dg_get_clip_workspace_size(), dev)
+    st = lib.dg_clip_grad_norm(grads.table, table, n, max_norm, norm.data_ptr(), wsp, wsb, _stream(norm))
+    if st:
+        _check(st)
     return norm
 
 

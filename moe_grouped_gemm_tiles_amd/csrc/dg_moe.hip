@@ -623,7 +623,7 @@ void launch_down(Params p, int chunks, int pairs, hipStream_t stream) {
 
 template <bool UE8M0>
 void launch(const Params& p, int chunks, int pairs, hipStream_t stream) {
-  const int cus = dg_get_num_cus() > 0 ? dg_get_num_cus() : 256;
+  const int usable = dg_get_num_cus(), cus = usable > 0 ? usable : 256;
   const int64_t units = (int64_t)std::min(pairs, p.experts) * (p.inter / 16);
   const auto grid = [&](int per_cu) { return dim3((unsigned)std::min<int64_t>(units, (int64_t)cus * per_cu), chunks); };
   // Tokens of an expert per pass: no more than 16 can come where there are no more tokens;

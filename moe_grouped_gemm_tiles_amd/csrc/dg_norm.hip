@@ -507,8 +507,9 @@ Shape shape_for(int k) {
 // million rows with 8, 427 us with 1) and for the longest, whose workgroups fill a CU
 // alone and need the prefetch (14560 x 16384: 298 us with 4, 318 us with 1).
 int fwd_rows(int m, int k) {
-  const int rows = k > 8192 ? 4 : k > 4096 ? 1 : k > 512 ? 2 : 8;
-  return std::max(1, std::min(rows, m / 2048));
+  int rows = std::max(1, std::min(k > 8192 ? 4 : k > 4096 ? 1 : k > 512 ? 2 : 8, m / 2048));
+  while (m / rows > 1 << 22) rows *= 2;  // (a launch holds fewer than 2^32 threads)
+  return rows;
 }
 
 // Workgroups of the backward's row loop, each of which leaves a row of partial sums:
