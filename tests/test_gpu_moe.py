@@ -76,6 +76,36 @@ def test_moe_shapes(m, experts, top_k, hidden, inter, routed, fmt):
     _check(x, _run(x), what=f"m={m} E={experts} top_k={top_k} H={hidden} I={inter} {fmt}")
 
 
+@pytest.mark.parametrize("cus", [0, 64, 8])
+@pytest.mark.parametrize("fmt", ["fp32", "ue8m0"])
+@pytest.mark.parametrize("m,experts", [(3, 1), (7, 1), (15, 1), (20, 1), (30, 1), (45, 1), (70, 1), (24, 3)])
+def test_moe_tile_forms(m, experts, fmt, cus):
+    """Every number of output columns per workgroup (fewer usable CUs: wider tiles, more units per
+    workgroup) with every amount of tokens per stage, up to several passes."""
+    x = gen_moe(m, experts, 1, 1024, 384, seed=510 + m, scale_fmt=fmt)
+    dg.set_num_cus(cus)
+    try:
+        _check(x, _run(x), what=f"m={m} E={experts} {fmt} cus={cus}")
+    finally:
+        dg.set_num_cus(0)
+
+
+@pytest.mark.parametrize("m,experts,top_k", [(40, 2, 1), (17, 3, 3), (128, 2, 2)])
+def test_moe_widest_rows(m, experts, top_k):
+    x = gen_moe(m, experts, top_k, 7168, 128, seed=515 + m, scale_fmt="ue8m0" if m == 17 else "fp32")
+    _check(x, _run(x), what=f"m={m} H=7168 I=128")
+
+
+def test_moe_full_chunk_with_wide_tiles():
+    """512 pairs of one expert in 32-column tiles: the sums take the most LDS, the rings the least."""
+    x = gen_moe(512, 1, 1, 512, 256, seed=518)
+    dg.set_num_cus(4)
+    try:
+        _check(x, _run(x), what="512 pairs, 32 columns")
+    finally:
+        dg.set_num_cus(0)
+
+
 def test_moe_larger_than_one_chunk_of_pairs():
     """More than 512 (token, slot) pairs: several chunks, the last with one token."""
     x = gen_moe(2 * 128 + 1, 5, 4, 256, 128, seed=520)

@@ -140,6 +140,32 @@ def test_norm_many_rows(m, dtype):
         _check(_run(x, w, dtype, True, None), dtype, True, what=f"{m}x{k} {dtype} ue8m0, no residual")
 
 
+@pytest.mark.parametrize("m,k,dtype", [(8300, 8320, "bf16"), (20001, 256, "bf16"), (4200, 1152, "fp32"), (4100, 4224, "bf16")])
+def test_norm_rows_per_workgroup(m, k, dtype):
+    """Several rows per workgroup (with a shorter last one) and one, streaming operands; rows sampled."""
+    gen = torch.Generator(device="cuda:0").manual_seed(m)
+    x, res = (torch.randn(m, k, device="cuda:0", generator=gen).to(DT[dtype]) for _ in range(2))
+    w = (1 + 0.2 * torch.randn(k, device="cuda:0", generator=gen)).to(DT[dtype])
+    o = dict(x=x, w=w, res=res, res_out=_filled(m, k, dtype), y=_filled(m, k, dtype),
+             q=torch.full((m, k), 0xAA, dtype=torch.uint8, device="cuda:0"),
+             sf=torch.full((k // 128, (m + 3) // 4 * 4), -7.0, device="cuda:0"), rstd=torch.full((m,), -1.0, device="cuda:0"))
+    dg.add_rms_norm_cast_to_fp8(x, w, 1e-6, o["q"], o["sf"], residual=res, residual_out=o["res_out"], y=o["y"], rstd=o["rstd"])
+    rows = torch.cat([torch.arange(40), torch.arange(m // 2, m // 2 + 40), torch.arange(m - 40, m)]).to("cuda:0")
+    part = {n: t[rows] if n not in ("w", "sf") else t for n, t in o.items()}
+    part["sf"] = o["sf"][:, rows]
+    _check(part, dtype, False, what=f"{m}x{k} {dtype}")
+    assert torch.equal(o["res_out"], (x.float() + res.float()).to(DT[dtype]))
+    g = dict(dy=x, s=o["res_out"], w=w, rstd=o["rstd"], dres=res, dx=_filled(m, k, dtype), dw=torch.empty(k, device="cuda:0"))
+    dg.rms_norm_backward(g["dy"], g["s"], w, g["rstd"], g["dx"], g["dw"], dresidual=res)
+    part = {n: t[rows] if n not in ("w", "dw") else t for n, t in g.items()}
+    dx, _, terms, _ = oracle.ref_rms_norm_backward(*(_f64(part[n]) for n in ("dy", "s", "w", "rstd", "dres")))
+    bound = 2.0 ** -16 * terms
+    bound = bound + (2.0 ** -8 * (np.abs(dx) + bound) if dtype == "bf16" else 0) + 1e-37
+    assert (np.abs(_f64(part["dx"]) - dx) <= bound).all()
+    t = g["dy"].double() * g["s"].double() * g["rstd"].double()[:, None]
+    assert bool(((g["dw"].double() - t.sum(0)).abs() <= 2.0 ** -16 * t.abs().sum(0)).all())
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_norm_strides_weight_types_and_no_residual(dtype):
     x, w, res = _inputs(19, 896, 320, dtype)
