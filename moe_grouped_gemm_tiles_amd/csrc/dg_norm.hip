@@ -291,7 +291,15 @@ __global__ void __launch_bounds__(kMaxThreads) fwd_kernel(const FwdParams p) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 63;
   const int chunks = p.k >> 3;
   const uint32_t bytes = (uint32_t)p.k * ES, res_bytes = p.res != nullptr ? bytes : 0;
-  const int row0 = blockIdx.x * p.rows_per_wg;
+  // Workgroups go to the eight XCDs in turn.  Each XCD takes runs of 32 adjacent rows, so that
+  // the scales of a run, one 128-byte line per K block, meet in its L2 and are written once.
+  const int run = max(1, 32 / p.rows_per_wg), whole = (int)gridDim.x / (8 * run) * (8 * run);
+  int wg = blockIdx.x;
+  if (wg < whole) {
+    const int slot = wg >> 3;
+    wg = (slot / run * 8 + (wg & 7)) * run + slot % run;
+  }
+  const int row0 = wg * p.rows_per_wg;
   const int row1 = min(row0 + p.rows_per_wg, p.m);
   if (tid < 4 * kSlots) (&s_sum[0][0][0])[tid] = 0.f;
   float w[C][8];
@@ -462,30 +470,37 @@ bwd_kernel(const BwdParams p) {
   for (int c = 0; c < C; ++c) store8_fp32<BF16, false>(rp, c * nt + tid, dw[c]);
 }
 
-constexpr int kDwCols = 32;  // columns of one workgroup of the column sum
-constexpr int kDwRows = 128;  // rows it takes at a time
+constexpr int kDwCols = 32;   // columns of one workgroup of the column sum
+constexpr int kDwWaves = 16;  // its waves; eight lanes take 32 columns of a row, a wave eight rows
 
-// dw[col] (+)= sum over rows of part[row][col]: eight lanes take 32 columns of a
-// row, and the sums of the 128 row classes are added in a fixed order.
-__global__ void __launch_bounds__(kDwRows * 8) dw_kernel(const float* part, int rows, int k, float* dw,
-                                                         int accumulate) {
-  __shared__ float t[kDwRows][kDwCols];
-  const int tid = threadIdx.x, r = tid >> 3, c4 = (tid & 7) * 4;
-  const int col = blockIdx.x * kDwCols + c4;
+// Sum of v over the lanes l, l + 8, l + 16, ... of the wave.
+__device__ __forceinline__ float sum_every8(float v) {
+  v += dpp<0x128>(v);  // rotated by eight in each 16 lanes
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// dw[col] (+)= sum over rows of part[row][col], in a fixed order.
+__global__ void __launch_bounds__(kDwWaves * 64) dw_kernel(const float* part, int rows, int k, float* dw,
+                                                           int accumulate) {
+  __shared__ float t[kDwWaves][kDwCols];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int c4 = (tid & 7) * 4, col = blockIdx.x * kDwCols + c4;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = r; i < rows; i += kDwRows) {
+  for (int i = tid >> 3; i < rows; i += kDwWaves * 8) {
     const float4 v = *reinterpret_cast<const float4*>(part + (int64_t)i * k + col);
     a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
   }
-  *reinterpret_cast<float4*>(&t[r][c4]) = a;
+  a = make_float4(sum_every8(a.x), sum_every8(a.y), sum_every8(a.z), sum_every8(a.w));
+  if (lane < 8) *reinterpret_cast<float4*>(&t[wave][c4]) = a;
   __syncthreads();
-  // 32 threads per column, four classes each, then across them
-  const int c = tid >> 5, g = tid & 31;
-  float sum = (t[g][c] + t[g + 32][c]) + (t[g + 64][c] + t[g + 96][c]);
+  if (tid < kDwCols) {
+    float sum = 0.f;
 #pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 32);
-  if (g == 0) {
-    float* o = dw + blockIdx.x * kDwCols + c;
+    for (int w = 0; w < kDwWaves; ++w) sum += t[w][tid];
+    float* o = dw + blockIdx.x * kDwCols + tid;
     *o = accumulate ? *o + sum : sum;
   }
 }
@@ -648,7 +663,7 @@ dg_status dg_rms_norm_backward(const void* dy, int64_t ld_dy, const void* s, int
     const dg_status st = launch_status();
     if (st != DG_SUCCESS) return st;
   }
-  hipLaunchKernelGGL(dw_kernel, dim3(k / kDwCols), dim3(kDwRows * 8), 0, stream, static_cast<const float*>(workspace), grid, k,
+  hipLaunchKernelGGL(dw_kernel, dim3(k / kDwCols), dim3(kDwWaves * 64), 0, stream, static_cast<const float*>(workspace), grid, k,
                      dw, accumulate_dw != 0);
   return launch_status();
 }
