@@ -58,10 +58,12 @@ class ExpertLayer:
 
     def __call__(self, x, residual):
         """Adds x to the residual stream (in place) and returns the layer's output."""
-        dg.add_rms_norm_cast_to_fp8(x, self.weight, 1e-6, self.q, self.sf, residual=residual, residual_out=residual, y=self.y)
+        dg.add_rms_norm_cast_to_fp8(x, self.weight, 1e-6, self.q, self.sf, residual=residual, residual_out=residual,
+                                    y=self.y)
         top, ids = torch.topk(self.y @ self.router.t(), self.top_k, dim=1)
         weights = torch.softmax(top.float(), dim=1)
-        return dg.fp8_moe_few_tokens((self.q, self.sf), self.w13, self.w2, ids.int(), weights, self.out, workspace=self.workspace)
+        return dg.fp8_moe_few_tokens((self.q, self.sf), self.w13, self.w2, ids.int(), weights, self.out,
+                                     workspace=self.workspace)
 
 
 def serve(tokens=4, hidden=2048, inter=1024, experts=16, top_k=4, layers=3, steps=8, dev="cuda:0"):

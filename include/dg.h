@@ -387,7 +387,7 @@ size_t dg_get_rms_norm_backward_workspace_size(int m, int k);
  * w2            E4M3 [num_experts, hidden, inter] contiguous.
  * sf2           FP32 [num_experts][hidden/128][inter/128] contiguous.
  * topk_ids      DEVICE int32 [m, top_k] contiguous; an id outside [0, num_experts)
- *               is no expert of this device and adds nothing (its weight is not read).
+ *               is no expert of this device and adds nothing, whatever its weight.
  * topk_weights  FP32 [m, top_k] contiguous.
  * out           BF16 [m, hidden], row stride ld_out (a multiple of 8), 16-B aligned.
  *               Every row is written; a token without an expert here gets zeros.

@@ -185,7 +185,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, ui
 // The same from an address that is the same on every lane: into scalar registers, which the asm below needs.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const void* base, uint32_t bytes) {
   const uint64_t a = reinterpret_cast<uint64_t>(base);
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a), hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
   return make_rsrc(reinterpret_cast<const void*>(((uint64_t)hi << 32) | lo), __builtin_amdgcn_readfirstlane(bytes));
 }
 constexpr uint32_t kNowhere = 0x80000000u;  // an offset past every operand here: the load gives zeros
@@ -203,14 +204,14 @@ constexpr uint32_t kNowhere = 0x80000000u;  // an offset past every operand here
 template <int BYTES, bool NT>
 __device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t r, uint32_t lds, uint32_t off) {
   if constexpr (BYTES == 16 && NT)
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen nt lds" : : "v"(off), "s"(r), "s"(lds)
-                 : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen nt lds"
+                 : : "v"(off), "s"(r), "s"(lds) : "memory", "m0");
   else if constexpr (BYTES == 16)
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" : : "v"(off), "s"(r), "s"(lds)
-                 : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+                 : : "v"(off), "s"(r), "s"(lds) : "memory", "m0");
   else
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tbuffer_load_dword %0, %1, 0 offen lds" : : "v"(off), "s"(r), "s"(lds)
-                 : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tbuffer_load_dword %0, %1, 0 offen lds"
+                 : : "v"(off), "s"(r), "s"(lds) : "memory", "m0");
 }
 template <int N>
 __device__ __forceinline__ void wait_loads() {
@@ -277,7 +278,8 @@ __global__ void __launch_bounds__(kUpWaves * 64) gate_up_kernel(const Params p) 
   const int wave = uniform(tid >> 6);
   const int t0 = blockIdx.y * p.tokens;
   const int tokens = min(p.tokens, p.m - t0);
-  make_plan<kUpWaves * 64>(p, t0, tokens * p.top_k, plan, reinterpret_cast<int16_t*>(ring), reinterpret_cast<uint32_t*>(red));
+  make_plan<kUpWaves * 64>(p, t0, tokens * p.top_k, plan, reinterpret_cast<int16_t*>(ring),
+                           reinterpret_cast<uint32_t*>(red));
   const int tiles = p.inter >> 4, nkb = p.hidden >> 7, nb = p.inter >> 7, nw = words<UE8M0>(nkb);
   const int rounds = (nkb + kUpWaves - 1) / kUpWaves;
   const int units = uniform(plan.touched) * tiles;
@@ -288,7 +290,8 @@ __global__ void __launch_bounds__(kUpWaves * 64) gate_up_kernel(const Params p) 
 
   uint8_t* my_ring = ring + wave * D * S::kBytes;
   const uint32_t my_lds = (uint32_t)uniform((int)(uintptr_t)(lds_ptr_t)my_ring);
-  const __amdgpu_buffer_rsrc_t rx = uniform_rsrc(p.x + (int64_t)t0 * p.ldx, (uint32_t)((tokens - 1) * p.ldx + p.hidden));
+  const __amdgpu_buffer_rsrc_t rx =
+      uniform_rsrc(p.x + (int64_t)t0 * p.ldx, (uint32_t)((tokens - 1) * p.ldx + p.hidden));
   const __amdgpu_buffer_rsrc_t rsx =
       uniform_rsrc(static_cast<const uint32_t*>(p.sfx) + t0, (uint32_t)(((nw - 1) * p.ld_sfx + tokens) * 4));
   const uint32_t w_off = (uint32_t)(lane >> 3) * p.hidden + tile_chunk(lane);
@@ -330,7 +333,8 @@ __global__ void __launch_bounds__(kUpWaves * 64) gate_up_kernel(const Params p) 
 #pragma unroll
       for (int h = 0; h < 2; ++h) to_lds<16, false>(rx, lds + S::kX + 2048 * g + 1024 * h, x_off[g][h] + k);
     const uint32_t wd = kb < nkb ? (uint32_t)word_of<UE8M0>(kb) : kNowhere;
-    to_lds<4, false>(rsx, lds + S::kSx, kb < nkb && sx_off != kNowhere ? sx_off + wd * (uint32_t)p.ld_sfx * 4 : kNowhere);
+    to_lds<4, false>(rsx, lds + S::kSx,
+                     kb < nkb && sx_off != kNowhere ? sx_off + wd * (uint32_t)p.ld_sfx * 4 : kNowhere);
     to_lds<4, false>(rsw, lds + S::kSw, kb < nkb && lane < 2 ? (lane * nb * nw + wd) * 4 : kNowhere);
     slot = slot + 1 == D ? 0 : slot + 1;
     if (++lit < rounds) return;
@@ -460,7 +464,9 @@ __device__ __forceinline__ void down_stream(const Params& p, const Plan& plan, c
 #pragma unroll
     for (int h = 0; h < AL; ++h) {
       const int row = 4 * h + (lane >> 4), c = lg0 + row;
-      a_off[h] = c < ln ? (uint32_t)pair_of(p, plan.order[first + c]) * (uint32_t)p.inter * 2 + (((lane ^ row) & 15) << 4) : kNowhere;
+      a_off[h] = c < ln ? (uint32_t)pair_of(p, plan.order[first + c]) * (uint32_t)p.inter * 2 +
+                              (((lane ^ row) & 15) << 4)
+                        : kNowhere;
     }
   };
   auto load = [&]() __attribute__((always_inline)) {
@@ -657,7 +663,8 @@ dg_status run(const void* x, int64_t ldx, const void* sfx, int64_t ld_sfx, const
   // offsets inside a chunk of tokens are 32-bit
   const int64_t chunk_tokens = std::min(m, kPairs / top_k);
   if (chunk_tokens * ldx >= kNowhere || (int64_t)(hidden / 128) * ld_sfx * 4 >= kNowhere ||
-      (int64_t)32 * hidden >= kNowhere || (int64_t)kPairs * inter * 2 >= kNowhere)
+      (int64_t)32 * hidden >= kNowhere || (int64_t)kPairs * inter * 2 >= kNowhere ||
+      ((int64_t)inter / 128 + 1) * (hidden / 128) * 4 >= kNowhere)
     return DG_ERROR_NOT_SUPPORTED;
   if (workspace == nullptr || !aligned_to(workspace, 256) ||
       workspace_bytes < dg_get_moe_workspace_size(m, top_k, inter))

@@ -86,7 +86,8 @@ __device__ __forceinline__ void load_row(__amdgpu_buffer_rsrc_t r, int tid, int 
   for (int c = 0; c < C; ++c)
 #pragma unroll
     for (int h = 0; h < (BF16 ? 1 : 2); ++h)
-      o.d[c][h] = __builtin_amdgcn_raw_buffer_load_b128(r, place<BF16>(c * nt + tid, h) * (BF16 ? 2 : 4), 0, kPolicy<NT>);
+      o.d[c][h] =
+          __builtin_amdgcn_raw_buffer_load_b128(r, place<BF16>(c * nt + tid, h) * (BF16 ? 2 : 4), 0, kPolicy<NT>);
 }
 
 template <bool BF16, int C>
@@ -375,9 +376,8 @@ __global__ void __launch_bounds__(kMaxThreads) fwd_kernel(const FwdParams p) {
         __builtin_amdgcn_raw_buffer_store_b32(
             word, rs, lane == 0 && ch < chunks ? (uint32_t)(ch >> 6) * (uint32_t)p.ld_sf : kNowhere, 0, 0);
       } else {
-        __builtin_amdgcn_raw_buffer_store_b32(
-            __float_as_uint(s), rs, (lane & 15) == 0 && ch < chunks ? (uint32_t)(ch >> 4) * (uint32_t)p.ld_sf : kNowhere,
-            0, 0);
+        const uint32_t at = (lane & 15) == 0 && ch < chunks ? (uint32_t)(ch >> 4) * (uint32_t)p.ld_sf : kNowhere;
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(s), rs, at, 0, 0);
       }
     }
   }
@@ -610,8 +610,8 @@ dg_status dg_add_rms_norm_cast_to_fp8(const void* x, int64_t ldx, const void* re
   if (!aligned_to(rstd, 4)) return DG_ERROR_INVALID_VALUE;
   FwdParams p{static_cast<const uint8_t*>(x), static_cast<const uint8_t*>(residual),
               static_cast<uint8_t*>(residual_out), static_cast<const uint8_t*>(weight), static_cast<uint8_t*>(q),
-              static_cast<uint8_t*>(sf), static_cast<uint8_t*>(y), rstd, ldx * es, ld_residual * es, ld_residual_out * es, ldq, ld_sf * 4,
-              ldy * es, eps, m, k, fwd_rows(m, k), weight_dtype == DG_DTYPE_BF16};
+              static_cast<uint8_t*>(sf), static_cast<uint8_t*>(y), rstd, ldx * es, ld_residual * es,
+              ld_residual_out * es, ldq, ld_sf * 4, ldy * es, eps, m, k, fwd_rows(m, k), weight_dtype == DG_DTYPE_BF16};
   const Shape s = shape_for(k);
   const bool nt = streams((int64_t)m * k * (es * (residual != nullptr ? 3 : 1) + 1));
   const dim3 grid((m + p.rows_per_wg - 1) / p.rows_per_wg);
@@ -663,8 +663,8 @@ dg_status dg_rms_norm_backward(const void* dy, int64_t ld_dy, const void* s, int
     const dg_status st = launch_status();
     if (st != DG_SUCCESS) return st;
   }
-  hipLaunchKernelGGL(dw_kernel, dim3(k / kDwCols), dim3(kDwWaves * 64), 0, stream, static_cast<const float*>(workspace), grid, k,
-                     dw, accumulate_dw != 0);
+  hipLaunchKernelGGL(dw_kernel, dim3(k / kDwCols), dim3(kDwWaves * 64), 0, stream,
+                     static_cast<const float*>(workspace), grid, k, dw, accumulate_dw != 0);
   return launch_status();
 }
 

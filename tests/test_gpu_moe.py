@@ -34,7 +34,8 @@ def _dev(x):
 def _run(x, ld=None, workspace=None):
     d = _dev(x)
     h = x["hidden"]
-    out = torch.full((x["m"], h if ld is None else ld), SENT_BF16, dtype=torch.int16, device="cuda:0").view(torch.bfloat16)
+    out = torch.full((x["m"], h if ld is None else ld), SENT_BF16, dtype=torch.int16, device="cuda:0")
+    out = out.view(torch.bfloat16)
     dg.fp8_moe_few_tokens(d["x"], d["w13"], d["w2"], d["ids"], d["weights"], out[:, :h], workspace=workspace)
     torch.cuda.synchronize()
     assert (out[:, h:].contiguous().view(torch.int16) == SENT_BF16).all(), "columns past hidden were written"

@@ -140,7 +140,8 @@ def test_norm_many_rows(m, dtype):
         _check(_run(x, w, dtype, True, None), dtype, True, what=f"{m}x{k} {dtype} ue8m0, no residual")
 
 
-@pytest.mark.parametrize("m,k,dtype", [(8300, 8320, "bf16"), (20001, 256, "bf16"), (4200, 1152, "fp32"), (4100, 4224, "bf16")])
+@pytest.mark.parametrize("m,k,dtype", [(8300, 8320, "bf16"), (20001, 256, "bf16"), (4200, 1152, "fp32"),
+                                       (4100, 4224, "bf16")])
 def test_norm_rows_per_workgroup(m, k, dtype):
     """Several rows per workgroup (with a shorter last one) and one, streaming operands; rows sampled."""
     gen = torch.Generator(device="cuda:0").manual_seed(m)
@@ -148,14 +149,17 @@ def test_norm_rows_per_workgroup(m, k, dtype):
     w = (1 + 0.2 * torch.randn(k, device="cuda:0", generator=gen)).to(DT[dtype])
     o = dict(x=x, w=w, res=res, res_out=_filled(m, k, dtype), y=_filled(m, k, dtype),
              q=torch.full((m, k), 0xAA, dtype=torch.uint8, device="cuda:0"),
-             sf=torch.full((k // 128, (m + 3) // 4 * 4), -7.0, device="cuda:0"), rstd=torch.full((m,), -1.0, device="cuda:0"))
-    dg.add_rms_norm_cast_to_fp8(x, w, 1e-6, o["q"], o["sf"], residual=res, residual_out=o["res_out"], y=o["y"], rstd=o["rstd"])
+             sf=torch.full((k // 128, (m + 3) // 4 * 4), -7.0, device="cuda:0"),
+             rstd=torch.full((m,), -1.0, device="cuda:0"))
+    dg.add_rms_norm_cast_to_fp8(x, w, 1e-6, o["q"], o["sf"], residual=res, residual_out=o["res_out"], y=o["y"],
+                                rstd=o["rstd"])
     rows = torch.cat([torch.arange(40), torch.arange(m // 2, m // 2 + 40), torch.arange(m - 40, m)]).to("cuda:0")
     part = {n: t[rows] if n not in ("w", "sf") else t for n, t in o.items()}
     part["sf"] = o["sf"][:, rows]
     _check(part, dtype, False, what=f"{m}x{k} {dtype}")
     assert torch.equal(o["res_out"], (x.float() + res.float()).to(DT[dtype]))
-    g = dict(dy=x, s=o["res_out"], w=w, rstd=o["rstd"], dres=res, dx=_filled(m, k, dtype), dw=torch.empty(k, device="cuda:0"))
+    g = dict(dy=x, s=o["res_out"], w=w, rstd=o["rstd"], dres=res, dx=_filled(m, k, dtype),
+             dw=torch.empty(k, device="cuda:0"))
     dg.rms_norm_backward(g["dy"], g["s"], w, g["rstd"], g["dx"], g["dw"], dresidual=res)
     part = {n: t[rows] if n not in ("w", "dw") else t for n, t in g.items()}
     dx, _, terms, _ = oracle.ref_rms_norm_backward(*(_f64(part[n]) for n in ("dy", "s", "w", "rstd", "dres")))
@@ -181,7 +185,8 @@ def test_norm_residual_in_place(dtype):
     for alias in ("residual", "x"):
         xd, rd = base["x"].clone(), base["res"].clone()
         q, sf = torch.empty_like(base["q"]), torch.zeros(11, 12, device="cuda:0")
-        dg.add_rms_norm_cast_to_fp8(xd, base["w"], 1e-6, q, sf, residual=rd, residual_out=rd if alias == "residual" else xd)
+        dg.add_rms_norm_cast_to_fp8(xd, base["w"], 1e-6, q, sf, residual=rd,
+                                    residual_out=rd if alias == "residual" else xd)
         assert torch.equal(rd if alias == "residual" else xd, base["res_out"])
         assert torch.equal(q, base["q"]) and torch.equal(sf[:, :9], base["sf"])
 
@@ -231,8 +236,8 @@ def _run_backward(dy, s, w, rstd, dtype, dres=None, pad=0, wdtype=None, dw0=None
         d.copy_(to_dev(t.astype(np.float32)))
         return d
 
-    o = dict(dy=up(dy), s=up(s), w=to_dev(w.astype(np.float32)).to(DT[wdtype or dtype]), rstd=to_dev(rstd.astype(np.float32)),
-             dres=up(dres) if dres is not None else None, dx=_filled(m, k, dtype, k + pad),
+    o = dict(dy=up(dy), s=up(s), w=to_dev(w.astype(np.float32)).to(DT[wdtype or dtype]),
+             rstd=to_dev(rstd.astype(np.float32)), dres=up(dres) if dres is not None else None, dx=_filled(m, k, dtype, k + pad),
              dw=torch.full((k,), float("nan"), device="cuda:0") if dw0 is None else to_dev(dw0.astype(np.float32)))
     ws = dg.alloc_rms_norm_backward_workspace(m, k) if workspace else None
     if ws is not None:
