@@ -165,3 +165,21 @@ def test_clip_large():
         ref = g.double() / (want + 1e-6)
         assert bool(((o.double() - ref).abs() <= 2.0 ** -21 * ref.abs()).all())
     note(f"norm {float(norm)}")
+
+
+def test_clip_large_with_empty_tensors_at_the_end():
+    """More tensors than one launch takes, the last ones without elements but with addresses."""
+    gen = torch.Generator(device="cuda:0").manual_seed(770)
+    data = torch.randn(10_000_000, device="cuda:0", generator=gen)
+    lists = []
+    for t in (data, torch.empty_like(data)):
+        tensors = dg.tensor_list([t] + [t[:0]] * 140)
+        for i in range(1, 141):
+            tensors.table[i].data = t.data_ptr()
+        lists.append(tensors)
+    norm = _norm()
+    dg.clip_grad_norm(lists[0], 1.0, norm, out=lists[1])
+    want = math.sqrt(float(data.double().square().sum()))
+    assert abs(float(norm) - want) <= 2.0 ** -22 * want
+    ref = data.double() / (want + 1e-6)
+    assert bool(((lists[1].tensors[0].double() - ref).abs() <= 2.0 ** -21 * ref.abs()).all())
