@@ -11,7 +11,8 @@
 // once from HBM, and everything else is arranged around that.
 //
 //   * gate/up kernel: a workgroup takes 16 gate and the matching 16 up rows of a
-//     touched expert at a time (a unit), its four waves split K, and one
+//     touched expert at a time (a unit; 32 and 32 with 17 to 32 tokens, whose tiles are
+//     then read half as often: 64 tokens 76 us, 83 us), its four waves split K, and one
 //     v_mfma_f32_16x16x128_f8f6f4 covers 16 rows, 16 tokens and one 128-K scale
 //     block.  The waves' partial sums meet in LDS and a is written once per (token,
 //     slot) in BF16.  (The second product then takes BF16; the composed path would
@@ -35,10 +36,10 @@
 //
 // Measured (both kernels, weights not in any cache; reads alone reach 7.0 TB/s):
 //     1 token, 8 of 16 experts of 7168 x 2048       63 us   5.6 TB/s (36 + 22 us of kernels)
-//     9 tokens, top 8 of 64 experts of 4096 x 1024  98 us   5.8 TB/s
-//     64 tokens, top 4 of 16 experts of 7168 x 2048 142 us  4.9 TB/s (a's tiles fill the down
+//     9 tokens, top 8 of 64 experts of 4096 x 1024  97 us   5.8 TB/s
+//     64 tokens, top 4 of 16 experts of 7168 x 2048 133 us  5.3 TB/s (a's tiles fill the down
 //                                                   kernel's rings: fewer stages in flight)
-//     37 tokens, 32 of 128 experts of 2048 x 1408   52 us   4.4 TB/s (two launches and two
+//     37 tokens, 32 of 128 experts of 2048 x 1408   51 us   4.5 TB/s (two launches and two
 //                                                   plans are 8 us of it)
 #include <hip/hip_runtime.h>
 
@@ -98,6 +99,21 @@ struct Plan {
 static_assert(kPairs <= 1 << 10 && kMaxTopK <= 64, "order[] packs a token and a slot into 16 bits");
 __device__ __forceinline__ int pair_of(const Params& p, int place) { return (place >> 6) * p.top_k + (place & 63); }
 
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, true);
+}
+// Sum of v over this lane and those below it: shifts of 1, 2, 4 and 8 inside each 16 lanes, then
+// the last lane of each 16 to the next, and of the lower half to the upper.
+__device__ __forceinline__ int scan(int v) {
+  v += dpp<0x111, 0xf>(v);
+  v += dpp<0x112, 0xf>(v);
+  v += dpp<0x114, 0xf>(v);
+  v += dpp<0x118, 0xf>(v);
+  v += dpp<0x142, 0xa>(v);
+  return v + dpp<0x143, 0xc>(v);
+}
+
 // Sorts the chunk's pairs by expert; id[pair] becomes the pair's expert or -1.
 // `count` holds kMaxExperts words of scratch.  The order of an expert's own
 // pairs depends on timing, but no result does: a pair's place only says which
@@ -129,12 +145,7 @@ __device__ __forceinline__ void make_plan(const Params& p, int t0, int pairs, Pl
       const int e = e0 + tid;
       const int c = e < p.experts ? (int)count[e] : 0;
       const uint64_t mask = __ballot(c > 0);
-      int before = c;  // inclusive sum of counts over the lanes
-#pragma unroll
-      for (int off = 1; off < 64; off <<= 1) {
-        const int v = __shfl_up(before, off);
-        if (tid >= off) before += v;
-      }
+      const int before = scan(c);
       if (c > 0) {
         const int i = touched + __popcll(mask & ((1ull << tid) - 1));
         plan.expert[i] = (uint16_t)e;
@@ -142,7 +153,7 @@ __device__ __forceinline__ void make_plan(const Params& p, int t0, int pairs, Pl
         count[e] = (uint32_t)(start + before - c);  // next free place of this expert
       }
       touched += __popcll(mask);
-      start += __shfl(before, 63);
+      start += __builtin_amdgcn_readlane(before, 63);
       most = max(most, c);
     }
 #pragma unroll
@@ -255,23 +266,25 @@ __device__ __forceinline__ bf16x8 widen(uint32_t lo, uint32_t hi) {
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + __expf(-g)); }
 
-// Stage of the gate/up kernel: gate tile, up tile, NG token tiles, the tokens' scales
-// (one per lane), the two block scales.
-template <int NG>
+// Stage of the gate/up kernel: RT gate tiles, RT up tiles, NG token tiles, and a word per
+// lane: the tokens' scales, and in the last two the block scales (with 64 tokens, whose
+// scales take them all, in words of their own).
+template <int NG, int RT>
 struct UpStage {
-  static constexpr int kX = 4096, kSx = kX + 2048 * NG, kSw = kSx + 256, kBytes = kSw + 256;
-  static constexpr int kLoads = 6 + 2 * NG;
+  static constexpr int kUp = 2048 * RT, kX = 2 * kUp, kSx = kX + 2048 * NG, kSw = kSx + (NG < 4 ? 248 : 256);
+  static constexpr int kBytes = kSx + (NG < 4 ? 256 : 512);
+  static constexpr int kLoads = 4 * RT + 2 * NG + 2;
 };
 
-// A unit is one touched expert's tile of 16 columns of a; workgroups take contiguous
+// A unit is one touched expert's tile of 16 * RT columns of a; workgroups take contiguous
 // ranges of units.  An expert with more than 16 * NG tokens takes several passes.
-// grid: (workgroups, chunks).
-template <bool UE8M0, int NG>
+// D: stages of a ring.  grid: (workgroups, chunks).
+template <bool UE8M0, int NG, int RT, int D>
 __global__ void __launch_bounds__(kUpWaves * 64) gate_up_kernel(const Params p) {
-  using S = UpStage<NG>;
-  constexpr int D = 2;  // stages of a ring
+  using S = UpStage<NG, RT>;
   __shared__ __attribute__((aligned(1024))) uint8_t ring[kUpWaves * D * S::kBytes];
-  __shared__ __attribute__((aligned(16))) float red[kUpWaves * 8 * 64];
+  // the waves' sums: [wave][token group, row tile][gate, up][lane]
+  __shared__ __attribute__((aligned(16))) f32x4 red[kUpWaves * NG * RT * 2 * 64];
   __shared__ Plan plan;
   static_assert(sizeof(red) >= sizeof(uint32_t) * kMaxExperts, "the plan's scratch shares red");
   const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, q4 = lane >> 4;
@@ -280,7 +293,7 @@ __global__ void __launch_bounds__(kUpWaves * 64) gate_up_kernel(const Params p) 
   const int tokens = min(p.tokens, p.m - t0);
   make_plan<kUpWaves * 64>(p, t0, tokens * p.top_k, plan, reinterpret_cast<int16_t*>(ring),
                            reinterpret_cast<uint32_t*>(red));
-  const int tiles = p.inter >> 4, nkb = p.hidden >> 7, nb = p.inter >> 7, nw = words<UE8M0>(nkb);
+  const int tiles = p.inter / (16 * RT), nkb = p.hidden >> 7, nb = p.inter >> 7, nw = words<UE8M0>(nkb);
   const int rounds = (nkb + kUpWaves - 1) / kUpWaves;
   const int units = uniform(plan.touched) * tiles;
   const int each = units / (int)gridDim.x, more = units - each * (int)gridDim.x;  // the first `more` take one more
@@ -305,8 +318,8 @@ __global__ void __launch_bounds__(kUpWaves * 64) gate_up_kernel(const Params p) 
   auto pass = [&]() __attribute__((always_inline)) {
     const int e = uniform((int)plan.expert[li]), first = uniform((int)plan.start[li]);
     ln = uniform((int)plan.start[li + 1]) - first;
-    lw = p.w13 + ((int64_t)e * 2 * p.inter + lt * 16) * p.hidden;
-    lsw = static_cast<const uint32_t*>(p.sf13) + ((int64_t)e * 2 * nb + (lt >> 3)) * nw;
+    lw = p.w13 + ((int64_t)e * 2 * p.inter + lt * 16 * RT) * p.hidden;
+    lsw = static_cast<const uint32_t*>(p.sf13) + ((int64_t)e * 2 * nb + (lt * RT >> 3)) * nw;
 #pragma unroll
     for (int g = 0; g < NG; ++g)
 #pragma unroll
@@ -321,21 +334,27 @@ __global__ void __launch_bounds__(kUpWaves * 64) gate_up_kernel(const Params p) 
     const int kb = wave + lit * kUpWaves;
     const uint32_t k = kb < nkb ? (uint32_t)kb * 128 : kNowhere;
     const uint32_t lds = (uint32_t)uniform((int)(my_lds + slot * S::kBytes));
-    const __amdgpu_buffer_rsrc_t rg = uniform_rsrc(lw, 16u * p.hidden);
-    const __amdgpu_buffer_rsrc_t ru = uniform_rsrc(lw + (int64_t)p.inter * p.hidden, 16u * p.hidden);
+    const __amdgpu_buffer_rsrc_t rg = uniform_rsrc(lw, 16u * RT * p.hidden);
+    const __amdgpu_buffer_rsrc_t ru = uniform_rsrc(lw + (int64_t)p.inter * p.hidden, 16u * RT * p.hidden);
     const __amdgpu_buffer_rsrc_t rsw = uniform_rsrc(lsw, (uint32_t)((nb + 1) * nw * 4));
-    to_lds<16, true>(rg, lds, w_off + k);
-    to_lds<16, true>(rg, lds + 1024, w_off + 8u * p.hidden + k);
-    to_lds<16, true>(ru, lds + 2048, w_off + k);
-    to_lds<16, true>(ru, lds + 3072, w_off + 8u * p.hidden + k);
+#pragma unroll
+    for (int h = 0; h < 2 * RT; ++h) to_lds<16, true>(rg, lds + 1024 * h, w_off + 8u * h * p.hidden + k);
+#pragma unroll
+    for (int h = 0; h < 2 * RT; ++h) to_lds<16, true>(ru, lds + S::kUp + 1024 * h, w_off + 8u * h * p.hidden + k);
 #pragma unroll
     for (int g = 0; g < NG; ++g)
 #pragma unroll
       for (int h = 0; h < 2; ++h) to_lds<16, false>(rx, lds + S::kX + 2048 * g + 1024 * h, x_off[g][h] + k);
     const uint32_t wd = kb < nkb ? (uint32_t)word_of<UE8M0>(kb) : kNowhere;
-    to_lds<4, false>(rsx, lds + S::kSx,
-                     kb < nkb && sx_off != kNowhere ? sx_off + wd * (uint32_t)p.ld_sfx * 4 : kNowhere);
-    to_lds<4, false>(rsw, lds + S::kSw, kb < nkb && lane < 2 ? (lane * nb * nw + wd) * 4 : kNowhere);
+    // (a lane's word lies at the address given and four bytes per lane, whichever lanes take part)
+    const uint32_t sx_at = kb < nkb && sx_off != kNowhere ? sx_off + wd * (uint32_t)p.ld_sfx * 4 : kNowhere;
+    if constexpr (NG < 4) {
+      if (lane < 62) to_lds<4, false>(rsx, lds + S::kSx, sx_at);
+      else to_lds<4, false>(rsw, lds + S::kSx, kb < nkb ? ((lane - 62) * nb * nw + wd) * 4 : kNowhere);
+    } else {
+      to_lds<4, false>(rsx, lds + S::kSx, sx_at);
+      to_lds<4, false>(rsw, lds + S::kSw, kb < nkb && lane < 2 ? (lane * nb * nw + wd) * 4 : kNowhere);
+    }
     slot = slot + 1 == D ? 0 : slot + 1;
     if (++lit < rounds) return;
     lit = 0;
@@ -354,18 +373,25 @@ __global__ void __launch_bounds__(kUpWaves * 64) gate_up_kernel(const Params p) 
 
   int at = 0, i = i0, t = u0 - i0 * tiles;
   for (int u = u0; u < u1; ++u) {
-    const int col0 = t * 16;
+    const int col0 = t * 16 * RT;
     const int first = uniform((int)plan.start[i]), n = uniform((int)plan.start[i + 1]) - first;
     for (int g0 = 0; g0 < n; g0 += 16 * NG) {
-      f32x4 ag[NG], au[NG];
+      f32x4 ag[NG][RT], au[NG][RT];
 #pragma unroll
-      for (int g = 0; g < NG; ++g) ag[g] = au[g] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int v = 0; v < RT; ++v) ag[g][v] = au[g][v] = f32x4{0.f, 0.f, 0.f, 0.f};
       for (int it = 0; it < rounds; ++it) {
         if (left > 0) wait_loads<(D - 1) * S::kLoads>();
         else wait_loads<0>();
         const uint8_t* st = my_ring + at * S::kBytes;
         const int kb = wave + it * kUpWaves;
-        const i32x8 fg = read_frag(st, r16, q4), fu = read_frag(st + 2048, r16, q4);
+        i32x8 fg[RT], fu[RT];
+#pragma unroll
+        for (int v = 0; v < RT; ++v) {
+          fg[v] = read_frag(st + 2048 * v, r16, q4);
+          fu[v] = read_frag(st + S::kUp + 2048 * v, r16, q4);
+        }
         const uint32_t* sw = reinterpret_cast<const uint32_t*>(st + S::kSw);
         const float sg = scale_of<UE8M0>(sw[0], kb), su = scale_of<UE8M0>(sw[1], kb);
 #pragma unroll
@@ -373,44 +399,48 @@ __global__ void __launch_bounds__(kUpWaves * 64) gate_up_kernel(const Params p) 
           if (g > 0 && g0 + 16 * g >= n) break;
           const i32x8 fx = read_frag(st + S::kX + 2048 * g, r16, q4);
           const float sx = scale_of<UE8M0>(reinterpret_cast<const uint32_t*>(st + S::kSx)[16 * g + r16], kb);
-          const f32x4 pg = mfma_fp8(fg, fx), pu = mfma_fp8(fu, fx);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            ag[g][r] = __builtin_fmaf(pg[r], sx * sg, ag[g][r]);
-            au[g][r] = __builtin_fmaf(pu[r], sx * su, au[g][r]);
+          for (int v = 0; v < RT; ++v) {
+            const f32x4 pg = mfma_fp8(fg[v], fx), pu = mfma_fp8(fu[v], fx);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              ag[g][v][r] = __builtin_fmaf(pg[r], sx * sg, ag[g][v][r]);
+              au[g][v][r] = __builtin_fmaf(pu[r], sx * su, au[g][v][r]);
+            }
           }
         }
         wait_lds();
         if (left > 0) load();
         at = at + 1 == D ? 0 : at + 1;
       }
-      // the waves' sums meet group by group: red[wave][gate 0..3, up 0..3][lane]
+      // the waves' sums meet in LDS, where one wave adds each tile's
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        if (g > 0 && g0 + 16 * g >= n) break;
+      for (int g = 0; g < NG; ++g)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          red[(wave * 8 + r) * 64 + lane] = ag[g][r];
-          red[(wave * 8 + 4 + r) * 64 + lane] = au[g][r];
+        for (int v = 0; v < RT; ++v) {
+          if (g > 0 && g0 + 16 * g >= n) break;
+          red[((wave * NG + g) * RT + v) * 128 + lane] = ag[g][v];
+          red[((wave * NG + g) * RT + v) * 128 + 64 + lane] = au[g][v];
         }
-        __syncthreads();
-        if (g % kUpWaves == wave && g0 + 16 * g + r16 < n) {
-          bf16x4 a;
+      __syncthreads();
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            float vg = 0.f, vu = 0.f;
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int v = 0; v < RT; ++v)
+          if ((g * RT + v) % kUpWaves == wave && g0 + 16 * g + r16 < n) {
+            f32x4 vg = {0.f, 0.f, 0.f, 0.f}, vu = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int k = 0; k < kUpWaves; ++k) {
-              vg += red[(k * 8 + r) * 64 + lane];
-              vu += red[(k * 8 + 4 + r) * 64 + lane];
+              vg += red[((k * NG + g) * RT + v) * 128 + lane];
+              vu += red[((k * NG + g) * RT + v) * 128 + 64 + lane];
             }
-            a[r] = (__bf16)(silu(vg) * vu);
+            bf16x4 a;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) a[r] = (__bf16)(silu(vg[r]) * vu[r]);
+            const int pair = pair_of(p, plan.order[first + g0 + 16 * g + r16]);
+            *reinterpret_cast<bf16x4*>(p.act + ((int64_t)t0 * p.top_k + pair) * p.inter + col0 + 16 * v + 4 * q4) = a;
           }
-          const int pair = pair_of(p, plan.order[first + g0 + 16 * g + r16]);
-          *reinterpret_cast<bf16x4*>(p.act + ((int64_t)t0 * p.top_k + pair) * p.inter + col0 + 4 * q4) = a;
-        }
-        __syncthreads();
-      }
+      __syncthreads();
     }
     if (++t == tiles) t = 0, ++i;
   }
@@ -420,7 +450,7 @@ __global__ void __launch_bounds__(kUpWaves * 64) gate_up_kernel(const Params p) 
 // values of a, and the block scale.
 template <int RB, int AL>
 struct DownStage {
-  static constexpr int kA = 128 * RB, kSw = kA + 1024 * AL, kBytes = kSw + 256;
+  static constexpr int kA = 128 * RB, kSw = kA + 1024 * AL, kBytes = kSw + 16;
   static constexpr int kLoads = RB / 8 + AL + 1;
 };
 
@@ -478,7 +508,7 @@ __device__ __forceinline__ void down_stream(const Params& p, const Plan& plan, c
       to_lds<16, true>(rw, lds + 1024 * r, w_off + (uint32_t)(8 * r) * p.inter + lkb * 128);
 #pragma unroll
     for (int h = 0; h < AL; ++h) to_lds<16, false>(ra, lds + S::kA + 1024 * h, a_off[h] + lkb * 256);
-    to_lds<4, false>(rsw, lds + S::kSw, lane == 0 ? word_of<UE8M0>(lkb) * 4 : kNowhere);
+    if (lane == 0) to_lds<4, false>(rsw, lds + S::kSw, word_of<UE8M0>(lkb) * 4);
     slot = slot + 1 == k.depth ? 0 : slot + 1;
     if (++lkb < lkb1) return;
     lg0 += T;
@@ -569,20 +599,19 @@ __global__ void __launch_bounds__(kDownWaves * 64) down_kernel(const Params p) {
   make_plan<kDownWaves * 64>(p, k.t0, k.pairs, plan, id, reinterpret_cast<uint32_t*>(lds));
   if (tid < kPairs) tw[tid] = my_tw;
   const int nkb = p.inter >> 7, touched = uniform(plan.touched), most = uniform(plan.most);
-  // the fullest expert's tokens decide how much of a stage a takes, and with it how many
-  // waves have rings of at least two stages
+  // The fullest expert's tokens decide how much of a stage a takes, and with it how many waves
+  // have rings of at least two stages.  (Any number of waves: 64 tokens 133 us, 136 us with
+  // powers of two.)
   const int al = most <= 4 ? 1 : most <= 8 ? 2 : most <= 16 ? 4 : most <= 24 ? 6 : 8;
-  const int bytes = 128 * RB + 1024 * al + 256;
-  int lw = 4;  // log2 of the waves
-  static_assert(kDownWaves == 16, "2^lw");
-  while (lw > 1 && (bytes << lw) * 2 > p.ring) --lw;
-  k.waves = 1 << lw;
-  k.depth = (bytes << lw) * 4 <= p.ring ? 4 : (bytes << lw) * 3 <= p.ring ? 3 : 2;
+  const int bytes = 128 * RB + 1024 * al + 16;
+  const int stages = p.ring / bytes;
+  k.waves = min(kDownWaves, stages / 2);
+  k.depth = min(4, stages / k.waves);
   // K ranges per expert: as many as balance the waves best, a piece costing two K blocks beside its own
   k.split = 0;
   int best = 0x7fffffff;
   for (int s = 0; 1 << s <= p.slots && 1 << s <= nkb; ++s) {
-    const int cost = (((touched << s) + k.waves - 1) >> lw) * (((nkb + (1 << s) - 1) >> s) + 2);
+    const int cost = (((touched << s) + k.waves - 1) / k.waves) * (((nkb + (1 << s) - 1) >> s) + 2);
     if (cost < best) best = cost, k.split = s;
   }
   switch (al) {
@@ -612,9 +641,9 @@ inline bool aligned_to(const void* p, uintptr_t a) { return reinterpret_cast<uin
 
 constexpr int kLds = 160 * 1024;  // LDS of a CU
 
-template <bool UE8M0, int NG>
+template <bool UE8M0, int NG, int RT, int D>
 void launch_up(const Params& p, dim3 grid, hipStream_t stream) {
-  hipLaunchKernelGGL((gate_up_kernel<UE8M0, NG>), grid, dim3(kUpWaves * 64), 0, stream, p);
+  hipLaunchKernelGGL((gate_up_kernel<UE8M0, NG, RT, D>), grid, dim3(kUpWaves * 64), 0, stream, p);
 }
 
 template <bool UE8M0, int RB>
@@ -630,14 +659,17 @@ void launch_down(Params p, int chunks, int pairs, hipStream_t stream) {
 template <bool UE8M0>
 void launch(const Params& p, int chunks, int pairs, hipStream_t stream) {
   const int usable = dg_get_num_cus(), cus = usable > 0 ? usable : 256;
-  const int64_t units = (int64_t)std::min(pairs, p.experts) * (p.inter / 16);
-  const auto grid = [&](int per_cu) { return dim3((unsigned)std::min<int64_t>(units, (int64_t)cus * per_cu), chunks); };
+  const auto grid = [&](int columns, int per_cu) {
+    const int64_t units = (int64_t)std::min(pairs, p.experts) * (p.inter / columns);
+    return dim3((unsigned)std::min<int64_t>(units, (int64_t)cus * per_cu), chunks);
+  };
   // Tokens of an expert per pass: no more than 16 can come where there are no more tokens;
-  // else 32, with room for an uneven routing, until that is the average itself (pairs / experts,
-  // if all ids are of this device).  An expert with more takes further passes over its weights.
-  if (std::min(p.m, p.tokens) <= 16) launch_up<UE8M0, 1>(p, grid(2), stream);
-  else if (pairs / p.experts <= 20) launch_up<UE8M0, 2>(p, grid(2), stream);
-  else launch_up<UE8M0, 4>(p, grid(1), stream);
+  // else 32, with room for an uneven routing, until the average (pairs / experts, if all ids are
+  // of this device) comes close to that: 16 experts of 4096 x 2048 with 24 on average 100 us, 111 us
+  // with 64 tokens per pass; with 28 126 and 121 us.  An expert with more takes further passes.
+  if (std::min(p.m, p.tokens) <= 16) launch_up<UE8M0, 1, 1, 2>(p, grid(16, 2), stream);
+  else if (pairs / p.experts <= 26) launch_up<UE8M0, 2, 2, 2>(p, grid(32, 1), stream);
+  else launch_up<UE8M0, 4, 1, 2>(p, grid(16, 1), stream);
   // columns per workgroup: what gives the fewest rounds over the CUs, weighted with their length
   const auto rounds = [&](int rb) { return (int64_t)((p.hidden / rb * (int64_t)chunks + cus - 1) / cus) * rb; };
   if (rounds(32) <= rounds(16) && rounds(32) <= rounds(8)) launch_down<UE8M0, 32>(p, chunks, pairs, stream);

@@ -400,7 +400,7 @@ struct BwdParams {
 // operands in flight) and keeps its sum of dy * xhat per column in registers;
 // it leaves that as one row of `part`.
 template <bool BF16, bool NT, int C>
-__global__ void __launch_bounds__(kMaxThreads) 
+__global__ void __launch_bounds__(kMaxThreads)
 bwd_kernel(const BwdParams p) {
   __shared__ float s_sum[2][kSlots];
   constexpr int ES = BF16 ? 2 : 4;
