@@ -579,9 +579,12 @@ def _row_scales(sf: torch.Tensor, dev: int, m: int, k: int, name: str):
     if not ue and sf.dtype is not torch.float32:
         raise TypeError(f"{name} must be float32 (FP32 scales) or int32 (packed UE8M0)")
     shape = sf.shape
-    if sf.get_device() != dev or len(shape) != 2 or shape[0] != _sf_rows(k, ue) or shape[1] < m \
-            or not _unit_last_stride(sf):
+    if sf.get_device() != dev or len(shape) != 2 or shape[0] != _sf_rows(k, ue) or shape[1] < m:
         raise ValueError(f"{name} shape {tuple(shape)} does not fit M = {m}, K = {k}")
+    if shape[0] > 1 and sf.is_contiguous():
+        return ue, sf.data_ptr(), shape[1]
+    if not _unit_last_stride(sf):
+        raise ValueError(f"{name} must be contiguous in its last dimension")
     return ue, sf.data_ptr(), _ld(sf, 0, 4)
 
 

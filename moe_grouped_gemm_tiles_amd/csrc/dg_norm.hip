@@ -74,6 +74,20 @@ __device__ __forceinline__ uint32_t place(int ch, int half) {
   return BF16 ? ch * 8 + half * 4 : (ch >> 4) * 128 + half * 64 + (ch & 15) * 4;
 }
 
+// Rows of 128 and 256 values take 16 and 32 lanes, so a wave works on four and two of them at a
+// time (ROWS): a lane's offset in its operand is then its row's distance from the wave's first row,
+// or kNoRow past the last row, and a descriptor reaches over the wave's rows.  (Longer rows: 0.)
+constexpr uint32_t kNoRow = 0x80000000u;
+template <int ROWS>
+__device__ __forceinline__ uint32_t row_off(int sub, bool valid, int64_t ld) {
+  if constexpr (ROWS == 1) return 0;
+  return valid ? (uint32_t)sub * (uint32_t)ld : kNoRow;
+}
+template <int ROWS>
+__device__ __forceinline__ uint32_t reach(uint32_t bytes, int64_t ld) {
+  return bytes == 0 ? 0 : (uint32_t)(ROWS - 1) * (uint32_t)ld + bytes;
+}
+
 // Raw bits of a thread's chunks of one row.
 template <bool BF16, int C>
 struct Raw {
@@ -81,13 +95,13 @@ struct Raw {
 };
 
 template <bool BF16, bool NT, int C>
-__device__ __forceinline__ void load_row(__amdgpu_buffer_rsrc_t r, int tid, int nt, Raw<BF16, C>& o) {
+__device__ __forceinline__ void load_row(__amdgpu_buffer_rsrc_t r, uint32_t off, int tid, int nt, Raw<BF16, C>& o) {
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
     for (int h = 0; h < (BF16 ? 1 : 2); ++h)
-      o.d[c][h] =
-          __builtin_amdgcn_raw_buffer_load_b128(r, place<BF16>(c * nt + tid, h) * (BF16 ? 2 : 4), 0, kPolicy<NT>);
+      o.d[c][h] = __builtin_amdgcn_raw_buffer_load_b128(r, off + place<BF16>(c * nt + tid, h) * (BF16 ? 2 : 4), 0,
+                                                        kPolicy<NT>);
 }
 
 template <bool BF16, int C>
@@ -111,23 +125,23 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
 
 // Eight values of chunk ch, laid out as rows of type BF16, to FP32 memory.
 template <bool BF16, bool NT>
-__device__ __forceinline__ void store8_fp32(__amdgpu_buffer_rsrc_t r, int ch, const float (&v)[8]) {
+__device__ __forceinline__ void store8_fp32(__amdgpu_buffer_rsrc_t r, uint32_t off, int ch, const float (&v)[8]) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const u32x4 o = {__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]), __float_as_uint(v[4 * h + 2]),
                      __float_as_uint(v[4 * h + 3])};
-    __builtin_amdgcn_raw_buffer_store_b128(o, r, place<BF16>(ch, h) * 4, 0, kPolicy<NT>);
+    __builtin_amdgcn_raw_buffer_store_b128(o, r, off + place<BF16>(ch, h) * 4, 0, kPolicy<NT>);
   }
 }
 
 // Eight values of chunk ch to a row, rounded to the row's type.
 template <bool BF16, bool NT>
-__device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t r, int ch, const float (&v)[8]) {
+__device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t r, uint32_t off, int ch, const float (&v)[8]) {
   if constexpr (BF16) {
     const u32x4 o = {bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])};
-    __builtin_amdgcn_raw_buffer_store_b128(o, r, ch * 16, 0, kPolicy<NT>);
+    __builtin_amdgcn_raw_buffer_store_b128(o, r, off + ch * 16, 0, kPolicy<NT>);
   } else {
-    store8_fp32<false, NT>(r, ch, v);
+    store8_fp32<false, NT>(r, off, ch, v);
   }
 }
 
@@ -178,24 +192,35 @@ __device__ __forceinline__ uint32_t max16(uint32_t v) {
   return max(v, dpp<0x140>(v));
 }
 
+// Sum of lanes l, l ^ 16 (or l ^ 32).
+__device__ __forceinline__ float add_xor16(float v) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+__device__ __forceinline__ float add_xor32(float v) {
+  const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+
+// Sum over the 64 / ROWS lanes of a row.
+template <int ROWS>
 __device__ __forceinline__ float wave_sum(float v) {
   v += dpp<0xB1>(v);
   v += dpp<0x4E>(v);
   v += dpp<0x141>(v);
   v += dpp<0x140>(v);
-  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+  if (ROWS < 4) v = add_xor16(v);
+  return ROWS < 2 ? add_xor32(v) : v;
 }
 
-// Sum over the workgroup, the same on every thread and in a fixed order.
+// Sum over the row, the same on every thread of it and in a fixed order.
 // `slot` holds one float per wave (zeros past the last); calls in turn use
 // different slots, so one barrier per call is enough.
 constexpr int kSlots = kMaxThreads / 64;
-__device__ __forceinline__ float block_sum(float v, float* slot) {
-  v = wave_sum(v);
-  if (blockDim.x == 64) return v;
+template <int ROWS>
+__device__ __forceinline__ float row_sum(float v, float* slot) {
+  v = wave_sum<ROWS>(v);
+  if (ROWS > 1 || blockDim.x == 64) return v;
   if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
   __syncthreads();
   float t[kSlots];
@@ -281,15 +306,16 @@ struct FwdParams {
   int w_bf16;
 };
 
-// One workgroup takes rows_per_wg rows in turn, the next row's operands being
+// One workgroup takes rows_per_wg rows in turn (ROWS at a time), the next row's operands being
 // loaded while a row is worked on; a thread holds chunks c * blockDim + tid of
 // eight values of a row, so 16 adjacent lanes hold one 128-value block and a
 // wave four adjacent ones (one packed UE8M0 word).
-template <bool BF16, bool UE8M0, bool NT, int C>
-__global__ void __launch_bounds__(kMaxThreads) fwd_kernel(const FwdParams p) {
+template <bool BF16, bool UE8M0, bool NT, int C, int ROWS>
+__global__ void __launch_bounds__(ROWS > 1 ? 64 : kMaxThreads) fwd_kernel(const FwdParams p) {
   __shared__ float s_sum[2][2][kSlots];  // [scaled again][row parity]
   constexpr int ES = BF16 ? 2 : 4;
-  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 63;
+  const int lane = threadIdx.x & 63, sub = ROWS > 1 ? lane / (64 / ROWS) : 0;
+  const int tid = ROWS > 1 ? lane % (64 / ROWS) : threadIdx.x, nt = blockDim.x;
   const int chunks = p.k >> 3;
   const uint32_t bytes = (uint32_t)p.k * ES, res_bytes = p.res != nullptr ? bytes : 0;
   // Workgroups go to the eight XCDs in turn.  Each XCD takes runs of 32 adjacent rows, so that
@@ -302,16 +328,25 @@ __global__ void __launch_bounds__(kMaxThreads) fwd_kernel(const FwdParams p) {
   }
   const int row0 = wg * p.rows_per_wg;
   const int row1 = min(row0 + p.rows_per_wg, p.m);
-  if (tid < 4 * kSlots) (&s_sum[0][0][0])[tid] = 0.f;
+  if (ROWS == 1) {
+    if (tid < 4 * kSlots) (&s_sum[0][0][0])[tid] = 0.f;
+  }
   float w[C][8];
   load_weight<BF16, C>(p.w, p.w_bf16, p.k, tid, nt, w);
   Raw<BF16, C> x, r;
-  load_row<BF16, NT, C>(make_rsrc(p.x + row0 * p.ldx, bytes), tid, nt, x);
-  load_row<BF16, NT, C>(make_rsrc(p.res + row0 * p.ldr, res_bytes), tid, nt, r);
+  const auto load = [&](int row) __attribute__((always_inline)) {
+    const bool valid = ROWS == 1 || row + sub < row1;
+    load_row<BF16, NT, C>(make_rsrc(p.x + row * p.ldx, reach<ROWS>(bytes, p.ldx)), row_off<ROWS>(sub, valid, p.ldx),
+                          tid, nt, x);
+    load_row<BF16, NT, C>(make_rsrc(p.res + row * p.ldr, reach<ROWS>(res_bytes, p.ldr)),
+                          row_off<ROWS>(sub, valid, p.ldr), tid, nt, r);
+  };
+  load(row0);
   const float inv_k = 1.0f / (float)p.k;
-  __syncthreads();
-  for (int row = row0; row < row1; ++row) {
-    const __amdgpu_buffer_rsrc_t ro = make_rsrc(p.res_out + row * p.ldro, res_bytes);
+  if (ROWS == 1) __syncthreads();
+  for (int row = row0; row < row1; row += ROWS) {
+    const bool valid = ROWS == 1 || row + sub < row1;
+    const __amdgpu_buffer_rsrc_t ro = make_rsrc(p.res_out + row * p.ldro, reach<ROWS>(res_bytes, p.ldro));
     float v[C][8];
     float ss = 0.f;
 #pragma unroll
@@ -325,15 +360,13 @@ __global__ void __launch_bounds__(kMaxThreads) fwd_kernel(const FwdParams p) {
         ss = __builtin_fmaf(v[c][i], v[c][i], ss);
       }
     }
-    if (row + 1 < row1) {
-      load_row<BF16, NT, C>(make_rsrc(p.x + (row + 1) * p.ldx, bytes), tid, nt, x);
-      load_row<BF16, NT, C>(make_rsrc(p.res + (row + 1) * p.ldr, res_bytes), tid, nt, r);
-    }
+    if (row + ROWS < row1) load(row + ROWS);
 #pragma unroll
-    for (int c = 0; c < C; ++c) store8<BF16, NT>(ro, c * nt + tid, v[c]);
-    ss = block_sum(ss, s_sum[0][row & 1]);
+    for (int c = 0; c < C; ++c) store8<BF16, NT>(ro, row_off<ROWS>(sub, valid, p.ldro), c * nt + tid, v[c]);
+    ss = row_sum<ROWS>(ss, s_sum[0][row & 1]);
     float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, inv_k, p.eps));
-    if (!(ss >= 0x1p-100f && ss < __builtin_inff())) {
+    const bool again = !(ss >= 0x1p-100f && ss < __builtin_inff());
+    if (ROWS > 1 ? __any(again) : again) {
       // squares past FP32's range on either side (the same branch on every thread): again, scaled
       const float f = ss < 1.0f ? 0x1p60f : 0x1p-64f;
       ss = 0.f;
@@ -341,14 +374,17 @@ __global__ void __launch_bounds__(kMaxThreads) fwd_kernel(const FwdParams p) {
       for (int c = 0; c < C; ++c)
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss += (v[c][i] * f) * (v[c][i] * f);
-      ss = block_sum(ss, s_sum[1][row & 1]);
-      rstd = (float)(1.0 / sqrt((double)ss / ((double)f * (double)f) / p.k + (double)p.eps));
+      ss = row_sum<ROWS>(ss, s_sum[1][row & 1]);
+      const float exact = (float)(1.0 / sqrt((double)ss / ((double)f * (double)f) / p.k + (double)p.eps));
+      rstd = again ? exact : rstd;
     }
-    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(rstd), make_rsrc(p.rstd + row, p.rstd != nullptr ? 4 : 0),
-                                          tid == 0 ? 0 : kNowhere, 0, 0);
-    const __amdgpu_buffer_rsrc_t ry = make_rsrc(p.y + row * p.ldy, p.y != nullptr ? bytes : 0);
-    const __amdgpu_buffer_rsrc_t rq = make_rsrc(p.q + row * p.ldq, (uint32_t)p.k);
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(rstd),
+                                          make_rsrc(p.rstd + row, p.rstd != nullptr ? 4 * ROWS : 0),
+                                          tid == 0 && valid ? sub * 4 : kNowhere, 0, 0);
+    const __amdgpu_buffer_rsrc_t ry = make_rsrc(p.y + row * p.ldy, p.y != nullptr ? reach<ROWS>(bytes, p.ldy) : 0);
+    const __amdgpu_buffer_rsrc_t rq = make_rsrc(p.q + row * p.ldq, reach<ROWS>((uint32_t)p.k, p.ldq));
     const __amdgpu_buffer_rsrc_t rs = make_rsrc(p.sf + (int64_t)row * 4, 0xfffffffeu);
+    const uint32_t q_off = row_off<ROWS>(sub, valid, p.ldq);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int ch = c * nt + tid;
@@ -358,25 +394,35 @@ __global__ void __launch_bounds__(kMaxThreads) fwd_kernel(const FwdParams p) {
         v[c][i] = v[c][i] * rstd * w[c][i];
         amax = max(amax, __float_as_uint(v[c][i]) & 0x7fffffffu);
       }
-      store8<BF16, NT>(ry, ch, v[c]);
+      store8<BF16, NT>(ry, row_off<ROWS>(sub, valid, p.ldy), ch, v[c]);
       amax = max16(amax);
       float s;
       uint32_t byte;
       const u32x2 q = codes8<UE8M0>(v[c], amax, s, byte);
       if constexpr (BF16) {
-        __builtin_amdgcn_raw_buffer_store_b64(q, rq, ch * 8, 0, kPolicy<NT>);
+        __builtin_amdgcn_raw_buffer_store_b64(q, rq, q_off + ch * 8, 0, kPolicy<NT>);
       } else {
-        __builtin_amdgcn_raw_buffer_store_b32(q[0], rq, place<false>(ch, 0), 0, kPolicy<NT>);
-        __builtin_amdgcn_raw_buffer_store_b32(q[1], rq, place<false>(ch, 1), 0, kPolicy<NT>);
+        __builtin_amdgcn_raw_buffer_store_b32(q[0], rq, q_off + place<false>(ch, 0), 0, kPolicy<NT>);
+        __builtin_amdgcn_raw_buffer_store_b32(q[1], rq, q_off + place<false>(ch, 1), 0, kPolicy<NT>);
       }
       if constexpr (UE8M0) {
         byte = ch < chunks ? byte : 127u;
-        const uint32_t word = __builtin_amdgcn_readlane(byte, 0) | __builtin_amdgcn_readlane(byte, 16) << 8 |
-                              __builtin_amdgcn_readlane(byte, 32) << 16 | __builtin_amdgcn_readlane(byte, 48) << 24;
-        __builtin_amdgcn_raw_buffer_store_b32(
-            word, rs, lane == 0 && ch < chunks ? (uint32_t)(ch >> 6) * (uint32_t)p.ld_sf : kNowhere, 0, 0);
+        uint32_t word;
+        if constexpr (ROWS == 1)
+          word = __builtin_amdgcn_readlane(byte, 0) | __builtin_amdgcn_readlane(byte, 16) << 8 |
+                 __builtin_amdgcn_readlane(byte, 32) << 16 | __builtin_amdgcn_readlane(byte, 48) << 24;
+        else if constexpr (ROWS == 2)
+          word = (sub == 0 ? __builtin_amdgcn_readlane(byte, 0) | __builtin_amdgcn_readlane(byte, 16) << 8
+                           : __builtin_amdgcn_readlane(byte, 32) | __builtin_amdgcn_readlane(byte, 48) << 8) |
+                 0x7f7f0000u;
+        else
+          word = byte | 0x7f7f7f00u;
+        const uint32_t at = (ROWS == 1 ? lane : tid) == 0 && ch < chunks && valid
+                                ? (uint32_t)(ch >> 6) * (uint32_t)p.ld_sf + sub * 4 : kNowhere;
+        __builtin_amdgcn_raw_buffer_store_b32(word, rs, at, 0, 0);
       } else {
-        const uint32_t at = (lane & 15) == 0 && ch < chunks ? (uint32_t)(ch >> 4) * (uint32_t)p.ld_sf : kNowhere;
+        const uint32_t at =
+            (lane & 15) == 0 && ch < chunks && valid ? (uint32_t)(ch >> 4) * (uint32_t)p.ld_sf + sub * 4 : kNowhere;
         __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(s), rs, at, 0, 0);
       }
     }
@@ -396,17 +442,19 @@ struct BwdParams {
   int w_bf16;
 };
 
-// One workgroup takes rows blockIdx, blockIdx + gridDim, ... (the next row's
+// One workgroup takes rows (ROWS at a time) blockIdx, blockIdx + gridDim, ... (the next ones'
 // operands in flight) and keeps its sum of dy * xhat per column in registers;
 // it leaves that as one row of `part`.
-template <bool BF16, bool NT, int C>
-__global__ void __launch_bounds__(kMaxThreads)
-bwd_kernel(const BwdParams p) {
+template <bool BF16, bool NT, int C, int ROWS>
+__global__ void __launch_bounds__(ROWS > 1 ? 64 : kMaxThreads) bwd_kernel(const BwdParams p) {
   __shared__ float s_sum[2][kSlots];
   constexpr int ES = BF16 ? 2 : 4;
-  const int tid = threadIdx.x, nt = blockDim.x;
+  const int lane = threadIdx.x & 63, sub = ROWS > 1 ? lane / (64 / ROWS) : 0;
+  const int tid = ROWS > 1 ? lane % (64 / ROWS) : threadIdx.x, nt = blockDim.x;
   const uint32_t bytes = (uint32_t)p.k * ES, res_bytes = p.dres != nullptr ? bytes : 0;
-  if (tid < 2 * kSlots) (&s_sum[0][0])[tid] = 0.f;
+  if (ROWS == 1) {
+    if (tid < 2 * kSlots) (&s_sum[0][0])[tid] = 0.f;
+  }
   float w[C][8], dw[C][8];
   load_weight<BF16, C>(p.w, p.w_bf16, p.k, tid, nt, w);
 #pragma unroll
@@ -414,22 +462,31 @@ bwd_kernel(const BwdParams p) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[c][i] = 0.f;
   Raw<BF16, C> dy, s, dr;
-  int row = blockIdx.x;
-  float rstd = p.rstd[row];
+  float rstd = 0.f;
+  const auto load = [&](int row) __attribute__((always_inline)) {
+    const bool valid = ROWS == 1 || row + sub < p.m;
+    load_row<BF16, NT, C>(make_rsrc(p.dy + row * p.lddy, reach<ROWS>(bytes, p.lddy)), row_off<ROWS>(sub, valid, p.lddy),
+                          tid, nt, dy);
+    load_row<BF16, NT, C>(make_rsrc(p.s + row * p.lds, reach<ROWS>(bytes, p.lds)), row_off<ROWS>(sub, valid, p.lds),
+                          tid, nt, s);
+    load_row<BF16, NT, C>(make_rsrc(p.dres + row * p.lddres, reach<ROWS>(res_bytes, p.lddres)),
+                          row_off<ROWS>(sub, valid, p.lddres), tid, nt, dr);
+  };
+  const auto load_rstd = [&](int row) __attribute__((always_inline)) {
+    if constexpr (ROWS == 1)
+      rstd = p.rstd[row];
+    else
+      rstd = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+          make_rsrc(p.rstd + row, 4 * (uint32_t)min(ROWS, p.m - row)), sub * 4, 0, 0));
+  };
+  int row = blockIdx.x * ROWS;
+  load_rstd(row);
   constexpr bool kAhead = BF16 || C < 4;  // (else the next row's operands would not fit in registers)
-  if (kAhead) {
-    load_row<BF16, NT, C>(make_rsrc(p.dy + row * p.lddy, bytes), tid, nt, dy);
-    load_row<BF16, NT, C>(make_rsrc(p.s + row * p.lds, bytes), tid, nt, s);
-    load_row<BF16, NT, C>(make_rsrc(p.dres + row * p.lddres, res_bytes), tid, nt, dr);
-  }
+  if (kAhead) load(row);
   const float inv_k = 1.0f / (float)p.k;
-  __syncthreads();
+  if (ROWS == 1) __syncthreads();
   for (int turn = 0; row < p.m; turn ^= 1) {
-    if (!kAhead) {
-      load_row<BF16, NT, C>(make_rsrc(p.dy + row * p.lddy, bytes), tid, nt, dy);
-      load_row<BF16, NT, C>(make_rsrc(p.s + row * p.lds, bytes), tid, nt, s);
-      load_row<BF16, NT, C>(make_rsrc(p.dres + row * p.lddres, res_bytes), tid, nt, dr);
-    }
+    if (!kAhead) load(row);
     float g[C][8], xh[C][8], d[C][8];
     float dot = 0.f;
 #pragma unroll
@@ -447,27 +504,31 @@ bwd_kernel(const BwdParams p) {
     }
     const float r = rstd;
     const int here = row;
-    row += gridDim.x;
+    row += gridDim.x * ROWS;
     if (row < p.m) {
-      rstd = p.rstd[row];
-      if (kAhead) {
-        load_row<BF16, NT, C>(make_rsrc(p.dy + row * p.lddy, bytes), tid, nt, dy);
-        load_row<BF16, NT, C>(make_rsrc(p.s + row * p.lds, bytes), tid, nt, s);
-        load_row<BF16, NT, C>(make_rsrc(p.dres + row * p.lddres, res_bytes), tid, nt, dr);
-      }
+      load_rstd(row);
+      if (kAhead) load(row);
     }
-    dot = block_sum(dot, s_sum[turn]) * inv_k;
-    const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.dx + here * p.lddx, bytes);
+    dot = row_sum<ROWS>(dot, s_sum[turn]) * inv_k;
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.dx + here * p.lddx, reach<ROWS>(bytes, p.lddx));
+    const uint32_t off = row_off<ROWS>(sub, here + sub < p.m, p.lddx);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) d[c][i] = __builtin_fmaf(r, __builtin_fmaf(-xh[c][i], dot, g[c][i]), d[c][i]);
-      store8<BF16, NT>(rx, c * nt + tid, d[c]);
+      store8<BF16, NT>(rx, off, c * nt + tid, d[c]);
+    }
+  }
+  if constexpr (ROWS > 1) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      dw[0][i] = add_xor32(dw[0][i]);
+      if (ROWS > 2) dw[0][i] = add_xor16(dw[0][i]);
     }
   }
   const __amdgpu_buffer_rsrc_t rp = make_rsrc(p.part + (int64_t)blockIdx.x * p.k, (uint32_t)p.k * 4);
 #pragma unroll
-  for (int c = 0; c < C; ++c) store8_fp32<BF16, false>(rp, c * nt + tid, dw[c]);
+  for (int c = 0; c < C; ++c) store8_fp32<BF16, false>(rp, sub == 0 ? 0 : kNoRow, c * nt + tid, dw[c]);
 }
 
 constexpr int kDwCols = 32;   // columns of one workgroup of the column sum
@@ -476,10 +537,7 @@ constexpr int kDwWaves = 16;  // its waves; eight lanes take 32 columns of a row
 // Sum of v over the lanes l, l + 8, l + 16, ... of the wave.
 __device__ __forceinline__ float sum_every8(float v) {
   v += dpp<0x128>(v);  // rotated by eight in each 16 lanes
-  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+  return add_xor32(add_xor16(v));
 }
 
 // dw[col] (+)= sum over rows of part[row][col], in a fixed order.
@@ -489,7 +547,17 @@ __global__ void __launch_bounds__(kDwWaves * 64) dw_kernel(const float* part, in
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int c4 = (tid & 7) * 4, col = blockIdx.x * kDwCols + c4;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = tid >> 3; i < rows; i += kDwWaves * 8) {
+  constexpr int kStep = kDwWaves * 8, kUnroll = 4;
+  int i = tid >> 3;
+  for (; i + (kUnroll - 1) * kStep < rows; i += kUnroll * kStep) {
+    float4 v[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      v[u] = *reinterpret_cast<const float4*>(part + (int64_t)(i + u * kStep) * k + col);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) { a.x += v[u].x; a.y += v[u].y; a.z += v[u].z; a.w += v[u].w; }
+  }
+  for (; i < rows; i += kStep) {
     const float4 v = *reinterpret_cast<const float4*>(part + (int64_t)i * k + col);
     a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
   }
@@ -517,12 +585,20 @@ Shape shape_for(int k) {
   return {((n + c - 1) / c + 63) / 64 * 64, c};
 }
 
-// Rows one workgroup of the forward takes in turn: one where a row keeps a CU's
-// load queue busy by itself, more for shorter rows (256 columns: 357 us for a
-// million rows with 8, 427 us with 1) and for the longest, whose workgroups fill a CU
-// alone and need the prefetch (14560 x 16384: 298 us with 4, 318 us with 1).
+// Rows a wave takes at a time.  (A million rows of 128: forward 150 us with four, 325 us with one;
+// backward 170 and 249 us.  500000 of 256: 150 and 188 us with two and one, 171 and 184 us.)
+int rows_of(int k) { return k == 128 ? 4 : k == 256 ? 2 : 1; }
+// Whether so many rows of an operand lie within 32-bit offsets.
+bool near(int64_t ld) { return ld < (int64_t)1 << 28; }
+
+// Rows one workgroup of the forward takes: one where a row keeps a CU's load queue busy by itself,
+// more for shorter rows (a million of 128 columns: 150 us with 8, 156 us with 4; 333000 of 384:
+// 160 us with 4, 167 us with 8; 500000 of 256: 148.5 and 150 us) and for the longest, whose workgroups
+// fill a CU alone and need the prefetch (14560 x 16384: 298 us with 4, 318 us with 1).
 int fwd_rows(int m, int k) {
-  int rows = std::max(1, std::min(k > 8192 ? 4 : k > 4096 ? 1 : k > 512 ? 2 : 8, m / 2048));
+  const int step = rows_of(k);
+  int rows = std::max(1, std::min(k > 8192 ? 4 : k > 4096 ? 1 : k > 512 ? 2 : k > 128 ? 4 : 8, m / 2048));
+  rows = std::max(step, rows / step * step);
   while (m / rows > 1 << 22) rows *= 2;  // (a launch holds fewer than 2^32 threads)
   return rows;
 }
@@ -530,10 +606,11 @@ int fwd_rows(int m, int k) {
 // Workgroups of the backward's row loop, each of which leaves a row of partial sums:
 // 208 for rows of 4096 values and more, in proportion for shorter ones (2048 columns,
 // 77000 rows: 206 us with 448, 224 us with 336; 384 columns, 600000 rows: 320 us with
-// 2240, 435 us with 1024), and no more than one for two rows.
+// 2240, 435 us with 1024; a million of 128: 170 us with 1664, 181 us with half as many more,
+// 186 us with a quarter less), and no more than one for two turns.
 int bwd_grid(int m, int k) {
-  const int most = 208 * std::max(1, 4096 / k);
-  return std::min(most, (m + 1) / 2);
+  const int rows = rows_of(k), most = 208 * std::max(1, 4096 / k) / rows;
+  return std::min(most, (m + 2 * rows - 1) / (2 * rows));
 }
 
 inline bool aligned_to(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -548,31 +625,33 @@ inline bool rows_ok(const void* p, int64_t ld, int64_t es, int k) {
 bool streams(int64_t bytes) { return bytes > (int64_t)32 << 20; }
 
 template <bool BF16, bool UE8M0, bool NT>
-void launch_fwd(const FwdParams& p, Shape s, dim3 grid, hipStream_t stream) {
-  switch (s.chunks) {
-    case 1: hipLaunchKernelGGL((fwd_kernel<BF16, UE8M0, NT, 1>), grid, dim3(s.threads), 0, stream, p); break;
-    case 2: hipLaunchKernelGGL((fwd_kernel<BF16, UE8M0, NT, 2>), grid, dim3(s.threads), 0, stream, p); break;
-    default: hipLaunchKernelGGL((fwd_kernel<BF16, UE8M0, NT, 4>), grid, dim3(s.threads), 0, stream, p); break;
-  }
+void launch_fwd(const FwdParams& p, Shape s, int rows, dim3 grid, hipStream_t stream) {
+  const dim3 block(s.threads);
+  if (rows == 4) hipLaunchKernelGGL((fwd_kernel<BF16, UE8M0, NT, 1, 4>), grid, block, 0, stream, p);
+  else if (rows == 2) hipLaunchKernelGGL((fwd_kernel<BF16, UE8M0, NT, 1, 2>), grid, block, 0, stream, p);
+  else if (s.chunks == 1) hipLaunchKernelGGL((fwd_kernel<BF16, UE8M0, NT, 1, 1>), grid, block, 0, stream, p);
+  else if (s.chunks == 2) hipLaunchKernelGGL((fwd_kernel<BF16, UE8M0, NT, 2, 1>), grid, block, 0, stream, p);
+  else hipLaunchKernelGGL((fwd_kernel<BF16, UE8M0, NT, 4, 1>), grid, block, 0, stream, p);
 }
 template <bool BF16, bool UE8M0>
-void launch_fwd(const FwdParams& p, Shape s, bool nt, dim3 grid, hipStream_t stream) {
-  if (nt) launch_fwd<BF16, UE8M0, true>(p, s, grid, stream);
-  else launch_fwd<BF16, UE8M0, false>(p, s, grid, stream);
+void launch_fwd(const FwdParams& p, Shape s, int rows, bool nt, dim3 grid, hipStream_t stream) {
+  if (nt) launch_fwd<BF16, UE8M0, true>(p, s, rows, grid, stream);
+  else launch_fwd<BF16, UE8M0, false>(p, s, rows, grid, stream);
 }
 
 template <bool BF16, bool NT>
-void launch_bwd(const BwdParams& p, Shape s, dim3 grid, hipStream_t stream) {
-  switch (s.chunks) {
-    case 1: hipLaunchKernelGGL((bwd_kernel<BF16, NT, 1>), grid, dim3(s.threads), 0, stream, p); break;
-    case 2: hipLaunchKernelGGL((bwd_kernel<BF16, NT, 2>), grid, dim3(s.threads), 0, stream, p); break;
-    default: hipLaunchKernelGGL((bwd_kernel<BF16, NT, 4>), grid, dim3(s.threads), 0, stream, p); break;
-  }
+void launch_bwd(const BwdParams& p, Shape s, int rows, dim3 grid, hipStream_t stream) {
+  const dim3 block(s.threads);
+  if (rows == 4) hipLaunchKernelGGL((bwd_kernel<BF16, NT, 1, 4>), grid, block, 0, stream, p);
+  else if (rows == 2) hipLaunchKernelGGL((bwd_kernel<BF16, NT, 1, 2>), grid, block, 0, stream, p);
+  else if (s.chunks == 1) hipLaunchKernelGGL((bwd_kernel<BF16, NT, 1, 1>), grid, block, 0, stream, p);
+  else if (s.chunks == 2) hipLaunchKernelGGL((bwd_kernel<BF16, NT, 2, 1>), grid, block, 0, stream, p);
+  else hipLaunchKernelGGL((bwd_kernel<BF16, NT, 4, 1>), grid, block, 0, stream, p);
 }
 template <bool BF16>
-void launch_bwd(const BwdParams& p, Shape s, bool nt, dim3 grid, hipStream_t stream) {
-  if (nt) launch_bwd<BF16, true>(p, s, grid, stream);
-  else launch_bwd<BF16, false>(p, s, grid, stream);
+void launch_bwd(const BwdParams& p, Shape s, int rows, bool nt, dim3 grid, hipStream_t stream) {
+  if (nt) launch_bwd<BF16, true>(p, s, rows, grid, stream);
+  else launch_bwd<BF16, false>(p, s, rows, grid, stream);
 }
 
 dg_status launch_status() {
@@ -615,12 +694,13 @@ dg_status dg_add_rms_norm_cast_to_fp8(const void* x, int64_t ldx, const void* re
   const Shape s = shape_for(k);
   const bool nt = streams((int64_t)m * k * (es * (residual != nullptr ? 3 : 1) + 1));
   const dim3 grid((m + p.rows_per_wg - 1) / p.rows_per_wg);
+  const int rows = near(p.ldx) && near(p.ldr) && near(p.ldro) && near(p.ldy) && near(ldq) ? rows_of(k) : 1;
   if (dtype == DG_DTYPE_BF16) {
-    if (ue8m0) launch_fwd<true, true>(p, s, nt, grid, stream);
-    else launch_fwd<true, false>(p, s, nt, grid, stream);
+    if (ue8m0) launch_fwd<true, true>(p, s, rows, nt, grid, stream);
+    else launch_fwd<true, false>(p, s, rows, nt, grid, stream);
   } else {
-    if (ue8m0) launch_fwd<false, true>(p, s, nt, grid, stream);
-    else launch_fwd<false, false>(p, s, nt, grid, stream);
+    if (ue8m0) launch_fwd<false, true>(p, s, rows, nt, grid, stream);
+    else launch_fwd<false, false>(p, s, rows, nt, grid, stream);
   }
   return launch_status();
 }
@@ -658,8 +738,9 @@ dg_status dg_rms_norm_backward(const void* dy, int64_t ld_dy, const void* s, int
                       ld_dresidual * es, ld_dx * es, m, k, weight_dtype == DG_DTYPE_BF16};
     const Shape sh = shape_for(k);
     const bool nt = streams((int64_t)m * k * es * (dresidual != nullptr ? 4 : 3));
-    if (dtype == DG_DTYPE_BF16) launch_bwd<true>(p, sh, nt, dim3(grid), stream);
-    else launch_bwd<false>(p, sh, nt, dim3(grid), stream);
+    const int rows = near(p.lddy) && near(p.lds) && near(p.lddres) && near(p.lddx) ? rows_of(k) : 1;
+    if (dtype == DG_DTYPE_BF16) launch_bwd<true>(p, sh, rows, nt, dim3(grid), stream);
+    else launch_bwd<false>(p, sh, rows, nt, dim3(grid), stream);
     const dg_status st = launch_status();
     if (st != DG_SUCCESS) return st;
   }

@@ -191,6 +191,71 @@ def test_norm_residual_in_place(dtype):
         assert torch.equal(q, base["q"]) and torch.equal(sf[:, :9], base["sf"])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("k", [128, 256])
+def test_norm_narrow_rows(k, dtype):
+    """Rows of which a wave takes several at a time: counts that end inside a wave, strides, and
+    enough rows for workgroups that take more than one turn."""
+    for m in (1, 2, 3, 4, 5, 7, 8, 9, 33, 8195, 16391):
+        x, w, res = _inputs(m, k, 340 + m, dtype)
+        for ue in (False, True):
+            _check(_run(x, w, dtype, ue, res, pad=16), dtype, ue, what=f"{m}x{k} {dtype} ue={ue}")
+        _check(_run(x, w, dtype, True, None, want_y=dtype == "fp32"), dtype, True, what=f"{m}x{k} {dtype}, no residual")
+
+
+@pytest.mark.parametrize("ue", [False, True])
+@pytest.mark.parametrize("k", [128, 256, 512])
+def test_norm_narrow_rows_do_not_mix(k, ue):
+    """Zeros, tiny, huge, infinite and NaN rows beside ordinary ones: every row's results are those
+    of that row alone, bit for bit."""
+    rng = np.random.default_rng(350 + k)
+    x = rng.standard_normal((13, k)).astype(np.float32)
+    x[1] = 0
+    x[2] *= 1e-25
+    x[5] *= 1e18
+    x[7, 3] = np.inf
+    x[8, k - 1] = np.nan
+    x[10] *= 1e-38
+    w = (1 + 0.1 * rng.standard_normal(k)).astype(np.float32)
+    whole = _outputs(x, w, ue)
+    for i in range(len(x)):
+        one = _outputs(x[i:i + 1], w, ue)
+        for a, b, rows in zip(whole, one, (0, 1, 0, 0)):
+            assert torch.equal(a.select(rows, i), b.select(rows, 0)), i
+
+
+def _outputs(x, w, ue):
+    """Bits of q, sf, y and 1/rms for FP32 rows."""
+    m, k = x.shape
+    sf = torch.zeros((k // 128 + 3) // 4 if ue else k // 128, (m + 3) // 4 * 4, device="cuda:0",
+                     dtype=torch.int32 if ue else torch.float32)
+    q = torch.zeros(m, k, dtype=torch.uint8, device="cuda:0")
+    y, rstd = torch.zeros(m, k, device="cuda:0"), torch.zeros(m, device="cuda:0")
+    dg.add_rms_norm_cast_to_fp8(to_dev(x), to_dev(w), 1e-6, q, sf, y=y, rstd=rstd)
+    return q, sf.view(torch.int32), y.view(torch.int32), rstd.view(torch.int32)
+
+
+@pytest.mark.parametrize("k", [128, 256])
+def test_norm_narrow_rows_far_apart(k):
+    """Rows 256 MiB apart: too far for 32-bit offsets between the rows of a wave."""
+    rng = np.random.default_rng(360 + k)
+    x, w = rng.standard_normal((5, k)).astype(np.float32), np.ones(k, np.float32)
+    far = torch.empty(5, 1 << 26, device="cuda:0")[:, :k]
+    far.copy_(to_dev(x))
+    near, out = to_dev(x), []
+    for a in (near, far):
+        q = torch.zeros(5, k, dtype=torch.uint8, device="cuda:0")
+        sf, rstd = torch.zeros(k // 128, 8, device="cuda:0"), torch.zeros(5, device="cuda:0")
+        dg.add_rms_norm_cast_to_fp8(a, to_dev(w), 1e-6, q, sf, rstd=rstd)
+        dx, dw = torch.zeros(5, k, device="cuda:0"), torch.zeros(k, device="cuda:0")
+        dg.rms_norm_backward(near, a, to_dev(w), rstd, dx, dw)
+        out.append((q, sf, rstd, dx, dw))
+    for i in range(4):  # each row's sums are added in the same order either way
+        assert torch.equal(out[0][i], out[1][i]), i
+    # five terms of at most 16, added in another order: 4 roundings of 2^-24 each way
+    assert bool(((out[0][4] - out[1][4]).abs() <= 5 * 16 * 2.0 ** -21).all())
+
+
 def test_norm_zero_rows_and_extremes():
     """A zero row (rstd = 1/sqrt(eps), all-zero blocks have scale 1), rows near both ends of the range."""
     rng = np.random.default_rng(340)
@@ -237,7 +302,8 @@ def _run_backward(dy, s, w, rstd, dtype, dres=None, pad=0, wdtype=None, dw0=None
         return d
 
     o = dict(dy=up(dy), s=up(s), w=to_dev(w.astype(np.float32)).to(DT[wdtype or dtype]),
-             rstd=to_dev(rstd.astype(np.float32)), dres=up(dres) if dres is not None else None, dx=_filled(m, k, dtype, k + pad),
+             rstd=to_dev(rstd.astype(np.float32)), dres=up(dres) if dres is not None else None,
+             dx=_filled(m, k, dtype, k + pad),
              dw=torch.full((k,), float("nan"), device="cuda:0") if dw0 is None else to_dev(dw0.astype(np.float32)))
     ws = dg.alloc_rms_norm_backward_workspace(m, k) if workspace else None
     if ws is not None:
@@ -273,6 +339,15 @@ def test_gradient_shapes(m, k, dtype):
     dy, s, w, rstd, dres = _grad_inputs(m, k, 400 + m + k)
     _check_backward(_run_backward(dy, s, w, rstd, dtype, dres), dtype, what=f"{m}x{k} {dtype}")
     _check_backward(_run_backward(dy, s, w, rstd, dtype), dtype, what=f"{m}x{k} {dtype}, no skip path")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("k", [128, 256])
+def test_gradient_narrow_rows(k, dtype):
+    """Rows of which a wave takes several at a time: counts that end inside a wave, and many turns."""
+    for m in (1, 2, 3, 4, 5, 7, 8, 9, 33, 8195, 30001):
+        dy, s, w, rstd, dres = _grad_inputs(m, k, 440 + m)
+        _check_backward(_run_backward(dy, s, w, rstd, dtype, dres, pad=16), dtype, what=f"{m}x{k} {dtype}")
 
 
 def test_gradient_strides_accumulation_and_own_workspace():
