@@ -93,7 +93,8 @@ struct Plan {
   uint16_t expert[kPairs];
   uint16_t start[kPairs + 1];
   int touched;
-  int most;  // tokens of the fullest expert
+  int most;                // tokens of the fullest expert
+  int passes24, passes32;  // over all experts' tokens, 24 or 32 at a time
 };
 
 static_assert(kPairs <= 1 << 10 && kMaxTopK <= 64, "order[] packs a token and a slot into 16 bits");
@@ -140,7 +141,7 @@ __device__ __forceinline__ void make_plan(const Params& p, int t0, int pairs, Pl
   }
   __syncthreads();
   if (tid < 64) {  // one wave: touched experts in order of their number, and where their pairs start
-    int touched = 0, start = 0, most = 0;
+    int touched = 0, start = 0, most = 0, passes24 = 0, passes32 = 0;
     for (int e0 = 0; e0 < p.experts; e0 += 64) {
       const int e = e0 + tid;
       const int c = e < p.experts ? (int)count[e] : 0;
@@ -155,12 +156,18 @@ __device__ __forceinline__ void make_plan(const Params& p, int t0, int pairs, Pl
       touched += __popcll(mask);
       start += __builtin_amdgcn_readlane(before, 63);
       most = max(most, c);
+      passes24 += (int)((uint32_t)(c + 23) / 24u);
+      passes32 += (c + 31) >> 5;
     }
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) most = max(most, __shfl_xor(most, off));
-    if (tid == 0) {
+    passes24 = scan(passes24);
+    passes32 = scan(passes32);
+    if (tid == 63) {
       plan.touched = touched;
       plan.most = most;
+      plan.passes24 = passes24;
+      plan.passes32 = passes32;
       plan.start[touched] = (uint16_t)start;
     }
   }
@@ -599,10 +606,14 @@ __global__ void __launch_bounds__(kDownWaves * 64) down_kernel(const Params p) {
   make_plan<kDownWaves * 64>(p, k.t0, k.pairs, plan, id, reinterpret_cast<uint32_t*>(lds));
   if (tid < kPairs) tw[tid] = my_tw;
   const int nkb = p.inter >> 7, touched = uniform(plan.touched), most = uniform(plan.most);
-  // The fullest expert's tokens decide how much of a stage a takes, and with it how many waves
-  // have rings of at least two stages.  (Any number of waves: 64 tokens 133 us, 136 us with
-  // powers of two.)
-  const int al = most <= 4 ? 1 : most <= 8 ? 2 : most <= 16 ? 4 : most <= 24 ? 6 : 8;
+  // How many tokens' rows of a a stage holds: the fullest expert's, up to 32; past that 24 or 32, whichever
+  // brings fewer bytes into LDS, each pass over an expert's tokens reading its weights and costing about
+  // 3 KiB's time besides (8 experts with 43 tokens on average: 23 us with 24, 27 us with 32; 16 with 32: 144 and
+  // 140 us).  (Several passes for few tokens: 32 experts with 3 on average 63 us, 59 us with one.)  The stage's
+  // size decides how many waves have rings of at least two stages.  (Any number of waves: 64 tokens
+  // 133 us, 136 us with powers of two.)
+  const bool less = uniform(plan.passes24) * (128 * RB + 9216) < uniform(plan.passes32) * (128 * RB + 11264);
+  const int al = most <= 4 ? 1 : most <= 8 ? 2 : most <= 16 ? 4 : most <= 24 || (most > 32 && less) ? 6 : 8;
   const int bytes = 128 * RB + 1024 * al + 16;
   const int stages = p.ring / bytes;
   k.waves = min(kDownWaves, stages / 2);
@@ -670,10 +681,20 @@ void launch(const Params& p, int chunks, int pairs, hipStream_t stream) {
   if (std::min(p.m, p.tokens) <= 16) launch_up<UE8M0, 1, 1, 2>(p, grid(16, 2), stream);
   else if (pairs / p.experts <= 26) launch_up<UE8M0, 2, 2, 2>(p, grid(32, 1), stream);
   else launch_up<UE8M0, 4, 1, 2>(p, grid(16, 1), stream);
-  // columns per workgroup: what gives the fewest rounds over the CUs, weighted with their length
-  const auto rounds = [&](int rb) { return (int64_t)((p.hidden / rb * (int64_t)chunks + cus - 1) / cus) * rb; };
-  if (rounds(32) <= rounds(16) && rounds(32) <= rounds(8)) launch_down<UE8M0, 32>(p, chunks, pairs, stream);
-  else if (rounds(16) <= rounds(8)) launch_down<UE8M0, 16>(p, chunks, pairs, stream);
+  // Columns per workgroup by the time they take, in bytes at the 45 B/ns that a CU brings in (of HBM's
+  // 7 TB/s its share is 3/5 of that): every round over the CUs costs 4 us, and each workgroup reads its
+  // rows of the weights and all of a.  (64 tokens, 7168 columns: 32 133 us, 16 154 us, 8 197 us; 27 tokens, 5
+  // experts, 4224 columns, 640 values: 23, 30 and 37 us; 24 tokens, 32 experts, 2048 columns: 77, 66 and 62 us.)
+  const auto cost = [&](int rb) {
+    const int64_t wgs = (int64_t)(p.hidden / rb) * chunks, last = wgs % cus;
+    const int64_t weights = (int64_t)rb * std::min(pairs, p.experts) * p.inter;
+    const int64_t all = weights + (int64_t)pairs * p.inter * 2;
+    const int64_t round = 180000 + std::max(weights * 5 / 3, all);
+    return wgs / cus * round + (last == 0 ? 0 : 180000 + std::max(weights * 5 / 3 * last / cus, all));
+  };
+  const int64_t c8 = cost(8), c16 = cost(16), c32 = cost(32);
+  if (c32 <= c16 && c32 <= c8) launch_down<UE8M0, 32>(p, chunks, pairs, stream);
+  else if (c16 <= c8) launch_down<UE8M0, 16>(p, chunks, pairs, stream);
   else launch_down<UE8M0, 8>(p, chunks, pairs, stream);
 }
 
