@@ -47,9 +47,11 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kMaxThreads = 512;
-constexpr int kMaxChunks = 4;                        // 8-value chunks a thread holds
-constexpr int kMaxK = 8 * kMaxChunks * kMaxThreads;  // 16384
+constexpr int kMaxK = 16384;
+// Threads of the longest rows and 8-value chunks that each holds: forward 1024 and two (3695 x 11264: 60 us, with
+// 512 and four 70 us), backward 512 and four (14560 x 16384: 318 us, the other way 327 us).
+constexpr int kFwdThreads = 1024, kFwdChunks = 2;
+constexpr int kBwdThreads = 512, kBwdChunks = 4;
 constexpr uint32_t kNowhere = 0xffffffffu;           // a buffer offset past every operand: the access is dropped
 
 // Rows go through buffer descriptors of exactly their length: lanes past the
@@ -202,35 +204,28 @@ __device__ __forceinline__ float add_xor32(float v) {
   return __uint_as_float(a[0]) + __uint_as_float(a[1]);
 }
 
-// Sum over the 64 / ROWS lanes of a row.
-template <int ROWS>
-__device__ __forceinline__ float wave_sum(float v) {
+// Sum of 16 adjacent lanes.
+__device__ __forceinline__ float sum16(float v) {
   v += dpp<0xB1>(v);
   v += dpp<0x4E>(v);
   v += dpp<0x141>(v);
-  v += dpp<0x140>(v);
-  if (ROWS < 4) v = add_xor16(v);
-  return ROWS < 2 ? add_xor32(v) : v;
+  return v + dpp<0x140>(v);
 }
 
-// Sum over the row, the same on every thread of it and in a fixed order.
-// `slot` holds one float per wave (zeros past the last); calls in turn use
-// different slots, so one barrier per call is enough.
-constexpr int kSlots = kMaxThreads / 64;
+// Sum over the row, the same on every thread of it and in a fixed order: over its 64 / ROWS
+// lanes, and then over the waves of the workgroup.  `slot` holds one float per wave (zeros past
+// the last); calls in turn use different slots, so one barrier per call is enough.
+constexpr int kSlots = 16;
+static_assert(kSlots * 64 >= std::max(kFwdThreads, kBwdThreads), "one slot per wave, read by 16 lanes");
 template <int ROWS>
 __device__ __forceinline__ float row_sum(float v, float* slot) {
-  v = wave_sum<ROWS>(v);
+  v = sum16(v);
+  if (ROWS < 4) v = add_xor16(v);
+  if (ROWS < 2) v = add_xor32(v);
   if (ROWS > 1 || blockDim.x == 64) return v;
   if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
   __syncthreads();
-  float t[kSlots];
-#pragma unroll
-  for (int i = 0; i < kSlots; ++i) t[i] = slot[i];
-#pragma unroll
-  for (int d = 1; d < kSlots; d *= 2)
-#pragma unroll
-    for (int i = 0; i < kSlots; i += 2 * d) t[i] += t[i + d];
-  return t[0];
+  return sum16(slot[threadIdx.x & 15]);
 }
 
 // Codes of eight values of a block whose amax has the bits `amax` (compared as
@@ -311,7 +306,8 @@ struct FwdParams {
 // eight values of a row, so 16 adjacent lanes hold one 128-value block and a
 // wave four adjacent ones (one packed UE8M0 word).
 template <bool BF16, bool UE8M0, bool NT, int C, int ROWS>
-__global__ void __launch_bounds__(ROWS > 1 ? 64 : kMaxThreads) fwd_kernel(const FwdParams p) {
+__global__ void __launch_bounds__(ROWS > 1 ? 64 : C == 1 ? 512 : kFwdThreads, C == 1 ? 7 : BF16 ? 6 : 4)
+    fwd_kernel(const FwdParams p) {
   __shared__ float s_sum[2][2][kSlots];  // [scaled again][row parity]
   constexpr int ES = BF16 ? 2 : 4;
   const int lane = threadIdx.x & 63, sub = ROWS > 1 ? lane / (64 / ROWS) : 0;
@@ -446,7 +442,7 @@ struct BwdParams {
 // operands in flight) and keeps its sum of dy * xhat per column in registers;
 // it leaves that as one row of `part`.
 template <bool BF16, bool NT, int C, int ROWS>
-__global__ void __launch_bounds__(ROWS > 1 ? 64 : kMaxThreads) bwd_kernel(const BwdParams p) {
+__global__ void __launch_bounds__(ROWS > 1 ? 64 : kBwdThreads) bwd_kernel(const BwdParams p) {
   __shared__ float s_sum[2][kSlots];
   constexpr int ES = BF16 ? 2 : 4;
   const int lane = threadIdx.x & 63, sub = ROWS > 1 ? lane / (64 / ROWS) : 0;
@@ -573,15 +569,15 @@ __global__ void __launch_bounds__(kDwWaves * 64) dw_kernel(const float* part, in
   }
 }
 
-// Threads and chunks per thread for rows of k values: as many threads as there
-// are chunks, up to 512.
+// Threads and chunks per thread for rows of k values: as many threads as there are chunks up to
+// 512, then more chunks per thread, no more than `most`.
 struct Shape {
   int threads, chunks;
 };
-Shape shape_for(int k) {
+Shape shape_for(int k, int most) {
   const int n = k / 8;
   int c = 1;
-  while ((n + c - 1) / c > kMaxThreads) c *= 2;
+  while (c < most && (n + c - 1) / c > 512) c *= 2;
   return {((n + c - 1) / c + 63) / 64 * 64, c};
 }
 
@@ -593,11 +589,13 @@ bool near(int64_t ld) { return ld < (int64_t)1 << 28; }
 
 // Rows one workgroup of the forward takes: one where a row keeps a CU's load queue busy by itself,
 // more for shorter rows (a million of 128 columns: 150 us with 8, 156 us with 4; 333000 of 384:
-// 160 us with 4, 167 us with 8; 500000 of 256: 148.5 and 150 us) and for the longest, whose workgroups
-// fill a CU alone and need the prefetch (14560 x 16384: 298 us with 4, 318 us with 1).
-int fwd_rows(int m, int k) {
+// 160 us with 4, 167 us with 8; 500000 of 256: 148.5 and 150 us) and for the longest BF16 ones, of which
+// few workgroups share a CU, so that they need the prefetch (20000 x 8320: 212 us with 4, 228 us with
+// 2, 281 us with 1; 14560 x 16384: 298, 284 and 305 us; FP32, 7000 x 16384: 250, 249 and 240 us).
+int fwd_rows(int m, int k, bool bf16) {
   const int step = rows_of(k);
-  int rows = std::max(1, std::min(k > 8192 ? 4 : k > 4096 ? 1 : k > 512 ? 2 : k > 128 ? 4 : 8, m / 2048));
+  int rows = k > 12288 ? (bf16 ? 2 : 1) : k > 8192 ? (bf16 ? 4 : 1) : k > 4096 ? 1 : k > 512 ? 2 : k > 128 ? 4 : 8;
+  rows = std::max(1, std::min(rows, m / (k > 8192 ? 512 : 2048)));
   rows = std::max(step, rows / step * step);
   while (m / rows > 1 << 22) rows *= 2;  // (a launch holds fewer than 2^32 threads)
   return rows;
@@ -630,8 +628,7 @@ void launch_fwd(const FwdParams& p, Shape s, int rows, dim3 grid, hipStream_t st
   if (rows == 4) hipLaunchKernelGGL((fwd_kernel<BF16, UE8M0, NT, 1, 4>), grid, block, 0, stream, p);
   else if (rows == 2) hipLaunchKernelGGL((fwd_kernel<BF16, UE8M0, NT, 1, 2>), grid, block, 0, stream, p);
   else if (s.chunks == 1) hipLaunchKernelGGL((fwd_kernel<BF16, UE8M0, NT, 1, 1>), grid, block, 0, stream, p);
-  else if (s.chunks == 2) hipLaunchKernelGGL((fwd_kernel<BF16, UE8M0, NT, 2, 1>), grid, block, 0, stream, p);
-  else hipLaunchKernelGGL((fwd_kernel<BF16, UE8M0, NT, 4, 1>), grid, block, 0, stream, p);
+  else hipLaunchKernelGGL((fwd_kernel<BF16, UE8M0, NT, 2, 1>), grid, block, 0, stream, p);
 }
 template <bool BF16, bool UE8M0>
 void launch_fwd(const FwdParams& p, Shape s, int rows, bool nt, dim3 grid, hipStream_t stream) {
@@ -690,8 +687,8 @@ dg_status dg_add_rms_norm_cast_to_fp8(const void* x, int64_t ldx, const void* re
   FwdParams p{static_cast<const uint8_t*>(x), static_cast<const uint8_t*>(residual),
               static_cast<uint8_t*>(residual_out), static_cast<const uint8_t*>(weight), static_cast<uint8_t*>(q),
               static_cast<uint8_t*>(sf), static_cast<uint8_t*>(y), rstd, ldx * es, ld_residual * es,
-              ld_residual_out * es, ldq, ld_sf * 4, ldy * es, eps, m, k, fwd_rows(m, k), weight_dtype == DG_DTYPE_BF16};
-  const Shape s = shape_for(k);
+              ld_residual_out * es, ldq, ld_sf * 4, ldy * es, eps, m, k, fwd_rows(m, k, dtype == DG_DTYPE_BF16), weight_dtype == DG_DTYPE_BF16};
+  const Shape s = shape_for(k, kFwdChunks);
   const bool nt = streams((int64_t)m * k * (es * (residual != nullptr ? 3 : 1) + 1));
   const dim3 grid((m + p.rows_per_wg - 1) / p.rows_per_wg);
   const int rows = near(p.ldx) && near(p.ldr) && near(p.ldro) && near(p.ldy) && near(ldq) ? rows_of(k) : 1;
@@ -736,7 +733,7 @@ dg_status dg_rms_norm_backward(const void* dy, int64_t ld_dy, const void* s, int
                       static_cast<const uint8_t*>(weight), static_cast<const uint8_t*>(dresidual), rstd,
                       static_cast<uint8_t*>(dx), static_cast<float*>(workspace), ld_dy * es, ld_s * es,
                       ld_dresidual * es, ld_dx * es, m, k, weight_dtype == DG_DTYPE_BF16};
-    const Shape sh = shape_for(k);
+    const Shape sh = shape_for(k, kBwdChunks);
     const bool nt = streams((int64_t)m * k * es * (dresidual != nullptr ? 4 : 3));
     const int rows = near(p.lddy) && near(p.lds) && near(p.lddres) && near(p.lddx) ? rows_of(k) : 1;
     if (dtype == DG_DTYPE_BF16) launch_bwd<true>(p, sh, rows, nt, dim3(grid), stream);
