@@ -605,10 +605,13 @@ int fwd_rows(int m, int k, bool bf16) {
 // 208 for rows of 4096 values and more, in proportion for shorter ones (2048 columns,
 // 77000 rows: 206 us with 448, 224 us with 336; 384 columns, 600000 rows: 320 us with
 // 2240, 435 us with 1024; a million of 128: 170 us with 1664, 181 us with half as many more,
-// 186 us with a quarter less), and no more than one for two turns.
+// 186 us with a quarter less).  Few rows: one turn each up to 64 workgroups (49 x 11264 FP32: 8.0 us, with
+// two turns 9.3 us), then three turns, because the column sum has to read what each of them leaves
+// (1000 x 1024: 7.0 us, two turns 7.8, six 7.7; 333 x 1536 FP32: 6.0, 6.0 and 6.8 us).
 int bwd_grid(int m, int k) {
   const int rows = rows_of(k), most = 208 * std::max(1, 4096 / k) / rows;
-  return std::min(most, (m + 2 * rows - 1) / (2 * rows));
+  const int turns = (m + rows - 1) / rows;
+  return turns <= 64 ? turns : std::max(64, std::min(most, (turns + 2) / 3));
 }
 
 inline bool aligned_to(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
