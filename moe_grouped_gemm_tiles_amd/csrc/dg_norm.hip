@@ -589,15 +589,21 @@ bool near(int64_t ld) { return ld < (int64_t)1 << 28; }
 
 // Rows one workgroup of the forward takes: one where a row keeps a CU's load queue busy by itself,
 // more for shorter rows (a million of 128 columns: 150 us with 8, 156 us with 4; 333000 of 384:
-// 160 us with 4, 167 us with 8; 500000 of 256: 148.5 and 150 us) and for the longest BF16 ones, of which
-// few workgroups share a CU, so that they need the prefetch (20000 x 8320: 212 us with 4, 228 us with
-// 2, 281 us with 1; 14560 x 16384: 298, 284 and 305 us; FP32, 7000 x 16384: 250, 249 and 240 us).
+// 160 us with 4, 167 us with 8; 500000 of 256: 148.5 and 150 us).  The longest BF16 rows, of which no more
+// than two workgroups share a CU, need the prefetch (20000 x 8320: 212 us with 4, 228 us with 2, 281 us
+// with 1; 14560 x 16384: 298, 284 and 305 us) and a full last round (4339 x 11520: 65 us with 3, 71 us with
+// 4); FP32 ones do not (7000 x 16384: 250, 249 and 240 us).
 int fwd_rows(int m, int k, bool bf16) {
   const int step = rows_of(k);
-  int rows = k > 12288 ? (bf16 ? 2 : 1) : k > 8192 ? (bf16 ? 4 : 1) : k > 4096 ? 1 : k > 512 ? 2 : k > 128 ? 4 : 8;
-  rows = std::max(1, std::min(rows, m / (k > 8192 ? 512 : 2048)));
+  int rows = std::max(1, std::min(k > 4096 ? 1 : k > 512 ? 2 : k > 128 ? 4 : 8, m / 2048));
   rows = std::max(step, rows / step * step);
-  while (m / rows > 1 << 22) rows *= 2;  // (a launch holds fewer than 2^32 threads)
+  if (k > 8192 && bf16) {
+    const int at_once = 256 * (24 / ((k / 16 + 63) / 64));  // 24 waves to a CU
+    const auto turns = [&](int r) { return ((int64_t)m + r * at_once - 1) / (r * at_once) * r; };
+    for (int r = 2; r <= (k > 12288 ? 2 : 4); ++r)
+      if (turns(r) * 15 <= turns(rows) * 16) rows = r;
+  }
+  while (m / rows > 1 << 21) rows *= 2;  // (a launch holds fewer than 2^32 threads)
   return rows;
 }
 

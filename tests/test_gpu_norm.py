@@ -235,6 +235,29 @@ def _outputs(x, w, ue):
     return q, sf.view(torch.int32), y.view(torch.int32), rstd.view(torch.int32)
 
 
+@pytest.mark.parametrize("m,k", [(4339, 8320), (1300, 8448), (1100, 16384), (600, 12544)])
+def test_norm_long_rows_per_workgroup(m, k):
+    """Numbers of rows that give a workgroup of long rows one to four of them, the last one fewer: every
+    row's results are those of a few rows alone, bit for bit."""
+    gen = torch.Generator(device="cuda:0").manual_seed(370 + m)
+    x, res = (torch.randn(m, k, device="cuda:0", generator=gen).bfloat16() for _ in range(2))
+    w = (1 + 0.1 * torch.randn(k, device="cuda:0", generator=gen)).bfloat16()
+
+    def run(rows):
+        n = len(rows)
+        o = dict(q=torch.zeros(n, k, dtype=torch.uint8, device="cuda:0"), rstd=torch.zeros(n, device="cuda:0"),
+                 sf=torch.zeros(k // 128, (n + 3) // 4 * 4, device="cuda:0"), s=torch.zeros_like(x[rows]))
+        dg.add_rms_norm_cast_to_fp8(x[rows], w, 1e-6, o["q"], o["sf"], residual=res[rows], residual_out=o["s"],
+                                    rstd=o["rstd"])
+        return o["q"], o["rstd"], o["sf"].T, o["s"]
+
+    whole = run(torch.arange(m, device="cuda:0"))
+    for at in (0, 1, 511, m // 2, m - 4):
+        rows = torch.arange(at, at + 4, device="cuda:0")
+        for a, b in zip(whole, run(rows)):
+            assert torch.equal(a[rows], b), at
+
+
 @pytest.mark.parametrize("k", [128, 256])
 def test_norm_narrow_rows_far_apart(k):
     """Rows 256 MiB apart: too far for 32-bit offsets between the rows of a wave."""
