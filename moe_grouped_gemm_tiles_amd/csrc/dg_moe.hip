@@ -11,7 +11,7 @@
 // once from HBM, and everything else is arranged around that.
 //
 //   * gate/up kernel: a workgroup takes 16 gate and the matching 16 up rows of a
-//     touched expert at a time (a unit; 32 and 32 with 17 to 32 tokens, whose tiles are
+//     touched expert at a time (a unit; 32 and 32 with more than 16 tokens, whose tiles are
 //     then read half as often: 64 tokens 76 us, 83 us), its four waves split K, and one
 //     v_mfma_f32_16x16x128_f8f6f4 covers 16 rows, 16 tokens and one 128-K scale
 //     block.  The waves' partial sums meet in LDS and a is written once per (token,
@@ -289,9 +289,10 @@ struct UpStage {
 template <bool UE8M0, int NG, int RT, int D>
 __global__ void __launch_bounds__(kUpWaves * 64) gate_up_kernel(const Params p) {
   using S = UpStage<NG, RT>;
+  constexpr int XG = NG * RT <= kUpWaves ? NG : 1;
   __shared__ __attribute__((aligned(1024))) uint8_t ring[kUpWaves * D * S::kBytes];
-  // the waves' sums: [wave][token group, row tile][gate, up][lane]
-  __shared__ __attribute__((aligned(16))) f32x4 red[kUpWaves * NG * RT * 2 * 64];
+  // the waves' sums, XG token groups at a time: [wave][token group, row tile][gate, up][lane]
+  __shared__ __attribute__((aligned(16))) f32x4 red[kUpWaves * XG * RT * 2 * 64];
   __shared__ Plan plan;
   static_assert(sizeof(red) >= sizeof(uint32_t) * kMaxExperts, "the plan's scratch shares red");
   const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, q4 = lane >> 4;
@@ -422,32 +423,37 @@ __global__ void __launch_bounds__(kUpWaves * 64) gate_up_kernel(const Params p) 
       }
       // the waves' sums meet in LDS, where one wave adds each tile's
 #pragma unroll
-      for (int g = 0; g < NG; ++g)
+      for (int x0 = 0; x0 < NG; x0 += XG) {
+        if (x0 > 0 && g0 + 16 * x0 >= n) break;
 #pragma unroll
-        for (int v = 0; v < RT; ++v) {
-          if (g > 0 && g0 + 16 * g >= n) break;
-          red[((wave * NG + g) * RT + v) * 128 + lane] = ag[g][v];
-          red[((wave * NG + g) * RT + v) * 128 + 64 + lane] = au[g][v];
-        }
-      __syncthreads();
+        for (int g = 0; g < XG; ++g)
 #pragma unroll
-      for (int g = 0; g < NG; ++g)
+          for (int v = 0; v < RT; ++v) {
+            if (g > 0 && g0 + 16 * g >= n) break;
+            red[((wave * XG + g) * RT + v) * 128 + lane] = ag[x0 + g][v];
+            red[((wave * XG + g) * RT + v) * 128 + 64 + lane] = au[x0 + g][v];
+          }
+        __syncthreads();
 #pragma unroll
-        for (int v = 0; v < RT; ++v)
-          if ((g * RT + v) % kUpWaves == wave && g0 + 16 * g + r16 < n) {
+        for (int g = 0; g < XG; ++g)
+#pragma unroll
+          for (int v = 0; v < RT; ++v) {
+            const int c = g0 + 16 * (x0 + g) + r16;
+            if (((x0 + g) * RT + v) % kUpWaves != wave || c >= n) continue;
             f32x4 vg = {0.f, 0.f, 0.f, 0.f}, vu = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int k = 0; k < kUpWaves; ++k) {
-              vg += red[((k * NG + g) * RT + v) * 128 + lane];
-              vu += red[((k * NG + g) * RT + v) * 128 + 64 + lane];
+              vg += red[((k * XG + g) * RT + v) * 128 + lane];
+              vu += red[((k * XG + g) * RT + v) * 128 + 64 + lane];
             }
             bf16x4 a;
 #pragma unroll
             for (int r = 0; r < 4; ++r) a[r] = (__bf16)(silu(vg[r]) * vu[r]);
-            const int pair = pair_of(p, plan.order[first + g0 + 16 * g + r16]);
+            const int pair = pair_of(p, plan.order[first + c]);
             *reinterpret_cast<bf16x4*>(p.act + ((int64_t)t0 * p.top_k + pair) * p.inter + col0 + 16 * v + 4 * q4) = a;
           }
-      __syncthreads();
+        __syncthreads();
+      }
     }
     if (++t == tiles) t = 0, ++i;
   }
@@ -670,16 +676,19 @@ void launch_down(Params p, int chunks, int pairs, hipStream_t stream) {
 template <bool UE8M0>
 void launch(const Params& p, int chunks, int pairs, hipStream_t stream) {
   const int usable = dg_get_num_cus(), cus = usable > 0 ? usable : 256;
+  const auto units = [&](int columns) { return (int64_t)std::min(pairs, p.experts) * (p.inter / columns); };
   const auto grid = [&](int columns, int per_cu) {
-    const int64_t units = (int64_t)std::min(pairs, p.experts) * (p.inter / columns);
-    return dim3((unsigned)std::min<int64_t>(units, (int64_t)cus * per_cu), chunks);
+    return dim3((unsigned)std::min<int64_t>(units(columns), (int64_t)cus * per_cu), chunks);
   };
   // Tokens of an expert per pass: no more than 16 can come where there are no more tokens;
   // else 32, with room for an uneven routing, until the average (pairs / experts, if all ids are
   // of this device) comes close to that: 16 experts of 4096 x 2048 with 24 on average 100 us, 111 us
   // with 64 tokens per pass; with 28 126 and 121 us.  An expert with more takes further passes.
+  // 64 tokens with 32 columns of a per unit where that leaves every CU two units (16 experts with 32 tokens on
+  // average, 7168 x 2048: 205 us, with 16 columns 228 us; 8 with 43, 1664 x 512: 25.4 and 23.6 us).
   if (std::min(p.m, p.tokens) <= 16) launch_up<UE8M0, 1, 1, 2>(p, grid(16, 2), stream);
   else if (pairs / p.experts <= 26) launch_up<UE8M0, 2, 2, 2>(p, grid(32, 1), stream);
+  else if (units(32) >= 2 * cus) launch_up<UE8M0, 4, 2, 2>(p, grid(32, 1), stream);
   else launch_up<UE8M0, 4, 1, 2>(p, grid(16, 1), stream);
   // Columns per workgroup by the time they take, in bytes at the 45 B/ns that a CU brings in (of HBM's
   // 7 TB/s its share is 3/5 of that): every round over the CUs costs 4 us, and each workgroup reads its

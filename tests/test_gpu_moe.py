@@ -97,6 +97,20 @@ def test_moe_widest_rows(m, experts, top_k):
     _check(x, _run(x), what=f"m={m} H=7168 I=128")
 
 
+@pytest.mark.parametrize("fmt", ["fp32", "ue8m0"])
+@pytest.mark.parametrize("m", [28, 33, 50, 64, 65, 90, 130])
+def test_moe_many_tokens_per_expert(m, fmt):
+    """Every token at both experts: 64 tokens a pass in the first product with 16 and, where each CU gets
+    two units, 32 columns; 24 or 32 tokens a stage in the second."""
+    x = gen_moe(m, 2, 2, 1152, 640, seed=530 + m, scale_fmt=fmt)
+    for cus in (8, 0):
+        dg.set_num_cus(cus)
+        try:
+            _check(x, _run(x), what=f"m={m} {fmt} cus={cus}")
+        finally:
+            dg.set_num_cus(0)
+
+
 def test_moe_full_chunk_with_wide_tiles():
     """512 pairs of one expert in 32-column tiles: the sums take the most LDS, the rings the least."""
     x = gen_moe(512, 1, 1, 512, 256, seed=518)
