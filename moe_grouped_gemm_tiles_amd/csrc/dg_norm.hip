@@ -607,15 +607,17 @@ int fwd_rows(int m, int k, bool bf16) {
   return rows;
 }
 
-// Workgroups of the backward's row loop, each of which leaves a row of partial sums:
-// 208 for rows of 4096 values and more, in proportion for shorter ones (2048 columns,
-// 77000 rows: 206 us with 448, 224 us with 336; 384 columns, 600000 rows: 320 us with
-// 2240, 435 us with 1024; a million of 128: 170 us with 1664, 181 us with half as many more,
-// 186 us with a quarter less).  Few rows: one turn each up to 64 workgroups (49 x 11264 FP32: 8.0 us, with
-// two turns 9.3 us), then three turns, because the column sum has to read what each of them leaves
-// (1000 x 1024: 7.0 us, two turns 7.8, six 7.7; 333 x 1536 FP32: 6.0, 6.0 and 6.8 us).
-int bwd_grid(int m, int k) {
-  const int rows = rows_of(k), most = 208 * std::max(1, 4096 / k) / rows;
+// Workgroups of the backward's row loop, each of which leaves a row of partial sums: 208 for rows
+// of 8 KiB and more, else a multiple of 208 that comes to about as many bytes in flight (a number between one
+// and two per CU leaves some CUs twice the work of others: 20000 x 2560 FP32 136 us with 208, 167 us with 332).
+// 20741 x 2176 BF16: 63 us with 416, 81 us with 208; 30000 x 1024 FP32: 82 us with 416, 91 us with 832;
+// a million x 128 BF16: 170 us with 1664, 181 us with half as many more, 186 us with a quarter less.
+// Few rows: one turn each up to 64 workgroups (49 x 11264 FP32: 8.0 us, with two turns 9.3 us), then three
+// turns, because the column sum has to read what each of them leaves (1000 x 1024: 7.0 us, two turns 7.8,
+// six 7.7; 333 x 1536 FP32: 6.0, 6.0 and 6.8 us).
+int bwd_grid(int m, int k, bool bf16) {
+  const int rows = rows_of(k), full = bf16 ? 4096 : 2048;
+  const int most = 208 * std::max(1, (3 * full + 2 * k) / (3 * k)) / rows;
   const int turns = (m + rows - 1) / rows;
   return turns <= 64 ? turns : std::max(64, std::min(most, (turns + 2) / 3));
 }
@@ -713,7 +715,8 @@ dg_status dg_add_rms_norm_cast_to_fp8(const void* x, int64_t ldx, const void* re
 
 size_t dg_get_rms_norm_backward_workspace_size(int m, int k) {
   if (m <= 0 || k <= 0 || k % 128 != 0 || k > norm::kMaxK) return 0;
-  return (size_t)norm::bwd_grid(m, k) * (size_t)k * sizeof(float);
+  // (BF16 rows have the most workgroups)
+  return (size_t)norm::bwd_grid(m, k, true) * (size_t)k * sizeof(float);
 }
 
 dg_status dg_rms_norm_backward(const void* dy, int64_t ld_dy, const void* s, int64_t ld_s, dg_dtype dtype,
@@ -727,7 +730,7 @@ dg_status dg_rms_norm_backward(const void* dy, int64_t ld_dy, const void* s, int
   if (k % 128 != 0 || k > kMaxK) return DG_ERROR_NOT_SUPPORTED;
   if (k == 0) return DG_SUCCESS;
   if (dw == nullptr || !aligned_to(dw, 16)) return DG_ERROR_INVALID_VALUE;
-  const int grid = m > 0 ? bwd_grid(m, k) : 0;
+  const int grid = m > 0 ? bwd_grid(m, k, dtype == DG_DTYPE_BF16) : 0;
   if (m > 0) {
     const int64_t es = dtype == DG_DTYPE_BF16 ? 2 : 4;
     if (!rows_ok(dy, ld_dy, es, k) || !rows_ok(s, ld_s, es, k) || !rows_ok(dx, ld_dx, es, k))
