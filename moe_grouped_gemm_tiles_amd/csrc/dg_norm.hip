@@ -592,13 +592,13 @@ bool near(int64_t ld) { return ld < (int64_t)1 << 28; }
 // 160 us with 4, 167 us with 8; 500000 of 256: 148.5 and 150 us).  The longest BF16 rows, of which no more
 // than two workgroups share a CU, need the prefetch (20000 x 8320: 212 us with 4, 228 us with 2, 281 us
 // with 1; 14560 x 16384: 298, 284 and 305 us) and a full last round (4339 x 11520: 65 us with 3, 71 us with
-// 4); FP32 ones do not (7000 x 16384: 250, 249 and 240 us).  Without a residual there is less to read for
-// the same arithmetic, and the prefetch decides (33280 x 7168: 154 us with 6, 158 us with 4, 175 us with 2,
-// 206 us with 1; 33280 x 4096: 92 us with 4, 101 us with 2).
-int fwd_rows(int m, int k, bool bf16, bool residual) {
+// 4); FP32 ones do not (7000 x 16384: 250, 249 and 240 us).  With neither residual nor y there is less
+// traffic for the same arithmetic, and the prefetch decides (33280 x 7168: 154 us with 6, 158 us with 4, 175 us
+// with 2, 206 us with 1; 33280 x 4096: 92 us with 4, 101 us with 2; with y, 20000 x 4096 FP32: 131 and 122 us).
+int fwd_rows(int m, int k, bool bf16, bool codes_only) {
   const int step = rows_of(k);
   int rows = std::max(1, std::min(k > 4096 ? 1 : k > 512 ? 2 : k > 128 ? 4 : 8, m / 2048));
-  if (!residual && k > 512) rows = std::max(1, std::min(k > 4096 ? 6 : 4, m / 1024));
+  if (codes_only && k > 512) rows = std::max(1, std::min(k > 4096 ? 6 : 4, m / 1024));
   rows = std::max(step, rows / step * step);
   if (k > 8192 && bf16) {
     const int at_once = 256 * (24 / ((k / 16 + 63) / 64));  // 24 waves to a CU
@@ -701,7 +701,9 @@ dg_status dg_add_rms_norm_cast_to_fp8(const void* x, int64_t ldx, const void* re
   FwdParams p{static_cast<const uint8_t*>(x), static_cast<const uint8_t*>(residual),
               static_cast<uint8_t*>(residual_out), static_cast<const uint8_t*>(weight), static_cast<uint8_t*>(q),
               static_cast<uint8_t*>(sf), static_cast<uint8_t*>(y), rstd, ldx * es, ld_residual * es,
-              ld_residual_out * es, ldq, ld_sf * 4, ldy * es, eps, m, k, fwd_rows(m, k, dtype == DG_DTYPE_BF16, residual != nullptr), weight_dtype == DG_DTYPE_BF16};
+              ld_residual_out * es, ldq, ld_sf * 4, ldy * es, eps, m, k,
+              fwd_rows(m, k, dtype == DG_DTYPE_BF16, residual == nullptr && y == nullptr),
+              weight_dtype == DG_DTYPE_BF16};
   const Shape s = shape_for(k, kFwdChunks);
   const bool nt = streams((int64_t)m * k * (es * (residual != nullptr ? 3 : 1) + 1));
   const dim3 grid((m + p.rows_per_wg - 1) / p.rows_per_wg);
