@@ -258,6 +258,30 @@ def test_norm_long_rows_per_workgroup(m, k):
             assert torch.equal(a[rows], b), at
 
 
+@pytest.mark.parametrize("ue", [False, True])
+@pytest.mark.parametrize("m,k,dtype", [(6151, 4224, "bf16"), (4099, 640, "bf16"), (2050, 1152, "fp32"),
+                                       (3077, 8320, "fp32"), (5200, 4480, "fp32"), (2500, 9216, "bf16")])
+def test_norm_codes_alone(m, k, dtype, ue):
+    """Neither residual nor y: up to six rows per workgroup, the last one fewer; every row's results are
+    those of a few rows alone, bit for bit."""
+    gen = torch.Generator(device="cuda:0").manual_seed(380 + m)
+    x = torch.randn(m, k, device="cuda:0", generator=gen).to(DT[dtype])
+    w = (1 + 0.1 * torch.randn(k, device="cuda:0", generator=gen)).to(DT[dtype])
+
+    def run(x):
+        n = len(x)
+        sf = torch.zeros((k // 128 + 3) // 4 if ue else k // 128, (n + 3) // 4 * 4, device="cuda:0",
+                         dtype=torch.int32 if ue else torch.float32)
+        q, rstd = torch.zeros(n, k, dtype=torch.uint8, device="cuda:0"), torch.zeros(n, device="cuda:0")
+        dg.add_rms_norm_cast_to_fp8(x, w, 1e-6, q, sf, rstd=rstd)
+        return q, rstd, sf.T[:n]
+
+    whole = run(x)
+    for at in (0, 5, 767, m // 2, m - 4):
+        for a, b in zip(whole, run(x[at:at + 4])):
+            assert torch.equal(a[at:at + 4], b), at
+
+
 @pytest.mark.parametrize("k", [128, 256])
 def test_norm_narrow_rows_far_apart(k):
     """Rows 256 MiB apart: too far for 32-bit offsets between the rows of a wave."""
