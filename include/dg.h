@@ -335,7 +335,8 @@ dg_status dg_per_block_cast_to_fp8(const void* w, int64_t ldw, dg_dtype w_dtype,
  *               scales, FP32 [k/128][ld_sf] or (ue8m0 != 0) packed words
  *               [ceil(k/512)][ld_sf], as in dg_per_token_cast_to_fp8.
  * y             optional [m, k], dtype: v itself (for a router, or training).
- * rstd          optional FP32 [m]: r, for dg_rms_norm_backward.
+ * rstd          optional FP32 [m]: r, for dg_rms_norm_backward (Inf where r is past FP32's range: eps == 0 and a
+ *               row below 2^-128; v is right there too).
  * An Inf or NaN in v is kept: the block's scale is not finite (UE8M0: 255) and
  * so is what the pair stands for.
  * eps >= 0; k % 128 != 0 or k > 16384 -> DG_ERROR_NOT_SUPPORTED; m or k == 0 ->

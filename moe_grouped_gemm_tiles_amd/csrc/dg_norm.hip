@@ -360,21 +360,31 @@ __global__ void __launch_bounds__(ROWS > 1 ? 64 : C == 1 ? 512 : kFwdThreads, C 
 #pragma unroll
     for (int c = 0; c < C; ++c) store8<BF16, NT>(ro, row_off<ROWS>(sub, valid, p.ldro), c * nt + tid, v[c]);
     ss = row_sum<ROWS>(ss, s_sum[0][row & 1]);
-    float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, inv_k, p.eps));
-    const bool again = !(ss >= 0x1p-100f && ss < __builtin_inff());
+    const float arg = __builtin_fmaf(ss, inv_k, p.eps);
+    float rstd = __builtin_amdgcn_rsqf(arg), rstd_out = rstd;  // what multiplies the row, and what is stored
+    const bool again = !(ss >= 0x1p-100f && arg < __builtin_inff());
     if (ROWS > 1 ? __any(again) : again) {
-      // squares past FP32's range on either side (the same branch on every thread): again, scaled
-      const float f = ss < 1.0f ? 0x1p60f : 0x1p-64f;
+      // Squares (or the argument) past FP32's range on either side (the same branch on every thread): again,
+      // scaled.  A sum that overflowed has a value of 2^57 or more, so 2^-80 brings the largest to between 2^-23 and
+      // 2^48; below 2^-100 all values are below 2^-50, and 2^100 brings even the smallest denormal to 2^-49.
+      const float f = ss < 1.0f ? 0x1p100f : 0x1p-80f;
       ss = 0.f;
 #pragma unroll
       for (int c = 0; c < C; ++c)
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss += (v[c][i] * f) * (v[c][i] * f);
       ss = row_sum<ROWS>(ss, s_sum[1][row & 1]);
-      const float exact = (float)(1.0 / sqrt((double)ss / ((double)f * (double)f) / p.k + (double)p.eps));
-      rstd = again ? exact : rstd;
+      const double exact = 1.0 / sqrt((double)ss / ((double)f * (double)f) / p.k + (double)p.eps);
+      // a row so small that 1/rms nears or passes FP32's range is scaled itself
+      const float up = again && exact >= 0x1p100 ? 0x1p100f : 1.0f;
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[c][i] *= up;
+      rstd = again ? (float)(exact / up) : rstd;
+      rstd_out = again ? (float)exact : rstd;
     }
-    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(rstd),
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(rstd_out),
                                           make_rsrc(p.rstd + row, p.rstd != nullptr ? 4 * ROWS : 0),
                                           tid == 0 && valid ? sub * 4 : kNowhere, 0, 0);
     const __amdgpu_buffer_rsrc_t ry = make_rsrc(p.y + row * p.ldy, p.y != nullptr ? reach<ROWS>(bytes, p.ldy) : 0);

@@ -338,6 +338,54 @@ def test_norm_no_rows():
     dg.add_rms_norm_cast_to_fp8(torch.empty(0, 256, device="cuda:0"), torch.ones(256, device="cuda:0"), 1e-6, q, sf)
 
 
+def _spread(rng, k, exponents):
+    """Rows of magnitudes 0.5 to 0.99 times 2^e."""
+    sign = rng.choice([-1.0, 1.0], (len(exponents), k))
+    return sign * rng.uniform(0.5, 0.99, sign.shape) * 2.0 ** np.array(exponents, dtype=np.float64)[:, None]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("k", [128, 256, 640, 7168, 16384])
+def test_norm_rows_at_the_top_of_the_range(k, dtype):
+    """Finite rows whose sum of squares passes FP32's range, up to the type's largest values, beside
+    ordinary ones: the bounds of every other row."""
+    rng = np.random.default_rng(390 + k)
+    x = _spread(rng, k, [0, 57, 60, 64, 100, 120, 122, 124, 126, 127, 128])
+    x[4, 1:] = rng.standard_normal(k - 1)  # one large value alone
+    w = (1 + 0.2 * rng.standard_normal(k)).astype(np.float32)
+    for ue in (False, True):
+        _check(_run(x, w, dtype, ue), dtype, ue, what=f"K={k} {dtype} ue={ue}")
+        _check(_run(0.7 * x, w, dtype, ue, 0.25 * x), dtype, ue, what=f"K={k} {dtype} ue={ue}, residual")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("k", [128, 256, 640, 7168, 16384])
+def test_norm_rows_at_the_bottom_of_the_range(k, dtype):
+    """eps = 0 and rows whose squares are denormal or zero in FP32, down to denormal values: the bounds of
+    every other row.  (1/rms of a row of 2^-135 is past FP32's range and comes back as Inf; y, of the order
+    of 1, is not.  In BF16 that row's values round to zero, and 0 * Inf is NaN on both sides.)"""
+    rng = np.random.default_rng(395 + k)
+    x = _spread(rng, k, [0, -48, -52, -60, -100, -120, -123, -125, -126, -127])
+    w = (1 + 0.2 * rng.standard_normal(k)).astype(np.float32)
+    for ue in (False, True):
+        _check(_run(x, w, dtype, ue, eps=0.0), dtype, ue, eps=0.0, what=f"K={k} {dtype} ue={ue}")
+    o = _run(_spread(rng, k, [0, -135, -130, 3]), w, dtype, eps=0.0)
+    _, _, v = oracle.ref_add_rms_norm(_f64(o["x"]), _f64(o["w"]), 0.0)
+    tol = 2.0 ** -17 if dtype == "fp32" else 2.0 ** -8 + 2.0 ** -16
+    y = _f64(o["y"])
+    assert ((np.abs(y - v) <= tol * np.abs(v)) | (np.isnan(v) & np.isnan(y))).all()
+    assert torch.isinf(o["rstd"]).tolist() == [False, True, True, False]
+
+
+@pytest.mark.parametrize("eps", [float("inf"), 3e38])
+def test_norm_eps_past_the_range(eps):
+    """mean + eps past FP32's range: 1/rms is what the formula gives (0 for an infinite eps)."""
+    x = _spread(np.random.default_rng(397), 256, [0, 60, 64, 127])
+    o = _run(x, np.ones(256, np.float32), "fp32", eps=eps)
+    want = 1 / np.sqrt((_f64(o["x"]) ** 2).mean(1) + float(np.float32(eps)))
+    assert (np.abs(_f64(o["rstd"]) - want) <= 2.0 ** -18 * want).all()
+
+
 # ---- gradient ----
 
 def _run_backward(dy, s, w, rstd, dtype, dres=None, pad=0, wdtype=None, dw0=None, workspace=True):
