@@ -228,6 +228,24 @@ __device__ __forceinline__ float row_sum(float v, float* slot) {
   return sum16(slot[threadIdx.x & 15]);
 }
 
+// A value that is the same on every lane, kept in a scalar register.
+__device__ __forceinline__ float uniform(float v) {
+  return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v)));
+}
+// ss / k with 1/k given, the quotient's error corrected once.
+__device__ __forceinline__ float mean(float ss, float k, float inv_k) {
+  const float q = ss * inv_k;
+  return __builtin_fmaf(__builtin_fmaf(-q, k, ss), inv_k, q);
+}
+// 1 / sqrt(t) for normal t: the hardware's estimate r (1 ulp) and one Newton step r + r (1 - t r^2) / 2, with the
+// rounding error of t r carried along, so that only the last addition rounds.  Every code of a row depends on this
+// one value: with the estimate alone one row in ten is off by an ulp.
+__device__ __forceinline__ float rsqrt(float t) {
+  const float r = __builtin_amdgcn_rsqf(t), a = t * r, e = __builtin_fmaf(t, r, -a);
+  const float d = __builtin_fmaf(-e, r, __builtin_fmaf(-a, r, 1.0f));
+  return __builtin_fmaf(0.5f * r, d, r);
+}
+
 // Codes of eight values of a block whose amax has the bits `amax` (compared as
 // an unsigned integer, so that a NaN is the largest).  The common case takes
 // amax / 448 and x / s with the steps of the correctly rounded division
@@ -338,7 +356,7 @@ __global__ void __launch_bounds__(ROWS > 1 ? 64 : C == 1 ? 512 : kFwdThreads, C 
                           row_off<ROWS>(sub, valid, p.ldr), tid, nt, r);
   };
   load(row0);
-  const float inv_k = 1.0f / (float)p.k;
+  const float k = uniform((float)p.k), inv_k = uniform(1.0f / (float)p.k);
   if (ROWS == 1) __syncthreads();
   for (int row = row0; row < row1; row += ROWS) {
     const bool valid = ROWS == 1 || row + sub < row1;
@@ -360,8 +378,8 @@ __global__ void __launch_bounds__(ROWS > 1 ? 64 : C == 1 ? 512 : kFwdThreads, C 
 #pragma unroll
     for (int c = 0; c < C; ++c) store8<BF16, NT>(ro, row_off<ROWS>(sub, valid, p.ldro), c * nt + tid, v[c]);
     ss = row_sum<ROWS>(ss, s_sum[0][row & 1]);
-    const float arg = __builtin_fmaf(ss, inv_k, p.eps);
-    float rstd = __builtin_amdgcn_rsqf(arg), rstd_out = rstd;  // what multiplies the row, and what is stored
+    const float arg = mean(ss, k, inv_k) + p.eps;
+    float rstd = rsqrt(arg), rstd_out = rstd;  // what multiplies the row, and what is stored
     const bool again = !(ss >= 0x1p-100f && arg < __builtin_inff());
     if (ROWS > 1 ? __any(again) : again) {
       // Squares (or the argument) past FP32's range on either side (the same branch on every thread): again,

@@ -386,6 +386,35 @@ def test_norm_eps_past_the_range(eps):
     assert (np.abs(_f64(o["rstd"]) - want) <= 2.0 ** -18 * want).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("k", [128, 256, 1024, 4096, 16384])
+def test_norm_rstd_is_rounded_once(k, dtype):
+    """Rows of small whole numbers: every partial sum of squares is exact in FP32 (< 2^24), so is the mean
+    over a power of two, and with eps = 0 only the root is left: half an ulp, and 0.01 for the higher terms."""
+    rng = np.random.default_rng(398)
+    x = np.stack([rng.integers(-a, a + 1, k) for a in range(1, 31) for _ in range(40)]).astype(np.float64)
+    x[:, 0] = 1
+    o = _run(x, np.ones(k, np.float32), dtype, eps=0.0, want_y=False)
+    want = 1 / np.sqrt((x * x).mean(1))
+    ulp = np.spacing(want.astype(np.float32)).astype(np.float64)
+    err = np.abs(_f64(o["rstd"]) - want) / ulp
+    assert (err <= 0.51).all(), f"{int((err > 0.51).sum())} of {len(err)} rows, worst {err.max():.3f} ulp"
+
+
+@pytest.mark.parametrize("k", [640, 7168])
+def test_norm_rstd_with_a_rounded_mean(k):
+    """The same sums over other widths and with eps: the mean and its sum with eps are rounded too, at most
+    2^-24 each and halved by the root."""
+    rng = np.random.default_rng(399)
+    x = np.stack([rng.integers(-a, a + 1, k) for a in range(1, 31) for _ in range(40)]).astype(np.float64)
+    x[:, 0] = 1
+    o = _run(x, np.ones(k, np.float32), "fp32", eps=1e-6, want_y=False)
+    want = 1 / np.sqrt((x * x).mean(1) + float(np.float32(1e-6)))
+    ulp = np.spacing(want.astype(np.float32)).astype(np.float64)
+    err = np.abs(_f64(o["rstd"]) - want)
+    assert (err <= 0.51 * ulp + 2.0 ** -24 * want).all()
+
+
 # ---- gradient ----
 
 def _run_backward(dy, s, w, rstd, dtype, dres=None, pad=0, wdtype=None, dw0=None, workspace=True):
