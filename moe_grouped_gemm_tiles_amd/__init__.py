@@ -714,8 +714,12 @@ class _Tensor(ctypes.Structure):
 
 
 class TensorList:
-    """The descriptors of a list of contiguous BF16 / FP32 tensors on one GPU, made once and kept
-    as long as the tensors themselves (it holds references to them)."""
+    """The descriptors of a list of contiguous BF16 / FP32 tensors on one GPU, made once.  It holds
+    references to the tensors, and is good for as long as each of them keeps its storage: every use
+    checks their addresses and sizes (0.2 us a tensor) and raises ValueError where ``t.data = ...``,
+    ``set_`` or ``resize_`` has given one another.  It knows nothing of other tensors that take their
+    place: gradients that a backward pass makes anew (after ``zero_grad(set_to_none=True)``, torch's
+    default) need a new list, or plain lists, each step."""
 
     def __init__(self, tensors):
         self.tensors = list(tensors)
@@ -727,6 +731,10 @@ class TensorList:
             if t.get_device() != self.dev or not t.is_contiguous():
                 raise ValueError("tensors must be contiguous and on one device")
             d.data, d.numel, d.dtype = t.data_ptr(), t.numel(), _DTYPES[t.dtype]
+        self._places = self._now()
+
+    def _now(self):
+        return list(map(torch.Tensor.data_ptr, self.tensors)), list(map(torch.Tensor.numel, self.tensors))
 
     def __len__(self):
         return len(self.tensors)
@@ -737,6 +745,15 @@ def tensor_list(tensors) -> TensorList:
     return TensorList(tensors)
 
 
+def _described(tensors, name: str) -> TensorList:
+    """A list of tensors as a ``TensorList``; one that was made earlier has to describe its tensors still."""
+    if not isinstance(tensors, TensorList):
+        return TensorList(tensors)
+    if tensors._now() != tensors._places:
+        raise ValueError(f"{name}: a tensor's storage or size has changed since its TensorList was made")
+    return tensors
+
+
 def alloc_clip_workspace(device=None) -> torch.Tensor:
     """A workspace for ``clip_grad_norm`` (any contents)."""
     size = int(load_library().dg_get_clip_workspace_size())
@@ -745,9 +762,10 @@ def alloc_clip_workspace(device=None) -> torch.Tensor:
 
 def clip_grad_norm(grads, max_norm: float, norm: torch.Tensor, out=None, workspace: torch.Tensor | None = None):
     """norm[0] = sqrt(sum of all squares) and out = grads * min(1, max_norm / (norm + 1e-6)); without
-    ``out`` in place.  grads and out: lists of tensors, or a ``TensorList`` kept between calls."""
+    ``out`` in place.  grads and out: lists of tensors, or a ``TensorList`` kept between calls for tensors
+    that keep their storage (gradients that are zeroed, not made anew)."""
     lib = _lib or load_library()
-    grads = grads if isinstance(grads, TensorList) else TensorList(grads)
+    grads = _described(grads, "grads")
     dev = norm.get_device()
     if norm.dtype is not torch.float32 or dev < 0 or norm.numel() != 1:
         raise TypeError("norm must be a float32 GPU tensor with one element")
@@ -756,7 +774,7 @@ def clip_grad_norm(grads, max_norm: float, norm: torch.Tensor, out=None, workspa
         raise ValueError("grads must be on norm's device")
     table = None
     if out is not None:
-        out = out if isinstance(out, TensorList) else TensorList(out)
+        out = _described(out, "out")
         if len(out.tensors) != n or (n and out.dev != dev):
             raise ValueError("out must have as many tensors as grads, on norm's device")
         table = out.table

@@ -183,3 +183,45 @@ def test_clip_large_with_empty_tensors_at_the_end():
     assert abs(float(norm) - want) <= 2.0 ** -22 * want
     ref = data.double() / (want + 1e-6)
     assert bool(((lists[1].tensors[0].double() - ref).abs() <= 2.0 ** -21 * ref.abs()).all())
+
+
+def _replace_data(t):
+    t.data = torch.ones(t.numel(), dtype=t.dtype, device="cuda:0")
+
+
+CHANGES = {
+    "data replaced": _replace_data,
+    "set to another storage": lambda t: t.set_(torch.ones(t.numel(), dtype=t.dtype, device="cuda:0")),
+    "grown": lambda t: t.resize_(t.numel() * 64),
+    "shrunk in place": lambda t: t.resize_(t.numel() - 1),
+    "narrowed": lambda t: setattr(t, "data", t.data[:-2]),
+}
+
+
+@pytest.mark.parametrize("role", ["grads", "out"])
+@pytest.mark.parametrize("how", list(CHANGES))
+def test_clip_refuses_a_list_whose_tensors_have_moved(how, role):
+    """Descriptors made before a tensor got another storage or size are not used: the call raises and
+    launches nothing.  A new list over the same tensors works."""
+    sets = {n: _grads([300, 5000, 40], ["fp32", "bf16", "fp32"], 790) for n in ("grads", "out")}
+    lists = {n: dg.tensor_list(t) for n, t in sets.items()}
+    norm = _norm()
+    dg.clip_grad_norm(lists["grads"], 0.5, norm, out=lists["out"])  # as made
+    dg.clip_grad_norm(lists["grads"], 0.5, norm, out=lists["out"])
+    before = float(norm)
+    kept = [t.clone() for t in sets["grads"]]
+    norm.fill_(-1.0)
+    CHANGES[how](sets[role][1])
+    with pytest.raises(ValueError, match=role):
+        dg.clip_grad_norm(lists["grads"], 0.5, norm, out=lists["out"])
+    if role == "grads":
+        with pytest.raises(ValueError, match=role):
+            dg.clip_grad_norm(lists["grads"], 0.5, norm)
+    torch.cuda.synchronize()
+    assert float(norm) == -1.0
+    for i in (0, 2):
+        assert torch.equal(sets["grads"][i], kept[i])
+    sets[role][1].resize_(5000).copy_(kept[1] if role == "out" else _grads([5000], ["bf16"], 791)[0])
+    dg.clip_grad_norm(dg.tensor_list(sets["grads"]), 0.5, norm, out=dg.tensor_list(sets["out"]))
+    _check(sets["grads"], 0.5, norm, sets["out"], how)
+    assert before > 0.5
