@@ -225,3 +225,65 @@ def test_clip_refuses_a_list_whose_tensors_have_moved(how, role):
     dg.clip_grad_norm(dg.tensor_list(sets["grads"]), 0.5, norm, out=dg.tensor_list(sets["out"]))
     _check(sets["grads"], 0.5, norm, sets["out"], how)
     assert before > 0.5
+
+
+def _check_large(grads, kept, max_norm, norm, out, what):
+    """The bounds of the small sets, with FP64 sums on the GPU; ``kept`` are the gradients as they were."""
+    want = math.sqrt(sum(float(g.double().square().sum()) for g in kept))
+    assert abs(float(norm) - want) <= 2.0 ** -22 * want, what
+    c = min(1.0, max_norm / (want + 1e-6))
+    for i, (g, o) in enumerate(zip(kept, out)):
+        ref = g.double() * c
+        tol = 2.0 ** -21 if o.dtype == torch.float32 else 2.0 ** -8 + 2.0 ** -20
+        assert bool(((o.double() - ref).abs() <= tol * ref.abs() + 1e-38).all()), f"{what}: tensor {i}"
+
+
+def _large_set(kind, shift):
+    """360 to 460 MB in 150 tensors, two launches; each tensor starts ``shift`` elements into its own buffer."""
+    gen = torch.Generator(device="cuda:0").manual_seed(780 + shift)
+    sizes = [20_000_003, 0, 13_000_001, 1, 4097] + [(i * 7919) % 90_000 + 1 for i in range(140)] + [14_999_999] * 5
+    grads = []
+    for i, n in enumerate(sizes):
+        half = kind == "bf16" or (kind == "mixed" and i % 2 == 1)
+        n = 2 * n if kind == "bf16" else n
+        t = torch.randn(n + 8, device="cuda:0", generator=gen)
+        grads.append((t.bfloat16() if half else t)[shift:shift + n])
+    return grads
+
+
+@pytest.mark.parametrize("shift", [0, 3])
+@pytest.mark.parametrize("kind", ["fp32", "bf16", "mixed"])
+def test_clip_past_the_last_level_cache(kind, shift):
+    """More than 256 MiB over two launches, so that the first pass streams and then stops streaming: out of
+    place (inputs and outputs that start alike and differently), in place, and in place with nothing to clip."""
+    grads = _large_set(kind, shift)
+    size = sum(g.numel() * g.element_size() for g in grads)
+    assert size > (256 << 20) + (32 << 20) and len(grads) > 128
+    norm = _norm()
+    for back in (shift, 1):
+        out = [torch.full((g.numel() + 8,), float("nan"), dtype=g.dtype, device="cuda:0")[back:back + g.numel()]
+               for g in grads]
+        dg.clip_grad_norm(grads, 0.5, norm, out=out)
+        _check_large(grads, grads, 0.5, norm, out, f"{kind}, starts {shift} and {back}")
+    whole = [g.as_strided((g.numel() + 8,), (1,), 0).clone() for g in grads]
+    mine = [t[shift:shift + g.numel()] for t, g in zip(whole, grads)]
+    dg.clip_grad_norm(mine, 1e9, norm)
+    assert all(torch.equal(a, b) for a, b in zip(mine, grads)), "a factor of 1"
+    dg.clip_grad_norm(mine, 0.5, norm)
+    _check_large(mine, grads, 0.5, norm, mine, f"{kind}, in place")
+    assert all(torch.equal(a, b) for a, b in zip(mine, out)), "in place and out of place"
+    for t, g in zip(whole, grads):
+        full = g.as_strided((g.numel() + 8,), (1,), 0)
+        assert torch.equal(t[:shift], full[:shift]) and torch.equal(t[shift + g.numel():], full[shift + g.numel():])
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16", "mixed"])
+def test_clip_streamed_sets_below_the_last_level_cache(kind):
+    """Between 32 and 256 MiB, one launch: in place and out of place."""
+    grads = _large_set(kind, 0)[2:100]
+    assert 32 << 20 < sum(g.numel() * g.element_size() for g in grads) < 256 << 20
+    out, mine, norm = [torch.empty_like(g) for g in grads], [g.clone() for g in grads], _norm()
+    dg.clip_grad_norm(grads, 2.0, norm, out=out)
+    _check_large(grads, grads, 2.0, norm, out, kind)
+    dg.clip_grad_norm(mine, 2.0, norm)
+    assert all(torch.equal(a, b) for a, b in zip(mine, out))
