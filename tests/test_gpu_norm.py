@@ -474,6 +474,28 @@ def test_gradient_narrow_rows(k, dtype):
         _check_backward(_run_backward(dy, s, w, rstd, dtype, dres, pad=16), dtype, what=f"{m}x{k} {dtype}")
 
 
+@pytest.mark.parametrize("skip", [False, True])
+@pytest.mark.parametrize("m,k", [(300, 16384), (1000, 8320), (1500, 7168), (150, 16384), (230, 12416)])
+def test_gradient_long_fp32_rows_in_turns(m, k, skip):
+    """FP32 rows past 4096 and past 8192 values in several turns per workgroup, operands above and below
+    32 MiB; every value of dx and dw against FP64."""
+    gen = torch.Generator(device="cuda:0").manual_seed(450 + m)
+    dy, s, dres = (torch.randn(m, k, device="cuda:0", generator=gen) for _ in range(3))
+    w = 1 + 0.2 * torch.randn(k, device="cuda:0", generator=gen)
+    rstd = torch.rsqrt(s.double().square().mean(1) + 1e-6).float()
+    dx, dw = torch.full_like(dy, float("nan")), torch.full_like(w, float("nan"))
+    dg.rms_norm_backward(dy, s, w, rstd, dx, dw, dresidual=dres if skip else None)
+    r = rstd.double()[:, None]
+    xhat, g = s.double() * r, dy.double() * w.double()
+    want = r * (g - xhat * (g * xhat).mean(1, keepdim=True))
+    terms = r * (g.abs() + xhat.abs() * (g * xhat).abs().mean(1, keepdim=True))
+    if skip:
+        want, terms = want + dres.double(), terms + dres.double().abs()
+    assert bool(((dx.double() - want).abs() <= 2.0 ** -16 * terms).all())
+    t = dy.double() * xhat
+    assert bool(((dw.double() - t.sum(0)).abs() <= 2.0 ** -16 * t.abs().sum(0)).all())
+
+
 def test_gradient_strides_accumulation_and_own_workspace():
     dy, s, w, rstd, dres = _grad_inputs(45, 640, 410)
     dw0 = np.random.default_rng(411).standard_normal(640).astype(np.float32)
