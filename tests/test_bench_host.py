@@ -142,3 +142,20 @@ def test_committed_bench_lines_keep_the_output_contract():
     assert base["config"]["workload"] == "baseline" and base["cpu_baseline"] is not None
     assert base["roofline"]["traffic"] is not None
     assert base["steps"] == 5 and base["warmup"] == 2  # the defaults the driver runs
+
+
+def test_traffic_records_are_of_the_current_sources():
+    """The default line's dominant launch, and every case with a profile of its own, has a traffic record
+    that belongs to the kernel sources as they are."""
+    import glob
+
+    base = _last_json_line(os.path.join(ROOT, "profiles", "bench_baseline.json"))
+    labels = {base["roofline"]["kernel_case"]}
+    for path in glob.glob(os.path.join(ROOT, "profiles", "*.md")):
+        with open(path) as f:
+            text = f.read()
+        if "calibrated HBM traffic per launch" in text:
+            labels.add(text.splitlines()[0].split(": ", 1)[1])
+    assert len(labels) >= 10
+    stale = [label for label in sorted(labels) if bench.lookup_traffic(label) is None]
+    assert not stale, stale
