@@ -23,7 +23,9 @@
 //     end at once when nothing is to be clipped;
 //   * the second pass begins with what the first read last: the last 256 MiB, the
 //     size of the last-level cache, are not marked as streaming (12 us less).
-// Together 435 us; 48 ragged tensors of 3.4 MB in all take 8.4 us, two launches.
+// Together 435 us; 48 ragged tensors of 3.4 MB in all take 8.4 us, two launches.  In place the eight
+// tensors take 464 us, and 151 us where nothing is to be clipped; in BF16 (470 MB) 221 and 83 us, out of
+// place 224 us.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>

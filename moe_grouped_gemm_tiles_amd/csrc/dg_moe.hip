@@ -35,12 +35,16 @@
 //     grid rows), about 1.5 us, so there is no planning kernel and no host work.
 //
 // Measured (both kernels, weights not in any cache; reads alone reach 7.0 TB/s):
-//     1 token, 8 of 16 experts of 7168 x 2048       63 us   5.6 TB/s (36 + 22 us of kernels)
-//     9 tokens, top 8 of 64 experts of 4096 x 1024  97 us   5.8 TB/s
-//     64 tokens, top 4 of 16 experts of 7168 x 2048 133 us  5.3 TB/s (a's tiles fill the down
+//     1 token, 8 of 16 experts of 7168 x 2048       60 us   5.9 TB/s (38 + 22 us of kernels)
+//     9 tokens, top 8 of 64 experts of 4096 x 1024  92 us   6.1 TB/s
+//     64 tokens, top 4 of 16 experts of 7168 x 2048 128 us  5.5 TB/s (a's tiles fill the down
 //                                                   kernel's rings: fewer stages in flight)
-//     37 tokens, 32 of 128 experts of 2048 x 1408   51 us   4.5 TB/s (two launches and two
-//                                                   plans are 8 us of it)
+//     37 tokens, 32 of 128 experts of 2048 x 1408   47 us   4.9 TB/s (the down kernel 3.9: a
+//                                                   workgroup's 8 columns bring in half as much
+//                                                   of a as of W2)
+// Where every workgroup's rows of a outweigh its columns of W2 (small layers, or few experts with
+// many tokens each) the layer is far from its bytes: 20 tokens, top 8 of 10 experts of 1280 x 1152
+// take 27 us (13 + 16 us of kernels) for 6 us of weights.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

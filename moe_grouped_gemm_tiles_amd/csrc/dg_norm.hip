@@ -22,12 +22,12 @@
 //   * workgroups run through memory together.  With one or two rows per workgroup
 //     the forward takes 276 us, with 4 297 us, with 16 336 us: the more regions are
 //     being read at once, the less HBM delivers.  The backward, whose workgroups
-//     persist to keep their column sums, is best with at most one per CU and a
-//     few MiB of rows in flight: 208 workgroups 316 us, 256 331 us, 512 354 us,
-//     1024 357 us;
+//     persist to keep their column sums, is best with a few MiB of rows in flight: 208
+//     workgroups for rows of 8 KiB and more (316 us; 256 331 us, 512 354 us, 1024
+//     357 us), a multiple of 208 for shorter ones (bwd_grid), up to 1664 for 128 columns;
 //   * FP32 rows are split so that every load instruction reads 256 adjacent bytes per
 //     16 lanes: 29000 x 4096 backward 343 -> 306 us, 4099 x 4096 forward 34 -> 29.5 us.
-// 33280 x 7168 BF16 now: forward 276 us, 6.07 TB/s; backward 316 us, 6.05 TB/s.
+// 33280 x 7168 BF16 now: forward 274 us, 6.1 TB/s; backward 313 us, 6.1 TB/s.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

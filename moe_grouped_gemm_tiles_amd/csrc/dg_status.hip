@@ -25,7 +25,9 @@ const char* dg_status_string(dg_status s) {
   switch (s) {
     case DG_SUCCESS: return "DG_SUCCESS";
     case DG_ERROR_INVALID_VALUE: return "DG_ERROR_INVALID_VALUE: invalid argument (pointer, alignment, stride, size or dtype)";
-    case DG_ERROR_NOT_SUPPORTED: return "DG_ERROR_NOT_SUPPORTED: shape not supported (K % 128 != 0 or contiguous M % 128 != 0)";
+    case DG_ERROR_NOT_SUPPORTED:
+      return "DG_ERROR_NOT_SUPPORTED: shape not supported (K % 128 != 0, contiguous M % 128 != 0, or a "
+             "limit of the entry point, see dg.h)";
     case DG_ERROR_LAUNCH_FAILED: return "DG_ERROR_LAUNCH_FAILED: a HIP call failed";
     case DG_ERROR_SCRATCH_LIMIT:
       return "DG_ERROR_SCRATCH_LIMIT: the call needs more split-K scratch than the allocation-free entry point "
