@@ -474,6 +474,17 @@ def test_gradient_narrow_rows(k, dtype):
         _check_backward(_run_backward(dy, s, w, rstd, dtype, dres, pad=16), dtype, what=f"{m}x{k} {dtype}")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("k", [128, 256, 640, 16384])
+def test_gradient_of_rows_at_the_ends_of_the_range(k, dtype):
+    """Rows up to the type's largest values (1/rms denormal) and, with eps = 0, down to 2^-120."""
+    rng = np.random.default_rng(460 + k)
+    s = _spread(rng, k, [0, 60, 64, 121, 126, 127, 128, -60, -100, -120])
+    rstd = (1 / np.sqrt((s * s).mean(1))).astype(np.float32)
+    w = 1 + 0.2 * rng.standard_normal(k)
+    _check_backward(_run_backward(rng.standard_normal(s.shape), s, w, rstd, dtype), dtype, what=f"K={k} {dtype}")
+
+
 @pytest.mark.parametrize("skip", [False, True])
 @pytest.mark.parametrize("m,k", [(300, 16384), (1000, 8320), (1500, 7168), (150, 16384), (230, 12416)])
 def test_gradient_long_fp32_rows_in_turns(m, k, skip):
