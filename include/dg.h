@@ -78,6 +78,8 @@ typedef enum {
 
 typedef enum { DG_DTYPE_BF16 = 0, DG_DTYPE_FP32 = 1 } dg_dtype;
 
+typedef enum { DG_SCORE_SOFTMAX = 0, DG_SCORE_SIGMOID = 1 } dg_score;
+
 /*
  * Dense GEMM: D[M,N] = C[M,N] + A[M,K] @ B[N,K]^T.
  *   [README] "Interfaces > Notices" (fp8_gemm_nt computes D = C + A @ B.T) and
@@ -442,6 +444,118 @@ typedef struct {
 dg_status dg_clip_grad_norm(const dg_tensor* grads, const dg_tensor* out, int num_tensors, float max_norm, float* norm,
                             void* workspace, size_t workspace_bytes, hipStream_t stream);
 size_t dg_get_clip_workspace_size(void);
+
+/*
+ * Microscaled 4-bit operands (OCP MXFP4): E2M1 codes, two to a byte along K (the
+ * even value in the low four bits), one E8M0 scale for each row and 32 consecutive
+ * K values.  The scales are packed like the UE8M0 forms' sfa, four bytes to a word
+ * along K and transposed: byte j (least significant first) of sf[q * ld_sf + r]
+ * scales row r's values 128 q + 32 j .. + 31; 255 is NaN.
+ *
+ * dg_cast_to_mxfp4: the quantisation, for activations and weights alike.
+ *   s = the smallest power of two with amax <= 6 s (1 for a block of zeros; never
+ *   below 2^-127), code = E2M1(x / s) to nearest with ties to even.  A block that
+ *   holds an Inf or NaN gets the scale 255 and zero codes.
+ *
+ * x          [num_groups][m][k], BF16 or FP32, row stride ldx, 16-B aligned rows;
+ *            groups follow each other (m * ldx apart, and likewise below).
+ * q          [num_groups][m][k / 2] bytes, row stride ldq (a multiple of 4), 4-B aligned.
+ * sf         [num_groups][k / 128][ld_sf] words, ld_sf >= m.
+ * y          optional [num_groups][m][k], x's dtype: the values that codes and scales
+ *            stand for (exact), for a straight-through forward; NaN in blocks with
+ *            scale 255, Inf for 2^128, to which inputs past 3.5 * 2^126 round.  May equal x.
+ * masked_m   optional DEVICE int32 [num_groups]: only the first masked_m[g] rows of a
+ *            group are read and written (clamped to [0, m]).
+ * k % 128 != 0 or more than 65535 groups -> DG_ERROR_NOT_SUPPORTED; an empty size ->
+ * DG_SUCCESS.
+ */
+dg_status dg_cast_to_mxfp4(const void* x, int64_t ldx, dg_dtype x_dtype, void* q, int64_t ldq, int32_t* sf,
+                           int64_t ld_sf, void* y, int64_t ldy, const int32_t* masked_m, int num_groups, int m, int k,
+                           hipStream_t stream);
+
+/*
+ * GEMMs of two such operands, D = C + A @ B^T: dense, M-grouped contiguous and
+ * M-grouped masked.  As the FP8 forms above (which rows are written, what C may be,
+ * how groups are given), with these differences:
+ *   a, b       bytes of two codes: rows of k / 2 bytes; lda, ldb in bytes, multiples of
+ *              16, at least k / 2.
+ *   sfa, sfb   scale words [k / 128][ld_sfa], [k / 128][ld_sfb] (masked / grouped: one
+ *              such array per group), ld_sfa >= rows of A, ld_sfb >= n, both multiples
+ *              of 4, 16-B aligned.
+ *   workspace  dg_get_mxfp4_workspace_size(m, n, k) bytes for the dense form, as
+ *              described at the top.
+ * A block whose scale is 255 makes its row of A (of B: its column of D) NaN.
+ * All of K accumulates in the matrix cores' FP32; C is added in FP32 and D rounded
+ * once.  The same bits every time for a shape and CU count.
+ */
+dg_status dg_mxfp4_gemm_nt(const void* a, int64_t lda, const int32_t* sfa, int64_t ld_sfa, const void* b, int64_t ldb,
+                           const int32_t* sfb, int64_t ld_sfb, const void* c, int64_t ldc, void* d, int64_t ldd,
+                           dg_dtype d_dtype, int m, int n, int k, void* workspace, size_t workspace_bytes,
+                           hipStream_t stream);
+size_t dg_get_mxfp4_workspace_size(int m, int n, int k);
+dg_status dg_m_grouped_mxfp4_gemm_nt_contiguous(const void* a, const int32_t* sfa, int64_t ld_sfa, const void* b,
+                                                const int32_t* sfb, int64_t ld_sfb, void* d, dg_dtype d_dtype,
+                                                const int32_t* m_indices, int m_total, int n, int k, int num_groups,
+                                                hipStream_t stream);
+dg_status dg_m_grouped_mxfp4_gemm_nt_masked(const void* a, const int32_t* sfa, int64_t ld_sfa, const void* b,
+                                            const int32_t* sfb, int64_t ld_sfb, void* d, dg_dtype d_dtype,
+                                            const int32_t* masked_m, int num_groups, int m_max, int n, int k,
+                                            int expected_m, hipStream_t stream);
+
+/*
+ * The router in front of an expert layer: scores, the choice of top_k experts for
+ * each row, their weights, rows per expert and the balance loss.  For a row x of
+ * logits:
+ *   p      = softmax(x) or sigmoid(x)
+ *   ids    = the experts of the top_k largest keys, largest first, ties to the lower
+ *            index; key = x without a bias, p + bias (compared as in FP64) with one
+ *   w_j    = scale * p_j / (sum of the chosen p + 1e-20) if normalize, else scale * p_j
+ *   share  = p (softmax), p / (sum of all p + 1e-20) (sigmoid)
+ *   counts[e] = rows that chose e,  prob_sum[e] = sum over rows of share[e]
+ *   loss   = num_experts * sum_e counts[e] * prob_sum[e] / (sum counts * sum prob_sum)
+ *            (1 when every expert is chosen equally often; 0 where nothing is chosen)
+ * An expert whose logit is -inf (or whose key is -inf or NaN) is never chosen; slots
+ * without an expert get id -1 and weight 0, as do all slots of a masked row, which
+ * adds nothing to counts and prob_sum.  A NaN or +inf logit gives the NaNs that the
+ * formulas give; ids are in range whatever the logits.
+ *
+ * logits        [m, num_experts], BF16 or FP32, row stride ld, aligned to its type.
+ * bias          optional FP32 [num_experts]; steers the choice only.
+ * mask          optional bytes [m]: 0 = padding, no row of the batch.
+ * topk_ids      int32 [m, top_k] contiguous, topk_weights FP32 [m, top_k] contiguous.
+ * counts        optional int32 [num_experts] (masked_m of a masked GEMM).
+ * prob_sum, loss  optional FP32 [num_experts], [1]; both or none, and with counts.
+ * workspace     dg_get_moe_router_workspace_size(m, num_experts) bytes, 256-byte
+ *               aligned, any contents; only where counts are asked for.
+ * num_experts in [1, 1024], top_k in [1, min(64, num_experts)], else
+ * DG_ERROR_NOT_SUPPORTED; scale >= 0.  m == 0 writes zeros to counts, prob_sum, loss.
+ * The same bits every time.
+ */
+dg_status dg_moe_router(const void* logits, int64_t ld, dg_dtype dtype, const float* bias, const void* mask, dg_score score,
+                        int normalize, float scale, int32_t* topk_ids, float* topk_weights, int32_t* counts, float* prob_sum,
+                        float* loss, int m, int num_experts, int top_k, void* workspace, size_t workspace_bytes,
+                        hipStream_t stream);
+size_t dg_get_moe_router_workspace_size(int m, int num_experts);
+
+/*
+ * Gradient of the router: of the weights (dweights) and of the balance loss (dloss).
+ * The choice, counts and bias have none.  With g_e = dloss * num_experts * counts[e] /
+ * (sum counts * sum prob_sum), the gradient of the loss by share[e] up to a constant
+ * that the normalisation of share cancels:
+ *   dlogits = d(sum_j dweights_j w_j + sum_e g_e share_e) / dx
+ * counts and prob_sum may be summed over the ranks of a data-parallel group before
+ * the call: then this is a rank's part of the gradient of the whole batch's loss.
+ *
+ * topk_ids      the forward's; slots outside [0, num_experts) have no gradient, and a
+ *               row without any (a masked one) gets zeros.
+ * counts, prob_sum, dloss (FP32 [1])  all or none.
+ * dlogits       [m, num_experts], logits' dtype, row stride ld_dlogits; may equal logits.
+ * Sizes as above.
+ */
+dg_status dg_moe_router_backward(const void* logits, int64_t ld, dg_dtype dtype, dg_score score, int normalize, float scale,
+                                 const int32_t* topk_ids, const float* dweights, const int32_t* counts,
+                                 const float* prob_sum, const float* dloss, void* dlogits, int64_t ld_dlogits, int m,
+                                 int num_experts, int top_k, hipStream_t stream);
 
 /*
  * Weighted-ReLU MQA logits (the lightning-indexer scoring kernel, non-paged).

@@ -24,6 +24,13 @@ as mirrored on the page "Weight gradient kernels for dense and MoE models #95":
   (a whole gated expert layer for a few tokens, two launches)
 * ``clip_grad_norm(grads, max_norm, norm, out)`` (global norm over many tensors
   and clipping by it; ``tensor_list`` keeps the descriptors between calls)
+* ``cast_to_mxfp4(x, q, sf, y, masked_m)`` (microscaled 4-bit quantisation) and the
+  products ``mxfp4_gemm_nt((a, sfa), (b, sfb), d, c, workspace)``,
+  ``m_grouped_mxfp4_gemm_nt_contiguous((a, sfa), (b, sfb), d, m_indices)``,
+  ``m_grouped_mxfp4_gemm_nt_masked((a, sfa), (b, sfb), d, masked_m, expected_m)``
+* ``moe_router(logits, topk_ids, topk_weights, counts, prob_sum, loss, ...)`` (scores,
+  choice of experts, weights, rows per expert, balance loss) and its gradient
+  ``moe_router_backward(logits, topk_ids, dweights, dlogits, counts, prob_sum, dloss, ...)``
 * ``get_mk_alignment_for_contiguous_layout()``, ``get_sf_aligned_size(mn)``,
   ``set_num_cus(n)`` / ``get_num_cus()``, ``get_workspace_size(m, n, k)`` and
   ``alloc_workspace(m, n, k)``
@@ -48,6 +55,12 @@ Operands follow the ``(tensor, scale)`` pair convention of the README:
 With UE8M0 scales, ``sfa`` is int32 ``[ceil(K/512), ld]`` (masked
 ``[G, ceil(K/512), ld]``) and ``sfb`` int32 ``[ceil(N/128), ceil(K/512)]``
 (grouped ``[G, ...]``).
+
+The 4-bit forms take bytes of two E2M1 codes (``torch.uint8`` or
+``torch.float4_e2m1fn_x2``): ``a`` is ``[M, K/2]`` (masked ``[G, M_max, K/2]``), ``b``
+``[N, K/2]`` (grouped ``[G, N, K/2]``), and both scales are int32 words of four E8M0 bytes,
+transposed: ``sfa`` ``[K/128, ld >= M]``, ``sfb`` ``[K/128, ld >= N]`` (with a leading ``G``
+where the operand has one).
 """
 
 from __future__ import annotations
@@ -73,6 +86,15 @@ __all__ = [
     "fp8_moe_few_tokens",
     "get_moe_workspace_size",
     "alloc_moe_workspace",
+    "cast_to_mxfp4",
+    "mxfp4_gemm_nt",
+    "m_grouped_mxfp4_gemm_nt_contiguous",
+    "m_grouped_mxfp4_gemm_nt_masked",
+    "get_mxfp4_workspace_size",
+    "alloc_mxfp4_workspace",
+    "moe_router",
+    "moe_router_backward",
+    "alloc_moe_router_workspace",
     "clip_grad_norm",
     "alloc_clip_workspace",
     "TensorList",
@@ -145,6 +167,19 @@ _SIGNATURES = {
     "dg_fp8_moe_few_tokens_ue8m0": (_i32, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64,
                                            _i32, _i32, _i32, _i32, _i32, _vp, _sz, _vp]),
     "dg_get_moe_workspace_size": (_sz, [_i32, _i32, _i32]),
+    "dg_cast_to_mxfp4": (_i32, [_vp, _i64, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i32, _i32, _i32, _vp]),
+    "dg_mxfp4_gemm_nt": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i32,
+                                _i32, _i32, _i32, _vp, _sz, _vp]),
+    "dg_get_mxfp4_workspace_size": (_sz, [_i32, _i32, _i32]),
+    "dg_m_grouped_mxfp4_gemm_nt_contiguous": (_i32, [_vp, _vp, _i64, _vp, _vp, _i64, _vp, _i32, _vp,
+                                                     _i32, _i32, _i32, _i32, _vp]),
+    "dg_m_grouped_mxfp4_gemm_nt_masked": (_i32, [_vp, _vp, _i64, _vp, _vp, _i64, _vp, _i32, _vp,
+                                                 _i32, _i32, _i32, _i32, _i32, _vp]),
+    "dg_moe_router": (_i32, [_vp, _i64, _i32, _vp, _vp, _i32, _i32, _f, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32,
+                             _vp, _sz, _vp]),
+    "dg_get_moe_router_workspace_size": (_sz, [_i32, _i32]),
+    "dg_moe_router_backward": (_i32, [_vp, _i64, _i32, _i32, _i32, _f, _vp, _vp, _vp, _vp, _vp, _vp, _i64,
+                                      _i32, _i32, _i32, _vp]),
     "dg_clip_grad_norm": (_i32, [_vp, _vp, _i32, _f, _vp, _vp, _sz, _vp]),
     "dg_get_clip_workspace_size": (_sz, []),
     "dg_transform_sf_into_required_layout": (_i32, [_vp, _vp, _i32, _i32, _i32, _i64, _i32, _vp]),
@@ -783,6 +818,252 @@ def clip_grad_norm(grads, max_norm: float, norm: torch.Tensor, out=None, workspa
     if st:
         _check(st)
     return norm
+
+
+def _fp4(t: torch.Tensor, dev: int, ndim: int, name: str):
+    """(pointer, bytes between rows) of an operand of packed 4-bit codes."""
+    if t.dtype is not torch.uint8 and t.dtype is not torch.float4_e2m1fn_x2:
+        raise TypeError(f"{name} must be bytes of two E2M1 codes (uint8 or float4_e2m1fn_x2), got {t.dtype}")
+    if t.get_device() != dev or t.dim() != ndim:
+        raise ValueError(f"{name} must be a {ndim}-D tensor on the output's device")
+    if t.is_contiguous():
+        return t.data_ptr(), t.shape[-1]
+    if ndim != 2 or not _unit_last_stride(t):
+        raise ValueError(f"{name} must be contiguous" + (" in its last dimension" if ndim == 2 else ""))
+    return t.data_ptr(), _ld(t, 0, 16)
+
+
+def _fp4_scales(sf: torch.Tensor, dev: int, lead, kw: int, rows: int, name: str):
+    """(pointer, words between scale rows) of packed scales [*lead, kw, ld >= rows]."""
+    shape = tuple(sf.shape)
+    if sf.dtype is not torch.int32:
+        raise TypeError(f"{name} must be int32 words of four E8M0 scales")
+    if sf.get_device() != dev or shape[:-1] != (*lead, kw) or shape[-1] < rows:
+        raise ValueError(f"{name} shape {shape} does not fit {(*lead, kw)} scale words of {rows} rows")
+    if lead:
+        _dense_contig(sf, name)
+        return sf.data_ptr(), shape[-1]
+    if not _unit_last_stride(sf):
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return sf.data_ptr(), _ld(sf, 0, 4)
+
+
+def cast_to_mxfp4(x: torch.Tensor, q: torch.Tensor, sf: torch.Tensor, y: torch.Tensor | None = None,
+                  masked_m: torch.Tensor | None = None):
+    """Microscaled 4-bit cast of x [M, K] (or [G, M, K]): q [..., M, K/2] bytes of two E2M1 codes, sf int32
+    [..., K/128, ld >= M] packed E8M0 scales of 32 values each, the operands of the mxfp4 GEMMs.  ``y``: the
+    values they stand for, in x's dtype (for a straight-through forward; may be x).  ``masked_m`` int32 [G]:
+    rows of each group that are there; the others are neither read nor written."""
+    lib = _lib or load_library()
+    dtype, dev, shape = x.dtype, x.get_device(), x.shape
+    code, nd = _DTYPES.get(dtype), len(shape)
+    if code is None or dev < 0 or nd not in (2, 3):
+        raise TypeError("x must be a 2-D or 3-D bfloat16 or float32 GPU tensor")
+    g, (m, k) = (1 if nd == 2 else shape[0]), shape[-2:]
+    if nd == 2:
+        xp, ldx = _like(x, dtype, dev, shape, "x")
+    else:
+        xp, ldx = _flat(x, dtype, dev, shape, "x"), k
+    lead = tuple(shape[:-2])
+    qp, ldq = _fp4(q, dev, nd, "q")
+    if tuple(q.shape) != (*lead, m, k // 2) or k % 2:
+        raise ValueError(f"q shape {tuple(q.shape)} does not fit x {tuple(shape)}")
+    sfp, ld_sf = _fp4_scales(sf, dev, lead, k // 128, m, "sf")
+    yp, ldy, mp = None, 0, None
+    if y is not None:
+        yp, ldy = _like(y, dtype, dev, shape, "y") if nd == 2 else (_flat(y, dtype, dev, shape, "y"), k)
+    if masked_m is not None:
+        if nd != 3:
+            raise ValueError("masked_m goes with a 3-D x")
+        mp = _flat(masked_m, torch.int32, dev, shape[:1], "masked_m")
+    st = lib.dg_cast_to_mxfp4(xp, ldx, code, qp, ldq, sfp, ld_sf, yp, ldy, mp, g, m, k, _stream(x))
+    if st:
+        _check(st)
+    return q, sf
+
+
+def get_mxfp4_workspace_size(m: int, n: int, k: int) -> int:
+    """Bytes of workspace a dense ``mxfp4_gemm_nt`` needs on the current device (0: none)."""
+    return int(load_library().dg_get_mxfp4_workspace_size(m, n, k))
+
+
+def alloc_mxfp4_workspace(m: int, n: int, k: int, device=None) -> torch.Tensor | None:
+    """A zero-filled workspace for ``mxfp4_gemm_nt`` of these sizes (None when it needs none).  Keep it and pass
+    it to every call of that shape; calls sharing it must not overlap."""
+    size = get_mxfp4_workspace_size(m, n, k)
+    if size == 0:
+        return None
+    return torch.zeros(size, dtype=torch.uint8, device=device if device is not None else torch.cuda.current_device())
+
+
+def mxfp4_gemm_nt(a_pair, b_pair, d: torch.Tensor, c: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """D = C + A @ B.T with A [M, K], B [N, K] microscaled 4-bit operands (``cast_to_mxfp4``), D BF16 or FP32.
+    ``workspace``: ``alloc_mxfp4_workspace``'s, or None."""
+    lib = _lib or load_library()
+    (a, sfa), (b, sfb) = a_pair, b_pair
+    dev, es = d.get_device(), d.element_size()
+    dt = _out(d)
+    ap, lda = _fp4(a, dev, 2, "a")
+    bp, ldb = _fp4(b, dev, 2, "b")
+    m, kh = a.shape
+    n = b.shape[0]
+    if b.shape[1] != kh or d.shape != (m, n):
+        raise ValueError(f"shape mismatch: a {tuple(a.shape)}, b {tuple(b.shape)}, d {tuple(d.shape)}")
+    kw = kh // 64
+    sfap, ld_sfa = _fp4_scales(sfa, dev, (), kw, m, "sfa")
+    sfbp, ld_sfb = _fp4_scales(sfb, dev, (), kw, n, "sfb")
+    cp, ldc = None, 0
+    if c is not None:
+        if c.dtype != d.dtype or c.shape != d.shape or not _unit_last_stride(c) or c.get_device() != dev:
+            raise ValueError("c must match d's dtype, shape and device")
+        cp, ldc = c.data_ptr(), _ld(c, 0, 16 // es)
+    size = lib.dg_get_mxfp4_workspace_size(m, n, 2 * kh)
+    wp, wb = None, 0
+    if size:
+        if workspace is None:
+            workspace = torch.zeros(size, dtype=torch.uint8, device=dev)
+        _, wp, wb = _scratch(workspace, size, dev)
+    st = lib.dg_mxfp4_gemm_nt(ap, lda, sfap, ld_sfa, bp, ldb, sfbp, ld_sfb, cp, ldc, d.data_ptr(), _ld(d, 0, 16 // es), dt,
+                              m, n, 2 * kh, wp, wb, _stream(d))
+    if st:
+        _check(st)
+    return d
+
+
+def m_grouped_mxfp4_gemm_nt_contiguous(a_pair, b_pair, d: torch.Tensor, m_indices: torch.Tensor):
+    """Contiguous-layout M-grouped product of 4-bit operands; rows whose group index is -1 are left unwritten."""
+    lib = _lib or load_library()
+    (a, sfa), (b, sfb) = a_pair, b_pair
+    dev = d.get_device()
+    dt = _out(d)
+    _dense_contig(a, "a")
+    _dense_contig(d, "d")
+    ap, _ = _fp4(a, dev, 2, "a")
+    bp, _ = _fp4(b, dev, 3, "b")
+    m_total, kh = a.shape
+    g, n = b.shape[:2]
+    if b.shape[2] != kh or d.shape != (m_total, n):
+        raise ValueError("shape mismatch")
+    sfap, ld_sfa = _fp4_scales(sfa, dev, (), kh // 64, m_total, "sfa")
+    sfbp, ld_sfb = _fp4_scales(sfb, dev, (g,), kh // 64, n, "sfb")
+    ip = _flat(m_indices, torch.int32, dev, (m_total,), "m_indices")
+    st = lib.dg_m_grouped_mxfp4_gemm_nt_contiguous(ap, sfap, ld_sfa, bp, sfbp, ld_sfb, d.data_ptr(), dt, ip, m_total, n,
+                                                   2 * kh, g, _stream(d))
+    if st:
+        _check(st)
+    return d
+
+
+def m_grouped_mxfp4_gemm_nt_masked(a_pair, b_pair, d: torch.Tensor, masked_m: torch.Tensor, expected_m: int = 0):
+    """Masked-layout M-grouped product of 4-bit operands; rows at or beyond masked_m[g] are left unwritten."""
+    lib = _lib or load_library()
+    (a, sfa), (b, sfb) = a_pair, b_pair
+    dev = d.get_device()
+    dt = _out(d)
+    _dense_contig(d, "d")
+    ap, _ = _fp4(a, dev, 3, "a")
+    bp, _ = _fp4(b, dev, 3, "b")
+    g, m_max, kh = a.shape
+    n = b.shape[1]
+    if b.shape != (g, n, kh) or d.shape != (g, m_max, n):
+        raise ValueError("shape mismatch")
+    sfap, ld_sfa = _fp4_scales(sfa, dev, (g,), kh // 64, m_max, "sfa")
+    sfbp, ld_sfb = _fp4_scales(sfb, dev, (g,), kh // 64, n, "sfb")
+    mp = _flat(masked_m, torch.int32, dev, (g,), "masked_m")
+    st = lib.dg_m_grouped_mxfp4_gemm_nt_masked(ap, sfap, ld_sfa, bp, sfbp, ld_sfb, d.data_ptr(), dt, mp, g, m_max, n,
+                                               2 * kh, int(expected_m), _stream(d))
+    if st:
+        _check(st)
+    return d
+
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _router_input(logits: torch.Tensor, topk_ids: torch.Tensor, score: str):
+    """(dtype code, device index, shape, top_k, pointer, row stride, pointer of the ids, score code)."""
+    dtype, dev, shape = logits.dtype, logits.get_device(), logits.shape
+    code = _DTYPES.get(dtype)
+    if code is None or dev < 0 or len(shape) != 2:
+        raise TypeError("logits must be a 2-D bfloat16 or float32 GPU tensor")
+    sc = _SCORES.get(score)
+    if sc is None:
+        raise ValueError(f"score must be one of {tuple(_SCORES)}, got {score!r}")
+    if topk_ids.dim() != 2:
+        raise ValueError("topk_ids must be [M, top_k]")
+    if not _unit_last_stride(logits):
+        raise ValueError("logits must be contiguous in its last dimension")
+    k = topk_ids.shape[1]
+    return (code, dev, shape, k, logits.data_ptr(), _ld(logits), _flat(topk_ids, torch.int32, dev, (shape[0], k), "topk_ids"),
+            sc)
+
+
+def alloc_moe_router_workspace(m: int, num_experts: int, device=None) -> torch.Tensor:
+    """A workspace for ``moe_router`` of [m, num_experts] logits (any contents)."""
+    size = int(load_library().dg_get_moe_router_workspace_size(m, num_experts))
+    return torch.empty(size, dtype=torch.uint8, device=device if device is not None else torch.cuda.current_device())
+
+
+def moe_router(logits: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Tensor, counts: torch.Tensor | None = None,
+               prob_sum: torch.Tensor | None = None, loss: torch.Tensor | None = None, *, score: str = "softmax",
+               bias: torch.Tensor | None = None, mask: torch.Tensor | None = None, normalize: bool = True,
+               scale: float = 1.0, workspace: torch.Tensor | None = None):
+    """Choice of experts for logits [M, E]: topk_ids int32 [M, top_k] (largest first, -1 where there is none left) and
+    topk_weights FP32 [M, top_k], ``scale`` times the chosen scores, divided by their sum with ``normalize``.
+    ``bias`` FP32 [E] is added to the scores for the choice alone; rows whose ``mask`` (bool [M]) is false are
+    padding.  Optional: counts int32 [E], how often each expert was chosen, and with them prob_sum FP32 [E], the sums
+    of the rows' score shares, and the balance loss FP32 [1], E * sum(counts * prob_sum) / (sum(counts) *
+    sum(prob_sum))."""
+    lib = _lib or load_library()
+    code, dev, shape, k, xp, ld, idp, sc = _router_input(logits, topk_ids, score)
+    m, e = shape
+    wp = _flat(topk_weights, torch.float32, dev, (m, k), "topk_weights")
+    bp = mp = cp = pp = lp = wsp = None
+    wsb = 0
+    if bias is not None:
+        bp = _flat(bias, torch.float32, dev, (e,), "bias")
+    if mask is not None:
+        mp = _flat(mask, torch.bool, dev, (m,), "mask")
+    if (prob_sum is None) != (loss is None) or (loss is not None and counts is None):
+        raise ValueError("prob_sum and loss go together, and with counts")
+    if counts is not None:
+        cp = _flat(counts, torch.int32, dev, (e,), "counts")
+        workspace, wsp, wsb = _scratch(workspace, 0 if workspace is not None
+                                       else lib.dg_get_moe_router_workspace_size(m, e), dev)
+        if loss is not None:
+            pp, lp = _flat(prob_sum, torch.float32, dev, (e,), "prob_sum"), _flat(loss, torch.float32, dev, (1,), "loss")
+    st = lib.dg_moe_router(xp, ld, code, bp, mp, sc, normalize, scale, idp, wp, cp, pp, lp, m, e, k, wsp, wsb,
+                           _stream(logits))
+    if st:
+        _check(st)
+    return topk_ids, topk_weights
+
+
+def moe_router_backward(logits: torch.Tensor, topk_ids: torch.Tensor, dweights: torch.Tensor, dlogits: torch.Tensor,
+                        counts: torch.Tensor | None = None, prob_sum: torch.Tensor | None = None,
+                        dloss: torch.Tensor | None = None, *, score: str = "softmax", normalize: bool = True,
+                        scale: float = 1.0):
+    """Gradient of ``moe_router`` by the logits: dweights FP32 [M, top_k] is that of topk_weights, dloss FP32 [1] that of
+    the balance loss (with the forward's counts and prob_sum, or their sums over data-parallel ranks) -> dlogits
+    [M, E] in logits' dtype (may be logits itself)."""
+    lib = _lib or load_library()
+    code, dev, shape, k, xp, ld, idp, sc = _router_input(logits, topk_ids, score)
+    m, e = shape
+    dwp = _flat(dweights, torch.float32, dev, (m, k), "dweights")
+    if dlogits.dtype is not logits.dtype or dlogits.get_device() != dev or dlogits.shape != shape \
+            or not _unit_last_stride(dlogits):
+        raise ValueError("dlogits must have logits' dtype, device and shape and be contiguous in its last dimension")
+    cp = pp = lp = None
+    if not (counts is None) == (prob_sum is None) == (dloss is None):
+        raise ValueError("counts, prob_sum and dloss go together")
+    if dloss is not None:
+        cp = _flat(counts, torch.int32, dev, (e,), "counts")
+        pp, lp = _flat(prob_sum, torch.float32, dev, (e,), "prob_sum"), _flat(dloss, torch.float32, dev, (1,), "dloss")
+    st = lib.dg_moe_router_backward(xp, ld, code, sc, normalize, scale, idp, dwp, cp, pp, lp, dlogits.data_ptr(),
+                                    _ld(dlogits), m, e, k, _stream(logits))
+    if st:
+        _check(st)
+    return dlogits
 
 
 def transform_sf_into_required_layout(sf: torch.Tensor, ue8m0: bool = False) -> torch.Tensor:

@@ -32,7 +32,8 @@ RES = os.path.join(PKG, "libdg.resources.txt")
 ARCH = "gfx950"
 
 SOURCES = [os.path.join(CSRC, f) for f in ("dg_api.hip", "dg_quant.hip", "dg_mqa.hip", "dg_layout.hip",
-                                             "dg_norm.hip", "dg_moe.hip", "dg_clip.hip", "dg_status.hip")]
+                                             "dg_norm.hip", "dg_moe.hip", "dg_clip.hip", "dg_fp4.hip", "dg_fp4_cast.hip",
+                                             "dg_router.hip", "dg_status.hip")]
 HEADERS = [os.path.join(CSRC, f) for f in ("dg_kernels.hpp", "dg_common.hpp", "dg_cast.hpp")] + [os.path.join(INCLUDE, "dg.h")]
 
 

@@ -1,0 +1,217 @@
+// dg_fp4_cast.hip -- microscaled 4-bit quantisation of GEMM operands on gfx950: E2M1 codes, one
+// power-of-two scale (E8M0) for each row and 32 consecutive K values, the scales written in the
+// layout the MXFP4 GEMMs take.
+//
+//   s    = the smallest power of two with amax <= 6 s (6 = E2M1's largest value; 1 for a block of
+//          zeros), held in [2^-127, 2^127]; a block with an Inf or NaN gets the NaN scale and zero codes
+//   code = E2M1(x / s), nearest, ties to even; x / s is exact, so this is the only rounding
+//   y    = code * s, exact in BF16 (two significant bits)
+//
+// The scale comes from amax's bits alone: amax = 1.f * 2^E is at most 1.5 * 2^(e + 2) for e = E - 2
+// where f <= 0.5 and for e = E - 1 above, which is one addition that carries into the exponent.
+// Largest magnitudes are compared as integers, so that Inf and NaN win.  The codes and y are the
+// conversion instructions with a scale (checked against the definition for every BF16 value and
+// scale byte).
+//
+// HBM-bound: reads 2 or 4 bytes, writes half a byte, 1/32 and, with y, 2 or 4 per value.  A workgroup
+// owns 64 rows x 512 columns; a lane takes 8 values of a row, so a wave reads 1 KiB (BF16) runs, four
+// rows in flight, and a block's amax is two exchanges among four lanes.  The 4 x 64 scale words go
+// through LDS and leave as 256-byte runs of the transposed layout.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "dg.h"
+#include "dg_common.hpp"
+
+namespace {
+
+namespace fp4c {
+
+constexpr int kRows = 64;   // rows per workgroup
+constexpr int kCols = 512;  // columns per workgroup (four scale words)
+constexpr int kBatch = 4;   // rows a wave has in flight
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// v with the lanes of each group of four exchanged by a quad permutation.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
+}
+constexpr int kQuadXor1 = 0xB1, kQuadXor2 = 0x4E, kRowRor4 = 0x124, kRowRor8 = 0x128;
+
+// Eight values as the conversion instructions take them.
+template <bool BF16>
+struct Eight;
+template <>
+struct Eight<true> {
+  uint4 w;
+  __device__ __forceinline__ void load(const uint8_t* p) { w = *reinterpret_cast<const uint4*>(p); }
+  // Bits of the largest magnitude, as FP32.
+  __device__ __forceinline__ uint32_t amax() const {
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+    uint32_t hi = 0, lo = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      hi = max(hi, v[i] & 0x7fff0000u);
+      lo = max(lo, (v[i] << 16) & 0x7fff0000u);
+    }
+    return max(hi, lo);
+  }
+  __device__ __forceinline__ uint32_t codes(float s) const {
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+    uint32_t r = 0;
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2, v[0]), s, 0);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2, v[1]), s, 1);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2, v[2]), s, 2);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2, v[3]), s, 3);
+    return r;
+  }
+  static __device__ __forceinline__ void store_values(uint8_t* p, uint32_t r, float s, bool nan) {
+    uint4 o;
+    o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(r, s, 0));
+    o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(r, s, 1));
+    o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(r, s, 2));
+    o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(r, s, 3));
+    if (nan) o = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
+    *reinterpret_cast<uint4*>(p) = o;
+  }
+};
+template <>
+struct Eight<false> {
+  float4 lo, hi;
+  __device__ __forceinline__ void load(const uint8_t* p) {
+    lo = *reinterpret_cast<const float4*>(p);
+    hi = *(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ uint32_t amax() const {
+    const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    uint32_t a = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a = max(a, __float_as_uint(v[i]) & 0x7fffffffu);
+    return a;
+  }
+  __device__ __forceinline__ uint32_t codes(float s) const {
+    uint32_t r = 0;
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, lo.x, lo.y, s, 0);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, lo.z, lo.w, s, 1);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, hi.x, hi.y, s, 2);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, hi.z, hi.w, s, 3);
+    return r;
+  }
+  static __device__ __forceinline__ void store_values(uint8_t* p, uint32_t r, float s, bool nan) {
+    const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(r, s, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(r, s, 1);
+    const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(r, s, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(r, s, 3);
+    const float q = __uint_as_float(0x7fc00000u);
+    *reinterpret_cast<float4*>(p) = nan ? make_float4(q, q, q, q) : make_float4(a[0], a[1], b[0], b[1]);
+    *(reinterpret_cast<float4*>(p) + 1) = nan ? make_float4(q, q, q, q) : make_float4(c[0], c[1], d[0], d[1]);
+  }
+};
+
+struct Args {
+  const uint8_t* x;
+  uint8_t* q;
+  int32_t* sf;
+  uint8_t* y;
+  const int32_t* masked_m;
+  int64_t ldx_bytes, ldq, ld_sf, ldy_bytes;
+  int m, k;
+};
+
+// Scale byte of a block from the bits of its amax.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
+  const int e = (int)((amax + 0x3fffffu) >> 23) - 2;
+  return amax == 0u ? 127u : (amax >= 0x7f800000u ? 255u : (uint32_t)max(e, 0));
+}
+
+template <bool BF16, bool VALUES>
+__global__ void __launch_bounds__(256) cast_kernel(const Args a) {
+  __shared__ uint32_t s_word[4][kRows];
+  constexpr int ES = BF16 ? 2 : 4;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int g = blockIdx.z;
+  const int m0 = blockIdx.x * kRows, c0 = blockIdx.y * kCols;
+  const int rows = min(a.masked_m != nullptr ? min(max(a.masked_m[g], 0), a.m) : a.m, m0 + kRows);
+  if (m0 >= rows) return;
+  const int col = c0 + 8 * lane;
+  const bool in = col < a.k;
+  const int kw = a.k >> 7;
+  const uint8_t* x = a.x + (int64_t)g * a.m * a.ldx_bytes + (int64_t)col * ES;
+  uint8_t* q = a.q + (int64_t)g * a.m * a.ldq + (col >> 1);
+  uint8_t* y = VALUES ? a.y + (int64_t)g * a.m * a.ldy_bytes + (int64_t)col * ES : nullptr;
+  for (int r0 = wave * kBatch; r0 < kRows; r0 += 4 * kBatch) {
+    Eight<BF16> v[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int row = m0 + r0 + i;
+      if (in && row < rows) v[i].load(x + (int64_t)row * a.ldx_bytes);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int row = m0 + r0 + i;
+      if (row >= rows) break;
+      uint32_t amax = v[i].amax();
+      amax = max(amax, dpp<kQuadXor1>(amax));
+      amax = max(amax, dpp<kQuadXor2>(amax));
+      const uint32_t byte = scale_byte(amax);
+      const bool nan = byte == 255u;
+      // 2^(byte - 127): the exponent alone (byte 0 is 2^-127, a denormal)
+      const float s = byte == 0u ? 0x1p-127f : __uint_as_float((nan ? 127u : byte) << 23);
+      uint32_t codes = v[i].codes(s);
+      codes = nan ? 0u : codes;
+      uint32_t word = byte << (8 * ((lane >> 2) & 3));
+      word |= dpp<kRowRor4>(word);
+      word |= dpp<kRowRor8>(word);
+      if (in) {
+        *reinterpret_cast<uint32_t*>(q + (int64_t)row * a.ldq) = codes;
+        if (VALUES) Eight<BF16>::store_values(y + (int64_t)row * a.ldy_bytes, codes, s, nan);
+        if ((lane & 15) == 0) s_word[lane >> 4][r0 + i] = word;
+      }
+    }
+  }
+  __syncthreads();
+  const int w = tid >> 6, r = tid & 63;
+  const int wk = (c0 >> 7) + w;
+  if (wk < kw && m0 + r < rows)
+    a.sf[((int64_t)g * kw + wk) * a.ld_sf + m0 + r] = (int32_t)s_word[w][r];
+}
+
+}  // namespace fp4c
+
+inline bool aligned_to(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+}  // namespace
+
+extern "C" {
+
+dg_status dg_cast_to_mxfp4(const void* x, int64_t ldx, dg_dtype x_dtype, void* q, int64_t ldq, int32_t* sf,
+                           int64_t ld_sf, void* y, int64_t ldy, const int32_t* masked_m, int num_groups, int m, int k,
+                           hipStream_t stream) {
+  if (m < 0 || k < 0 || num_groups < 0 || (x_dtype != DG_DTYPE_BF16 && x_dtype != DG_DTYPE_FP32))
+    return DG_ERROR_INVALID_VALUE;
+  if (k % 128 != 0) return DG_ERROR_NOT_SUPPORTED;
+  if (m == 0 || k == 0 || num_groups == 0) return DG_SUCCESS;
+  const int64_t es = x_dtype == DG_DTYPE_BF16 ? 2 : 4;
+  if (x == nullptr || q == nullptr || sf == nullptr) return DG_ERROR_INVALID_VALUE;
+  if (!aligned_to(x, 16) || !aligned_to(q, 4) || !aligned_to(sf, 4) || !aligned_to(masked_m, 4))
+    return DG_ERROR_INVALID_VALUE;
+  if (ldx < k || (ldx * es) % 16 != 0 || ldq < k / 2 || ldq % 4 != 0 || ld_sf < m) return DG_ERROR_INVALID_VALUE;
+  if (y != nullptr && (!aligned_to(y, 16) || ldy < k || (ldy * es) % 16 != 0)) return DG_ERROR_INVALID_VALUE;
+  const dim3 grid((m + fp4c::kRows - 1) / fp4c::kRows, (k + fp4c::kCols - 1) / fp4c::kCols, num_groups);
+  if (grid.y > 65535 || grid.z > 65535) return DG_ERROR_NOT_SUPPORTED;
+  const fp4c::Args a{static_cast<const uint8_t*>(x), static_cast<uint8_t*>(q), sf, static_cast<uint8_t*>(y), masked_m,
+                     ldx * es, ldq, ld_sf, ldy * es, m, k};
+  if (x_dtype == DG_DTYPE_BF16) {
+    if (y) hipLaunchKernelGGL((fp4c::cast_kernel<true, true>), grid, dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((fp4c::cast_kernel<true, false>), grid, dim3(256), 0, stream, a);
+  } else {
+    if (y) hipLaunchKernelGGL((fp4c::cast_kernel<false, true>), grid, dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((fp4c::cast_kernel<false, false>), grid, dim3(256), 0, stream, a);
+  }
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? DG_SUCCESS : dg::record_hip_error(e);
+}
+
+}  // extern "C"

@@ -23,6 +23,8 @@ What it computes, written out plainly in FP64 with numpy:
 * RMS norm with the residual's addition and its gradient (``norm.py``), the
   gated expert layer (``moe.py``), global gradient norm and clipping
   (``clip.py``);
+* microscaled 4-bit operands and their products (``mxfp4.py``), the router with
+  its balance loss and gradient (``router.py``);
 * the acceptance check (``check.py``).
 
 Sources, by page title and section:
@@ -73,4 +75,12 @@ from .layout import transform_sf  # noqa: F401
 from .norm import ref_add_rms_norm, ref_rms_norm_backward  # noqa: F401
 from .moe import ref_moe  # noqa: F401
 from .clip import ref_clip  # noqa: F401
+from .mxfp4 import (  # noqa: F401
+    E2M1_TABLE,
+    decode_mxfp4,
+    pack_scale_words,
+    ref_cast_mxfp4,
+    ref_mxfp4,
+)
+from .router import ref_router, ref_router_backward  # noqa: F401
 from .check import tolerance_report, assert_close, TOL_REL, TOL_RMS, TOL_COS  # noqa: F401
