@@ -9,7 +9,9 @@
 //   loss   = E * sum_e counts_e prob_sum_e / (sum counts * sum prob_sum)
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "dg.h"
 #include "dg_common.hpp"
@@ -19,8 +21,13 @@ namespace {
 namespace route {
 
 constexpr float kTiny = 1e-20f;
-constexpr int kWaves = 4;       // waves per workgroup, one row each at a time
-constexpr int kMaxBlocks = 512;
+constexpr int kWaves = 8;        // waves per workgroup
+constexpr int kMaxBlocks = 520;  // workgroups of a large batch, each with its own partial sums
+constexpr int kFinishCols = 32;  // experts per workgroup of the second kernel
+
+// Workspace: a header (the count of finished workgroups, then three sums for each workgroup of the second kernel),
+// counts [blocks][E] and probability sums [blocks][E].
+constexpr size_t kHeader = 1024;
 
 struct Args {
   const uint8_t* logits;
@@ -31,11 +38,10 @@ struct Args {
   int32_t* counts;
   float* prob_sum;
   float* loss;
-  uint32_t* part_counts;  // [blocks][E]
-  float* part_probs;      // [blocks][E]
-  int64_t ld;
+  uint8_t* ws;
+  int64_t ld;  // bytes
   float scale;
-  int m, e, k, normalize, blocks;
+  int m, e, k, normalize, blocks, vec;
 };
 
 struct GradArgs {
@@ -46,34 +52,54 @@ struct GradArgs {
   const float* prob_sum;
   const float* dloss;
   uint8_t* dx;
-  int64_t ld, ld_dx;
+  int64_t ld, ld_dx;  // bytes
   float scale;
-  int m, e, k, normalize;
+  int m, e, k, normalize, vec;
 };
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
 }
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
-  return v;
-}
-template <typename T>
-__device__ __forceinline__ T wave_max(T v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) {
-    const T w = __shfl_xor(v, o);
-    v = w > v ? w : v;
+
+// Reduction over the L lanes (16, 32 or 64) of a row, the result in each of them: rotations within 16 lanes, then
+// exchanges of whole 16-lane rows.  Every lane adds the same pairs, so all get the same bits.
+template <int L, typename T, typename Op>
+__device__ __forceinline__ T reduce(T v, Op op) {
+  static_assert(sizeof(T) == 4, "one register");
+  auto step = [&](uint32_t o) { v = op(v, __builtin_bit_cast(T, o)); };
+  step(dpp<0x128>(__builtin_bit_cast(uint32_t, v)));  // row_ror 8, 4, 2, 1
+  step(dpp<0x124>(__builtin_bit_cast(uint32_t, v)));
+  step(dpp<0x122>(__builtin_bit_cast(uint32_t, v)));
+  step(dpp<0x121>(__builtin_bit_cast(uint32_t, v)));
+  if constexpr (L >= 32) {
+    const auto s = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+    v = op(__builtin_bit_cast(T, (uint32_t)s[0]), __builtin_bit_cast(T, (uint32_t)s[1]));
+  }
+  if constexpr (L >= 64) {
+    const auto s = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+    v = op(__builtin_bit_cast(T, (uint32_t)s[0]), __builtin_bit_cast(T, (uint32_t)s[1]));
   }
   return v;
 }
-__device__ __forceinline__ int wave_min(int v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v = min(v, __shfl_xor(v, o));
-  return v;
+template <int L>
+__device__ __forceinline__ float sum_of(float v) {
+  return reduce<L>(v, [](float a, float b) { return a + b; });
+}
+template <int L>
+__device__ __forceinline__ float max_of(float v) {
+  return reduce<L>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+template <int L>
+__device__ __forceinline__ uint32_t max_of(uint32_t v) {
+  return reduce<L>(v, [](uint32_t a, uint32_t b) { return max(a, b); });
+}
+// Whether any of a row's lanes says so.
+template <int L>
+__device__ __forceinline__ bool any_of(bool v, int lane) {
+  const uint64_t b = __ballot(v);
+  if constexpr (L == 64) return b != 0;
+  return ((b >> (lane & ~(L - 1))) & ((1ull << L) - 1)) != 0;
 }
 
 // Orders a wave's LDS accesses before this point with those after it, for all its lanes.
@@ -82,287 +108,531 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
-template <bool BF16>
-__device__ __forceinline__ float load(const uint8_t* row, int e) {
-  if constexpr (BF16) return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[e] << 16);
-  return reinterpret_cast<const float*>(row)[e];
+// Value i of lane l (of a row's L) is expert 4 * (l + L * (i / 4)) + i % 4: four in a row, so that a lane's loads
+// and stores are vectors and a row's lanes cover whole runs.
+template <int L>
+__device__ __forceinline__ int expert(int l, int i) {
+  return 4 * (l + L * (i >> 2)) + (i & 3);
 }
 
-// Scores of a row's V experts per lane (0 past the last one), and the sum over all.
-template <int V, bool SIGMOID>
-__device__ __forceinline__ float scores(const float (&x)[V], float (&p)[V]) {
+template <bool BF16>
+__device__ __forceinline__ float load1(const uint8_t* row, int e) {
+  if constexpr (BF16) return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(row)[e] << 16);
+  else return reinterpret_cast<const float*>(row)[e];
+}
+
+// A row's values of a lane, -inf past the last expert.  vec: rows are aligned to four values and hold whole fours.
+template <int L, int V, bool BF16>
+__device__ __forceinline__ void load_row(const uint8_t* row, int e, int vec, int l, float (&x)[V]) {
+  if (vec) {
+#pragma unroll
+    for (int c = 0; c < V / 4; ++c) {
+      const int at = 4 * (l + L * c);
+      float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (at < e) {
+        if constexpr (BF16) {
+          const uint2 w = *reinterpret_cast<const uint2*>(row + 2 * at);
+          v = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                          __uint_as_float(w.y & 0xffff0000u));
+        } else {
+          v = *reinterpret_cast<const float4*>(row + 4 * at);
+        }
+      }
+      x[4 * c] = v.x, x[4 * c + 1] = v.y, x[4 * c + 2] = v.z, x[4 * c + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = expert<L>(l, i) < e ? load1<BF16>(row, expert<L>(l, i)) : -INFINITY;
+  }
+}
+
+// What turns a row's logits into scores: the largest (0 for a row of -inf alone) and 1 / sum of the exponentials.
+struct Norm {
+  float top, inv;
+};
+// exp(-|x|) decides a sigmoid without overflow; 1 - sigmoid(x) is sigmoid(-x).
+__device__ __forceinline__ float sigmoid(float x) {
+  const float t = __expf(-fabsf(x)), r = __builtin_amdgcn_rcpf(1.0f + t);
+  return x >= 0.f ? r : t * r;
+}
+template <bool SIGMOID>
+__device__ __forceinline__ float score(float x, Norm n) {
+  if constexpr (SIGMOID) return sigmoid(x);
+  return __expf(x - n.top) * n.inv;
+}
+// Scores of a row; for sigmoids n.inv is 1 / (their sum + 1e-20).
+template <int L, int V, bool SIGMOID>
+__device__ __forceinline__ Norm scores(const float (&x)[V], float (&p)[V]) {
+  Norm n{0.f, 0.f};
   float sum = 0.f;
   if constexpr (SIGMOID) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const float t = __expf(-fabsf(x[i])), r = 1.0f / (1.0f + t);
-      p[i] = x[i] >= 0.f ? r : t * r;
+      p[i] = sigmoid(x[i]);
       sum += p[i];
     }
-    return wave_sum(sum);
+    n.inv = 1.0f / (sum_of<L>(sum) + kTiny);
   } else {
     float top = x[0];
 #pragma unroll
     for (int i = 1; i < V; ++i) top = fmaxf(top, x[i]);
-    top = wave_max(top);
-    if (top == -INFINITY) top = 0.f;
+    top = max_of<L>(top);
+    n.top = top == -INFINITY ? 0.f : top;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      p[i] = __expf(x[i] - top);
+      p[i] = __expf(x[i] - n.top);
       sum += p[i];
     }
-    sum = wave_sum(sum);
-    const float r = sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum);
+    sum = sum_of<L>(sum);
+    n.inv = sum == 0.f ? 0.f : 1.0f / sum;
 #pragma unroll
-    for (int i = 0; i < V; ++i) p[i] *= r;
-    return sum > 0.f ? 1.f : sum;
+    for (int i = 0; i < V; ++i) p[i] *= n.inv;
   }
+  return n;
 }
 
-// expert of value i of a lane
-__device__ __forceinline__ int expert(int lane, int i) { return lane + 64 * i; }
+// Floats as unsigned integers of the same order, and back.
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t u) { return __uint_as_float((u >> 31) ? u ^ 0x80000000u : ~u); }
 
-template <int V, bool BF16, bool SIGMOID, bool BIAS, bool STATS>
-__global__ void __launch_bounds__(kWaves * 64) forward_kernel(const Args a) {
-  extern __shared__ uint32_t s_mem[];  // counts [E], then per wave probability sums [kWaves][E]
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  uint32_t* s_counts = s_mem;
-  float* s_probs = reinterpret_cast<float*>(s_mem + a.e);
-  if (STATS) {
-    for (int e = threadIdx.x; e < a.e; e += kWaves * 64) s_counts[e] = 0;
-    __syncthreads();
+// Descending sort of V registers (odd-even merges: V = 4, 8, 16 take 5, 19, 63 exchanges).
+template <int V>
+__device__ __forceinline__ void sort_desc(uint32_t (&k)[V]) {
+#pragma unroll
+  for (int p = 1; p < V; p <<= 1)
+#pragma unroll
+    for (int q = p; q >= 1; q >>= 1)
+#pragma unroll
+      for (int j = q % p; j + q < V; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; ++i)
+          if (i + j + q < V && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+            const uint32_t a = k[i + j], b = k[i + j + q];
+            k[i + j] = max(a, b);
+            k[i + j + q] = min(a, b);
+          }
+}
+
+// The choice for a row whose order FP32 leaves open, by a whole wave: every key in FP64, the largest taken k times.
+// Lane j gets the j-th one's expert (-1: none).
+template <int E, bool SIGMOID>
+__device__ __forceinline__ int choose_exact(const float* row, const float* bias, int e, int k, int lane) {
+  constexpr int N = (E + 63) / 64;
+  double key[N], top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int at = lane + 64 * i;
+    const float x = at < e ? row[at] : -INFINITY;
+    key[i] = x > -INFINITY ? (double)x : -INFINITY;
+    top = key[i] > top ? key[i] : top;
   }
+  auto wave_max = [](double v) {
+    for (int o = 32; o >= 1; o >>= 1) {
+      const double w = __shfl_xor(v, o);
+      v = w > v ? w : v;
+    }
+    return v;
+  };
+  if (bias != nullptr) {
+    double total = 0.0;
+    top = SIGMOID ? 0.0 : wave_max(top);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const bool live = key[i] > -INFINITY;
+      const double t = exp(SIGMOID ? -key[i] : key[i] - top);
+      key[i] = live ? (SIGMOID ? 1.0 / (1.0 + t) : t) : -INFINITY;
+      total += live ? t : 0.0;
+    }
+    if constexpr (!SIGMOID)
+      for (int o = 32; o >= 1; o >>= 1) total += __shfl_xor(total, o);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (key[i] > -INFINITY) {
+        key[i] = (SIGMOID ? key[i] : key[i] / total) + (double)bias[lane + 64 * i];
+        if (!(key[i] > -INFINITY)) key[i] = -INFINITY;  // a bias of NaN
+      }
+  }
+  int mine = -1;
+  for (int j = 0; j < k; ++j) {
+    double best = key[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) best = key[i] > best ? key[i] : best;
+    best = wave_max(best);
+    int at = 0x7fffffff;
+#pragma unroll
+    for (int i = N - 1; i >= 0; --i)
+      if (key[i] == best) at = lane + 64 * i;
+    for (int o = 32; o >= 1; o >>= 1) at = min(at, __shfl_xor(at, o));
+    if (!(best > -INFINITY)) break;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (lane + 64 * i == at) key[i] = -INFINITY;
+    if (lane == j) mine = at;
+  }
+  return mine;
+}
+
+template <int L, int V, bool BF16, bool SIGMOID>
+__global__ void __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(L == 16 ? 4 : 2))) forward_kernel(const Args a) {
+  constexpr int R = 64 / L;             // rows a wave works on
+  constexpr int E = L * V;              // experts a row has room for
+  constexpr uint32_t IDX = E - 1;       // low bits of a key: E - 1 - expert, so that ties go to the lower one
+  __shared__ float s_x[kWaves * R][E];  // the rows at work; at the end their sums of scores
+  __shared__ __attribute__((aligned(16))) float s_bias[E];
+  __shared__ uint32_t s_counts[E];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int grp = lane / L, l = lane % L;
+  const bool stats = a.counts != nullptr;
+  if (stats) {
+    for (int e = tid; e < E; e += kWaves * 64) s_counts[e] = 0;
+    if (blockIdx.x == 0 && tid == 0 && a.blocks > 1) *reinterpret_cast<uint32_t*>(a.ws) = 0;
+  }
+  if (a.bias != nullptr)
+    for (int e = tid; e < E; e += kWaves * 64) s_bias[e] = e < a.e ? a.bias[e] : 0.f;
+  if (stats || a.bias != nullptr) __syncthreads();
+  float* xs = s_x[wave * R + grp];
   float ps[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) ps[i] = 0.f;
-  for (int row = blockIdx.x * kWaves + wave; row < a.m; row += gridDim.x * kWaves) {
-    const bool on = a.mask == nullptr || a.mask[row] != 0;
-    const uint8_t* src = a.logits + row * a.ld;
+  const int stride = gridDim.x * kWaves * R;
+  // rows past the end repeat the last one and store nothing
+  const int first = (blockIdx.x * kWaves + wave) * R + grp;
+  for (int base = first - grp; base < a.m; base += stride) {
+    const int row = base + grp;
+    const bool on = row < a.m && (a.mask == nullptr || a.mask[row] != 0);
     float x[V], p[V];
+    load_row<L, V, BF16>(a.logits + (int64_t)min(row, a.m - 1) * a.ld, a.e, a.vec, l, x);
+    wave_sync();  // the last rows' reads are done
 #pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = expert(lane, i) < a.e ? load<BF16>(src, expert(lane, i)) : -INFINITY;
-    const float sum = scores<V, SIGMOID>(x, p);
-    if (STATS && on) {
-      const float r = SIGMOID ? 1.0f / (sum + kTiny) : 1.0f;
+    for (int c = 0; c < V / 4; ++c)
+      *reinterpret_cast<float4*>(xs + 4 * (l + L * c)) = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+    const Norm n = scores<L, V, SIGMOID>(x, p);
+    if (stats && on) {
+      const float r = SIGMOID ? n.inv : 1.0f;
 #pragma unroll
       for (int i = 0; i < V; ++i) ps[i] += p[i] * r;
     }
-    double key[V];
+    // Keys: the value's leading bits, then the index.  What the index pushed out is looked at below.
+    uint32_t key[V], lost = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      key[i] = x[i];
-      if (BIAS && x[i] > -INFINITY) {
-        const double b = a.bias[expert(lane, i)];
-        if constexpr (SIGMOID) key[i] = 1.0 / (1.0 + exp(-(double)x[i])) + b;
+      float v = x[i];
+      if (a.bias != nullptr) v = p[i] + s_bias[expert<L>(l, i)];
+      const uint32_t u = ordered(v + 0.0f);  // -0 and 0 are one value
+      lost |= __float_as_uint(v);
+      key[i] = (x[i] > -INFINITY && v > -INFINITY) ? (u & ~IDX) | (IDX - expert<L>(l, i)) : 0u;
+    }
+    sort_desc<V>(key);
+    wave_sync();
+    uint32_t mine = 0, last = 0, kth = 0;
+    int taken = 0;
+    auto take = [&]() {
+      last = max_of<L>(key[0]);
+      if (l == taken) mine = last;
+      const bool won = key[0] == last && last != 0;
+#pragma unroll
+      for (int i = 0; i + 1 < V; ++i) key[i] = won ? key[i + 1] : key[i];
+      if (won) key[V - 1] = 0;
+      ++taken;
+    };
+    for (int j = 0; j < a.k; ++j) take();
+    kth = last;
+    int id = mine != 0 ? (int)(IDX - (mine & IDX)) : -1;
+    // BF16 logits lose nothing, nor do FP32 ones whose last bits are zero
+    const bool rough = a.bias != nullptr || (!BF16 && any_of<L>((lost & IDX) != 0, lane));
+    if (__any(rough)) {
+      // Take more until none of the rest can belong to the first k, as far as there are lanes for them.
+      auto open = [&]() {
+        if (kth == 0 || last == 0) return false;
+        if (a.bias == nullptr) return (last | IDX) >= (kth & ~IDX);
+        const float lo = unordered(kth & ~IDX), hi = unordered(last | IDX);
+        return !(lo - hi > 0x1p-18f * (1.0f + fabsf(lo)));
+      };
+      do take();
+      while (taken < L && __any(rough && open()));
+      bool slow = rough && open();
+      // the order of what was taken, by full FP32 values
+      id = mine != 0 ? (int)(IDX - (mine & IDX)) : -1;
+      float xv = id >= 0 ? xs[id] : -INFINITY, bv = 0.f, v = xv;
+      if (a.bias != nullptr && id >= 0) {
+        bv = s_bias[id];
+        v = score<SIGMOID>(xv, n) + bv;
+      }
+      for (int turn = 0; turn <= L; ++turn) {
+        const float up = __shfl_up(v, 1, L);
+        const int uid = __shfl_up(id, 1, L);
+        const bool wrong = l > 0 && id >= 0 && (v > up || (v == up && id < uid));
+        if (!__any(rough && wrong)) break;
+        const bool high = (l + turn) & 1;  // of the pairs (odd, even) and (even, odd) by turns
+        const int other = high ? l - 1 : l + 1;
+        const bool pair = other >= 0 && other < L;
+        const float ov = __shfl(v, pair ? other : l, L), ox = __shfl(xv, pair ? other : l, L), ob = __shfl(bv, pair ? other : l, L);
+        const int oid = __shfl(id, pair ? other : l, L);
+        const bool ahead = oid >= 0 && (id < 0 || ov > v || (ov == v && oid < id));  // the other one goes first
+        if (rough && pair && oid != id && (high ? !ahead : ahead)) v = ov, xv = ox, bv = ob, id = oid;
+      }
+      if (a.bias != nullptr) {
+        const float up = __shfl_up(v, 1, L), ux = __shfl_up(xv, 1, L), ub = __shfl_up(bv, 1, L);
+        const bool near = l > 0 && id >= 0 && !(up - v > 0x1p-18f * (1.0f + fabsf(v))) && !(xv == ux && bv == ub);
+        slow = slow || any_of<L>(near, lane);
+      }
+      for (uint64_t left = __ballot(slow && on && l == 0); left != 0; left &= left - 1) {
+        const int g = __builtin_ctzll(left) / L;
+        const int exact = __shfl(choose_exact<E, SIGMOID>(s_x[wave * R + g], a.bias, a.e, a.k, lane), l);
+        if (grp == g) id = exact;
       }
     }
-    if constexpr (BIAS && !SIGMOID) {
-      double top = key[0];
-#pragma unroll
-      for (int i = 1; i < V; ++i) top = key[i] > top ? key[i] : top;
-      top = wave_max(top);
-      double total = 0.0, ex[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        ex[i] = x[i] > -INFINITY ? exp(key[i] - top) : 0.0;
-        total += ex[i];
-      }
-      total = wave_sum(total);
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (x[i] > -INFINITY) key[i] = ex[i] / total + (double)a.bias[expert(lane, i)];
+    if (l >= a.k || !on) id = -1;
+    const float w = id >= 0 ? score<SIGMOID>(xs[id], n) : 0.f;
+    const float f = a.normalize ? a.scale / (sum_of<L>(w) + kTiny) : a.scale;
+    if (l < a.k && row < a.m) {
+      a.ids[(int64_t)row * a.k + l] = id;
+      a.weights[(int64_t)row * a.k + l] = w * f;
     }
+    if (stats && id >= 0) atomicAdd(&s_counts[id], 1u);
+  }
+  if (!stats) return;
+  wave_sync();
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (!(key[i] > -INFINITY)) key[i] = -INFINITY;  // NaN too
-    int my_id = -1;
-    float my_w = 0.f, chosen = 0.f;
-    for (int j = 0; j < a.k; ++j) {
-      double best = key[0];
-#pragma unroll
-      for (int i = 1; i < V; ++i) best = key[i] > best ? key[i] : best;
-      best = wave_max(best);
-      if (!(best > -INFINITY) || !on) break;
-      int at = 0x7fffffff;
-#pragma unroll
-      for (int i = V - 1; i >= 0; --i)
-        if (key[i] == best) at = expert(lane, i);
-      at = wave_min(at);
-      float w = 0.f;
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (expert(lane, i) == at) {
-          w = p[i];
-          key[i] = -INFINITY;
-        }
-      w = __shfl(w, at & 63);
-      chosen += w;
-      if (lane == j) {
-        my_id = at;
-        my_w = w;
-      }
-      if (STATS && lane == 0) atomicAdd(&s_counts[at], 1u);
-    }
-    if (lane < a.k) {
-      a.ids[(int64_t)row * a.k + lane] = my_id;
-      a.weights[(int64_t)row * a.k + lane] = my_id < 0 ? 0.f : a.scale * (a.normalize ? my_w / (chosen + kTiny) : my_w);
+  for (int c = 0; c < V / 4; ++c)
+    *reinterpret_cast<float4*>(xs + 4 * (l + L * c)) = make_float4(ps[4 * c], ps[4 * c + 1], ps[4 * c + 2], ps[4 * c + 3]);
+  __syncthreads();
+  uint32_t* part_counts = reinterpret_cast<uint32_t*>(a.ws + kHeader);
+  float* part_probs = reinterpret_cast<float*>(part_counts + (size_t)a.blocks * a.e);
+  double c = 0, s = 0, cs = 0;
+  for (int e = tid; e < a.e; e += kWaves * 64) {
+    float t = 0.f;
+#pragma unroll 8
+    for (int w = 0; w < kWaves * R; ++w) t += s_x[w][e];
+    const uint32_t cnt = s_counts[e];
+    if (a.blocks > 1) {
+      part_counts[(size_t)blockIdx.x * a.e + e] = cnt;
+      part_probs[(size_t)blockIdx.x * a.e + e] = t;
+    } else {
+      a.counts[e] = (int32_t)cnt;
+      if (a.prob_sum != nullptr) a.prob_sum[e] = t;
+      c += cnt;
+      s += t;
+      cs += (double)cnt * t;
     }
   }
-  if (STATS) {
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (expert(lane, i) < a.e) s_probs[wave * a.e + expert(lane, i)] = ps[i];
+  if (a.blocks == 1 && a.loss != nullptr) {
+    __shared__ double s_red[3][kWaves];
+    for (int o = 32; o >= 1; o >>= 1) {
+      c += __shfl_xor(c, o);
+      s += __shfl_xor(s, o);
+      cs += __shfl_xor(cs, o);
+    }
+    if (lane == 0) s_red[0][wave] = c, s_red[1][wave] = s, s_red[2][wave] = cs;
     __syncthreads();
-    for (int e = threadIdx.x; e < a.e; e += kWaves * 64) {
-      float s = 0.f;
-      for (int w = 0; w < kWaves; ++w) s += s_probs[w * a.e + e];
-      a.part_counts[(int64_t)blockIdx.x * a.e + e] = s_counts[e];
-      a.part_probs[(int64_t)blockIdx.x * a.e + e] = s;
+    if (tid == 0) {
+      for (int w = 1; w < kWaves; ++w) c += s_red[0][w], s += s_red[1][w], cs += s_red[2][w];
+      *a.loss = c * s == 0 ? 0.f : (float)(a.e * cs / (c * s));
     }
   }
 }
 
-__global__ void __launch_bounds__(1024) finish_kernel(const Args a) {
-  __shared__ double s_red[3][16];
-  double c = 0, s = 0, cs = 0;
-  for (int e = threadIdx.x; e < a.e; e += 1024) {
-    uint32_t n = 0;
-    double p = 0;
-    for (int b = 0; b < a.blocks; ++b) {
-      n += a.part_counts[(int64_t)b * a.e + e];
-      p += (double)a.part_probs[(int64_t)b * a.e + e];
+// The workgroups' partial sums, kFinishCols experts to a workgroup; the last one to finish adds up the loss.
+__global__ void __launch_bounds__(512) finish_kernel(const Args a) {
+  constexpr int PARTS = 512 / kFinishCols;
+  __shared__ uint32_t s_c[PARTS][kFinishCols];
+  __shared__ double s_p[PARTS][kFinishCols];
+  __shared__ int s_last;
+  const int tid = threadIdx.x, col = tid % kFinishCols, part = tid / kFinishCols;
+  const int e = blockIdx.x * kFinishCols + col;
+  const uint32_t* part_counts = reinterpret_cast<const uint32_t*>(a.ws + kHeader);
+  const float* part_probs = reinterpret_cast<const float*>(part_counts + (size_t)a.blocks * a.e);
+  uint32_t n = 0;
+  double p = 0;
+  if (e < a.e) {
+#pragma unroll 8
+    for (int b = part; b < a.blocks; b += PARTS) {
+      n += part_counts[(size_t)b * a.e + e];
+      p += (double)part_probs[(size_t)b * a.e + e];
     }
+  }
+  s_c[part][col] = n;
+  s_p[part][col] = p;
+  __syncthreads();
+  if (tid >= 64) return;
+  double c = 0, cs = 0;
+  p = 0;
+  if (tid < kFinishCols && e < a.e) {
+    n = 0;
+    for (int i = 0; i < PARTS; ++i) n += s_c[i][col], p += s_p[i][col];
     a.counts[e] = (int32_t)n;
     if (a.prob_sum != nullptr) a.prob_sum[e] = (float)p;
-    c += n;
-    s += p;
-    cs += n * p;
+    c = n;
+    cs = c * p;
   }
-  c = wave_sum(c);
-  s = wave_sum(s);
-  cs = wave_sum(cs);
-  if ((threadIdx.x & 63) == 0) {
-    s_red[0][threadIdx.x >> 6] = c;
-    s_red[1][threadIdx.x >> 6] = s;
-    s_red[2][threadIdx.x >> 6] = cs;
+  if (a.loss == nullptr) return;
+  for (int o = 32; o >= 1; o >>= 1) {
+    c += __shfl_xor(c, o);
+    p += __shfl_xor(p, o);
+    cs += __shfl_xor(cs, o);
   }
-  __syncthreads();
-  if (threadIdx.x == 0 && a.loss != nullptr) {
-    double t[3] = {0, 0, 0};
-    for (int w = 0; w < 16; ++w)
-      for (int i = 0; i < 3; ++i) t[i] += s_red[i][w];
-    const double den = t[0] * t[1];
-    *a.loss = den == 0 ? 0.f : (float)(a.e * t[2] / den);
+  double* sums = reinterpret_cast<double*>(a.ws + 64);
+  if (tid == 0) {
+    double* mine = sums + 3 * blockIdx.x;
+    __hip_atomic_store(mine, c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(mine + 1, p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(mine + 2, cs, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    s_last = __hip_atomic_fetch_add(reinterpret_cast<uint32_t*>(a.ws), 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) + 1 ==
+             gridDim.x;
+    if (s_last) {
+      c = p = cs = 0;
+      for (uint32_t i = 0; i < gridDim.x; ++i) {
+        c += __hip_atomic_load(sums + 3 * i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        p += __hip_atomic_load(sums + 3 * i + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        cs += __hip_atomic_load(sums + 3 * i + 2, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+      *a.loss = c * p == 0 ? 0.f : (float)(a.e * cs / (c * p));
+    }
   }
 }
 
-template <int V, bool BF16, bool SIGMOID>
+// A batch of no rows.
+__global__ void __launch_bounds__(1024) zero_kernel(const Args a) {
+  if ((int)threadIdx.x < a.e) {
+    a.counts[threadIdx.x] = 0;
+    if (a.prob_sum != nullptr) a.prob_sum[threadIdx.x] = 0.f;
+  }
+  if (threadIdx.x == 0 && a.loss != nullptr) *a.loss = 0.f;
+}
+
+template <int L, int V, bool BF16, bool SIGMOID>
 __global__ void __launch_bounds__(kWaves * 64) backward_kernel(const GradArgs a) {
-  __shared__ float s_dp[kWaves][V * 64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  // g_e = dloss * E * counts_e / (sum counts * sum prob_sum)
+  constexpr int R = 64 / L, E = L * V;
+  __shared__ float s_d[kWaves * R][E];  // the gradient by the chosen scores, 0 elsewhere
+  __shared__ double s_red[2][kWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int grp = lane / L, l = lane % L;
+  float* ds = s_d[wave * R + grp];
   float g[V];
-  {
-    double c = 0, s = 0;
-    float mine[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = expert(lane, i);
-      mine[i] = 0.f;
-      if (a.counts != nullptr && e < a.e) {
-        mine[i] = (float)a.counts[e];
-        c += a.counts[e];
-        s += (double)a.prob_sum[e];
+  for (int i = 0; i < V; ++i) g[i] = 0.f;
+  const int stride = gridDim.x * kWaves * R;
+  const int first = (blockIdx.x * kWaves + wave) * R + grp;
+  float next[V];
+  load_row<L, V, BF16>(a.logits + (int64_t)min(first, a.m - 1) * a.ld, a.e, a.vec, l, next);
+  if (a.counts != nullptr) {  // g_e = dloss * E * counts_e / (sum counts * sum prob_sum)
+    double c = 0, s = 0;
+    for (int e = tid; e < a.e; e += kWaves * 64) {
+      c += a.counts[e];
+      s += (double)a.prob_sum[e];
+    }
+    for (int o = 32; o >= 1; o >>= 1) {
+      c += __shfl_xor(c, o);
+      s += __shfl_xor(s, o);
+    }
+    if (lane == 0) s_red[0][wave] = c, s_red[1][wave] = s;
+    __syncthreads();
+    c = s = 0;
+    for (int w = 0; w < kWaves; ++w) c += s_red[0][w], s += s_red[1][w];
+    const float f = c * s == 0 ? 0.f : (float)((double)*a.dloss * a.e / (c * s));
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (expert<L>(l, i) < a.e) g[i] = f * (float)a.counts[expert<L>(l, i)];
+  }
+  for (int base = first - grp; base < a.m; base += stride) {
+    const int row = min(base + grp, a.m - 1);
+    float x[V], p[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = next[i];
+    int id = -1;
+    float d = 0.f, xv = -INFINITY;
+    if (l < a.k) {
+      id = a.ids[(int64_t)row * a.k + l];
+      if ((uint32_t)id >= (uint32_t)a.e) id = -1;
+      if (id >= 0) {
+        d = a.scale * a.dw[(int64_t)row * a.k + l];
+        xv = load1<BF16>(a.logits + (int64_t)row * a.ld, id);
       }
     }
-    c = wave_sum(c);
-    s = wave_sum(s);
-    const double den = c * s;
-    const float f = (a.counts == nullptr || den == 0) ? 0.f : (float)((double)*a.dloss * a.e / den);
-#pragma unroll
-    for (int i = 0; i < V; ++i) g[i] = f * mine[i];
-  }
-  for (int row = blockIdx.x * kWaves + wave; row < a.m; row += gridDim.x * kWaves) {
-    const uint8_t* src = a.logits + row * a.ld;
-    float x[V], p[V], dp[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = expert(lane, i) < a.e ? load<BF16>(src, expert(lane, i)) : -INFINITY;
-    const float sum = scores<V, SIGMOID>(x, p);
-    int id = -1;
-    float dw = 0.f;
-    if (lane < a.k) {
-      id = a.ids[(int64_t)row * a.k + lane];
-      if (id < 0 || id >= a.e) id = -1;
-      if (id >= 0) dw = a.dw[(int64_t)row * a.k + lane];
-    }
-    const bool on = __any(id >= 0);
-#pragma unroll
-    for (int i = 0; i < V; ++i) s_dp[wave][expert(lane, i)] = p[i];
+    if (base + stride < a.m)
+      load_row<L, V, BF16>(a.logits + (int64_t)min(base + grp + stride, a.m - 1) * a.ld, a.e, a.vec, l, next);
     wave_sync();
-    const float chosen = id >= 0 ? s_dp[wave][id] : 0.f;
-    float d = a.scale * dw;
+#pragma unroll
+    for (int c = 0; c < V / 4; ++c) *reinterpret_cast<float4*>(ds + 4 * (l + L * c)) = make_float4(0.f, 0.f, 0.f, 0.f);
+    const Norm n = scores<L, V, SIGMOID>(x, p);
+    const bool on = any_of<L>(id >= 0, lane);
     if (a.normalize) {
-      const float total = wave_sum(chosen) + kTiny;
-      d = (d - wave_sum(d * chosen) / total) / total;
+      const float w = id >= 0 ? score<SIGMOID>(xv, n) : 0.f;
+      const float r = 1.0f / (sum_of<L>(w) + kTiny);
+      d = (d - sum_of<L>(d * w) * r) * r;
     }
     wave_sync();
+    if (id >= 0) atomicAdd(&ds[id], d);
+    wave_sync();
+    float dot = 0.f, dp[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) s_dp[wave][expert(lane, i)] = 0.f;
-    wave_sync();
-    if (id >= 0) atomicAdd(&s_dp[wave][id], d);
-    wave_sync();
-    float dot = 0.f;
+    for (int c = 0; c < V / 4; ++c) {
+      const float4 v = *reinterpret_cast<const float4*>(ds + 4 * (l + L * c));
+      dp[4 * c] = v.x, dp[4 * c + 1] = v.y, dp[4 * c + 2] = v.z, dp[4 * c + 3] = v.w;
+    }
     if constexpr (SIGMOID) {
-      const float r = 1.0f / (sum + kTiny);
 #pragma unroll
       for (int i = 0; i < V; ++i) dot += g[i] * p[i];
-      dot = wave_sum(dot) * r;
+      dot = sum_of<L>(dot) * n.inv;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float t = __expf(-fabsf(x[i])), q = 1.0f / (1.0f + t);
-        dp[i] = (s_dp[wave][expert(lane, i)] + (g[i] - dot) * r) * p[i] * (x[i] >= 0.f ? t * q : q);
+        // p (1 - p), the second factor without cancellation: t / (1 + t) or 1 / (1 + t)
+        const float q = x[i] >= 0.f ? __expf(-x[i]) * p[i] : __builtin_amdgcn_rcpf(1.0f + __expf(x[i]));
+        dp[i] = (dp[i] + (g[i] - dot) * n.inv) * p[i] * q;
       }
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        dp[i] = s_dp[wave][expert(lane, i)] + g[i];
+        dp[i] += g[i];
         dot += dp[i] * p[i];
       }
-      dot = wave_sum(dot);
+      dot = sum_of<L>(dot);
 #pragma unroll
       for (int i = 0; i < V; ++i) dp[i] = p[i] * (dp[i] - dot);
     }
-    wave_sync();
+    if (base + grp < a.m) {
+      uint8_t* out = a.dx + (int64_t)row * a.ld_dx;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = expert(lane, i);
-      if (e >= a.e) continue;
-      const float v = on ? dp[i] : 0.f;
-      if constexpr (BF16) reinterpret_cast<__bf16*>(a.dx + row * a.ld_dx)[e] = (__bf16)v;
-      else reinterpret_cast<float*>(a.dx + row * a.ld_dx)[e] = v;
+      for (int i = 0; i < V; ++i) dp[i] = on ? dp[i] : 0.f;
+      if (a.vec) {
+#pragma unroll
+        for (int c = 0; c < V / 4; ++c) {
+          const int at = 4 * (l + L * c);
+          if (at >= a.e) continue;
+          if constexpr (BF16) {
+            typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+            typedef float f32x4 __attribute__((ext_vector_type(4)));
+            const f32x4 v = {dp[4 * c], dp[4 * c + 1], dp[4 * c + 2], dp[4 * c + 3]};
+            *reinterpret_cast<bf16x4*>(out + 2 * at) = __builtin_convertvector(v, bf16x4);
+          } else {
+            *reinterpret_cast<float4*>(out + 4 * at) = make_float4(dp[4 * c], dp[4 * c + 1], dp[4 * c + 2], dp[4 * c + 3]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const int e = expert<L>(l, i);
+          if (e >= a.e) continue;
+          if constexpr (BF16) reinterpret_cast<__bf16*>(out)[e] = (__bf16)dp[i];
+          else reinterpret_cast<float*>(out)[e] = dp[i];
+        }
+      }
     }
   }
 }
 
-template <int V, bool BF16, bool SIGMOID>
-void run_forward(const Args& a, hipStream_t stream) {
-  const bool stats = a.counts != nullptr;
-  const dim3 grid(a.blocks), block(kWaves * 64);
-  const size_t lds = stats ? (size_t)a.e * 4 * (1 + kWaves) : 0;
-  if (a.bias != nullptr) {
-    if (stats) hipLaunchKernelGGL((forward_kernel<V, BF16, SIGMOID, true, true>), grid, block, lds, stream, a);
-    else hipLaunchKernelGGL((forward_kernel<V, BF16, SIGMOID, true, false>), grid, block, lds, stream, a);
-  } else {
-    if (stats) hipLaunchKernelGGL((forward_kernel<V, BF16, SIGMOID, false, true>), grid, block, lds, stream, a);
-    else hipLaunchKernelGGL((forward_kernel<V, BF16, SIGMOID, false, false>), grid, block, lds, stream, a);
-  }
-  if (stats) hipLaunchKernelGGL(finish_kernel, dim3(1), dim3(1024), 0, stream, a);
-}
+// Rows a workgroup works on at a time, by the lanes of a row.
+inline int rows_at_once(int lanes) { return kWaves * (64 / lanes); }
 
-template <int V, bool BF16, bool SIGMOID>
-void run_backward(const GradArgs& a, hipStream_t stream) {
-  const int blocks = min((a.m + kWaves - 1) / kWaves, 2048);
-  hipLaunchKernelGGL((backward_kernel<V, BF16, SIGMOID>), dim3(blocks), dim3(kWaves * 64), 0, stream, a);
+// Lanes and values of a row: 16 lanes of 4, 8 or 16 values up to 256 experts (reductions stay within a DPP row and a
+// wave works on four rows), more lanes past that, or where the chosen and one more do not fit the lanes.
+inline int lanes_of(int e, int k) { return e <= 256 && k < 16 ? 16 : (e <= 512 && k < 32 ? 32 : 64); }
+inline int values_of(int e, int lanes) {
+  const int v = (e + lanes - 1) / lanes;
+  return v <= 4 ? 4 : (v <= 8 ? 8 : 16);
 }
 
 }  // namespace route
@@ -376,22 +646,27 @@ dg_status sizes(int m, int e, int k, dg_dtype t, dg_score s) {
   return DG_SUCCESS;
 }
 
-inline int blocks_of(int m) {
-  const int b = (m + route::kWaves - 1) / route::kWaves;
+inline int blocks_of(int m, int e) {
+  const int rows = route::rows_at_once(route::lanes_of(e, 1));
+  const int b = (m + rows - 1) / rows;
   return b < 1 ? 1 : (b > route::kMaxBlocks ? route::kMaxBlocks : b);
 }
 
-#define DG_ROUTE_DISPATCH(FN, ARGS)                                                       \
-  do {                                                                                    \
-    const int v = (ARGS.e + 63) / 64;                                                     \
-    const bool bf = dtype == DG_DTYPE_BF16, sg = score == DG_SCORE_SIGMOID;               \
-    if (v <= 1) bf ? (sg ? FN<1, true, true>(ARGS, stream) : FN<1, true, false>(ARGS, stream))      \
-                   : (sg ? FN<1, false, true>(ARGS, stream) : FN<1, false, false>(ARGS, stream));   \
-    else if (v <= 4) bf ? (sg ? FN<4, true, true>(ARGS, stream) : FN<4, true, false>(ARGS, stream)) \
-                   : (sg ? FN<4, false, true>(ARGS, stream) : FN<4, false, false>(ARGS, stream));   \
-    else bf ? (sg ? FN<16, true, true>(ARGS, stream) : FN<16, true, false>(ARGS, stream))           \
-                   : (sg ? FN<16, false, true>(ARGS, stream) : FN<16, false, false>(ARGS, stream)); \
-  } while (0)
+// Calls f(lanes, values, bf16?, sigmoid?) with compile-time constants.
+template <int L, int V, typename F>
+void with_types(dg_dtype t, dg_score s, F f) {
+  using std::integral_constant;
+  auto lv = [&](auto bf, auto sg) { f(integral_constant<int, L>{}, integral_constant<int, V>{}, bf, sg); };
+  if (t == DG_DTYPE_BF16) s == DG_SCORE_SIGMOID ? lv(std::true_type{}, std::true_type{}) : lv(std::true_type{}, std::false_type{});
+  else s == DG_SCORE_SIGMOID ? lv(std::false_type{}, std::true_type{}) : lv(std::false_type{}, std::false_type{});
+}
+template <typename F>
+void with_variant(int e, int k, dg_dtype t, dg_score s, F f) {
+  const int l = route::lanes_of(e, k), v = route::values_of(e, l);
+  if (l == 16) v == 4 ? with_types<16, 4>(t, s, f) : (v == 8 ? with_types<16, 8>(t, s, f) : with_types<16, 16>(t, s, f));
+  else if (l == 32) v == 4 ? with_types<32, 4>(t, s, f) : (v == 8 ? with_types<32, 8>(t, s, f) : with_types<32, 16>(t, s, f));
+  else v == 4 ? with_types<64, 4>(t, s, f) : (v == 8 ? with_types<64, 8>(t, s, f) : with_types<64, 16>(t, s, f));
+}
 
 }  // namespace
 
@@ -399,7 +674,7 @@ extern "C" {
 
 size_t dg_get_moe_router_workspace_size(int m, int num_experts) {
   if (m <= 0 || num_experts <= 0 || num_experts > 1024) return 0;
-  return static_cast<size_t>(blocks_of(m)) * num_experts * 8;
+  return route::kHeader + static_cast<size_t>(blocks_of(m, num_experts)) * num_experts * 8;
 }
 
 dg_status dg_moe_router(const void* logits, int64_t ld, dg_dtype dtype, const float* bias, const void* mask, dg_score score,
@@ -419,15 +694,21 @@ dg_status dg_moe_router(const void* logits, int64_t ld, dg_dtype dtype, const fl
                                      workspace_bytes < dg_get_moe_router_workspace_size(m, num_experts)))
     return DG_ERROR_WORKSPACE;
   if (m == 0 && counts == nullptr) return DG_SUCCESS;
+  const int64_t ldb = ld * es;
+  const int vec = num_experts % 4 == 0 && aligned(logits, 4 * es) && ldb % (4 * es) == 0;
   route::Args a{static_cast<const uint8_t*>(logits), bias, static_cast<const uint8_t*>(mask), topk_ids, topk_weights, counts,
-                prob_sum, loss, static_cast<uint32_t*>(workspace),
-                reinterpret_cast<float*>(static_cast<uint32_t*>(workspace) + (size_t)blocks_of(m) * num_experts), ld * es,
-                scale, m, num_experts, top_k, normalize, blocks_of(m)};
+                prob_sum, loss, static_cast<uint8_t*>(workspace), ldb, scale, m, num_experts, top_k, normalize, 0, vec};
   if (m == 0) {
-    a.blocks = 0;
-    hipLaunchKernelGGL(route::finish_kernel, dim3(1), dim3(1024), 0, stream, a);
+    hipLaunchKernelGGL(route::zero_kernel, dim3(1), dim3(1024), 0, stream, a);
   } else {
-    DG_ROUTE_DISPATCH(route::run_forward, a);
+    with_variant(num_experts, top_k, dtype, score, [&](auto l, auto v, auto bf, auto sg) {
+      const int rows = route::rows_at_once(l), need = (m + rows - 1) / rows;
+      a.blocks = counts == nullptr ? need : std::min(need, blocks_of(m, num_experts));
+      hipLaunchKernelGGL((route::forward_kernel<l, v, bf, sg>), dim3(a.blocks), dim3(route::kWaves * 64), 0, stream, a);
+    });
+    if (counts != nullptr && a.blocks > 1)
+      hipLaunchKernelGGL(route::finish_kernel, dim3((num_experts + route::kFinishCols - 1) / route::kFinishCols), dim3(512), 0,
+                         stream, a);
   }
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? DG_SUCCESS : dg::record_hip_error(e);
@@ -447,9 +728,15 @@ dg_status dg_moe_router_backward(const void* logits, int64_t ld, dg_dtype dtype,
   if (logits == nullptr || !aligned(logits, es) || dlogits == nullptr || !aligned(dlogits, es) || topk_ids == nullptr ||
       !aligned(topk_ids, 4) || dweights == nullptr || !aligned(dweights, 4) || ld < num_experts || ld_dlogits < num_experts)
     return DG_ERROR_INVALID_VALUE;
+  const int64_t ldb = ld * es, ldd = ld_dlogits * es;
+  const int vec = num_experts % 4 == 0 && aligned(logits, 4 * es) && ldb % (4 * es) == 0 && aligned(dlogits, 4 * es) &&
+                  ldd % (4 * es) == 0;
   const route::GradArgs a{static_cast<const uint8_t*>(logits), topk_ids, dweights, counts, prob_sum, dloss,
-                          static_cast<uint8_t*>(dlogits), ld * es, ld_dlogits * es, scale, m, num_experts, top_k, normalize};
-  DG_ROUTE_DISPATCH(route::run_backward, a);
+                          static_cast<uint8_t*>(dlogits), ldb, ldd, scale, m, num_experts, top_k, normalize, vec};
+  with_variant(num_experts, top_k, dtype, score, [&](auto l, auto v, auto bf, auto sg) {
+    const int rows = route::rows_at_once(l), need = (m + rows - 1) / rows;
+    hipLaunchKernelGGL((route::backward_kernel<l, v, bf, sg>), dim3(std::min(need, 1024)), dim3(route::kWaves * 64), 0, stream, a);
+  });
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? DG_SUCCESS : dg::record_hip_error(e);
 }
