@@ -21,13 +21,13 @@ namespace {
 namespace route {
 
 constexpr float kTiny = 1e-20f;
-constexpr int kWaves = 8;        // waves per workgroup
-constexpr int kMaxBlocks = 520;  // workgroups of a large batch, each with its own partial sums
-constexpr int kFinishCols = 32;  // experts per workgroup of the second kernel
+constexpr int kWaves = 4;         // waves per workgroup
+constexpr int kMaxBlocks = 1280;  // workgroups of a large batch, each with its own partial sums
+constexpr int kFinishCols = 16;  // experts per workgroup of the second kernel
 
 // Workspace: a header (the count of finished workgroups, then three sums for each workgroup of the second kernel),
 // counts [blocks][E] and probability sums [blocks][E].
-constexpr size_t kHeader = 1024;
+constexpr size_t kHeader = 2048;
 
 struct Args {
   const uint8_t* logits;
@@ -121,28 +121,38 @@ __device__ __forceinline__ float load1(const uint8_t* row, int e) {
   else return reinterpret_cast<const float*>(row)[e];
 }
 
-// A row's values of a lane, -inf past the last expert.  vec: rows are aligned to four values and hold whole fours.
+// A row's values of a lane, -inf past the last expert (loaded at a clamped place, so that no load sits in a branch).
+// vec: rows are aligned to four values and hold whole fours.
 template <int L, int V, bool BF16>
 __device__ __forceinline__ void load_row(const uint8_t* row, int e, int vec, int l, float (&x)[V]) {
+  asm volatile("" : "+v"(l));  // places are worked out here, not kept in registers over the loop around
   if (vec) {
+    float4 v[V / 4];
 #pragma unroll
     for (int c = 0; c < V / 4; ++c) {
-      const int at = 4 * (l + L * c);
-      float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      if (at < e) {
-        if constexpr (BF16) {
-          const uint2 w = *reinterpret_cast<const uint2*>(row + 2 * at);
-          v = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                          __uint_as_float(w.y & 0xffff0000u));
-        } else {
-          v = *reinterpret_cast<const float4*>(row + 4 * at);
-        }
+      const int at = min(4 * (l + L * c), e - 4);
+      if constexpr (BF16) {
+        const uint2 w = *reinterpret_cast<const uint2*>(row + 2 * at);
+        v[c] = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                           __uint_as_float(w.y & 0xffff0000u));
+      } else {
+        v[c] = *reinterpret_cast<const float4*>(row + 4 * at);
       }
-      x[4 * c] = v.x, x[4 * c + 1] = v.y, x[4 * c + 2] = v.z, x[4 * c + 3] = v.w;
+    }
+#pragma unroll
+    for (int c = 0; c < V / 4; ++c) x[4 * c] = v[c].x, x[4 * c + 1] = v[c].y, x[4 * c + 2] = v[c].z, x[4 * c + 3] = v[c].w;
+    if (e == L * V) return;
+#pragma unroll
+    for (int c = 0; c < V / 4; ++c) {
+      const bool in = 4 * (l + L * c) < e;
+      x[4 * c] = in ? v[c].x : -INFINITY, x[4 * c + 1] = in ? v[c].y : -INFINITY;
+      x[4 * c + 2] = in ? v[c].z : -INFINITY, x[4 * c + 3] = in ? v[c].w : -INFINITY;
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = expert<L>(l, i) < e ? load1<BF16>(row, expert<L>(l, i)) : -INFINITY;
+    for (int i = 0; i < V; ++i) x[i] = load1<BF16>(row, min(expert<L>(l, i), e - 1));
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = expert<L>(l, i) < e ? x[i] : -INFINITY;
   }
 }
 
@@ -150,17 +160,14 @@ __device__ __forceinline__ void load_row(const uint8_t* row, int e, int vec, int
 struct Norm {
   float top, inv;
 };
-// exp(-|x|) decides a sigmoid without overflow; 1 - sigmoid(x) is sigmoid(-x).
-__device__ __forceinline__ float sigmoid(float x) {
-  const float t = __expf(-fabsf(x)), r = __builtin_amdgcn_rcpf(1.0f + t);
-  return x >= 0.f ? r : t * r;
-}
+// exp(-x) overflows to Inf where the sigmoid is below 2^-126: 0.  1 - sigmoid(x) is sigmoid(-x), without cancellation.
+__device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + __expf(-x)); }
 template <bool SIGMOID>
 __device__ __forceinline__ float score(float x, Norm n) {
   if constexpr (SIGMOID) return sigmoid(x);
   return __expf(x - n.top) * n.inv;
 }
-// Scores of a row; for sigmoids n.inv is 1 / (their sum + 1e-20).
+// A row's exponentials (a softmax is n.inv times them), or its sigmoids, for which n.inv is 1 / (their sum + 1e-20).
 template <int L, int V, bool SIGMOID>
 __device__ __forceinline__ Norm scores(const float (&x)[V], float (&p)[V]) {
   Norm n{0.f, 0.f};
@@ -185,18 +192,34 @@ __device__ __forceinline__ Norm scores(const float (&x)[V], float (&p)[V]) {
     }
     sum = sum_of<L>(sum);
     n.inv = sum == 0.f ? 0.f : 1.0f / sum;
-#pragma unroll
-    for (int i = 0; i < V; ++i) p[i] *= n.inv;
   }
   return n;
 }
 
-// Floats as unsigned integers of the same order, and back.
+// Floats as unsigned integers of the same order, and back.  -0 and 0 are one value; -inf and NaN are kDead at most.
+constexpr uint32_t kDead = 0x007fffffu;
 __device__ __forceinline__ uint32_t ordered(float v) {
-  const uint32_t b = __float_as_uint(v);
+  const uint32_t b = __float_as_uint(fmaxf(v, -INFINITY) + 0.0f);
   return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float unordered(uint32_t u) { return __uint_as_float((u >> 31) ? u ^ 0x80000000u : ~u); }
+
+// Scores plus bias further apart than kNear * (1 + |key|) are in the order of their FP32 values.  A sigmoid is off by at
+// most 6 steps of 2^-24 (the exponential's own and its argument's, each damped by p (1 - p), the sum, the reciprocal); a
+// softmax p by p (24 + 2 |ln p|) steps (a sum of 22 roundings at most), which for two scores of one row is under 26 steps
+// together; adding the bias rounds by half a step of the key: under 30 * 2^-24 < 2^-19.
+constexpr float kNear = 0x1p-19f;
+
+// The value one lane before (lane 0 of a row: its own).
+template <int L>
+__device__ __forceinline__ uint32_t before(uint32_t v) {
+  if constexpr (L == 16) return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x111, 0xF, 0xF, false);
+  else return __shfl_up(v, 1, L);
+}
+template <int L>
+__device__ __forceinline__ float before(float v) {
+  return __uint_as_float(before<L>(__float_as_uint(v)));
+}
 
 // Descending sort of V registers (odd-even merges: V = 4, 8, 16 take 5, 19, 63 exchanges).
 template <int V>
@@ -214,6 +237,27 @@ __device__ __forceinline__ void sort_desc(uint32_t (&k)[V]) {
             k[i + j] = max(a, b);
             k[i + j + q] = min(a, b);
           }
+}
+
+// exp(x) in FP64 for the exact choice: x = n ln 2 + r with |r| <= ln 2 / 2 (ln 2 in two parts, the first with 31 bits so that
+// n times it is exact), the series of exp(r) to r^13 / 13! (the next term is below 2^-57), times 2^n.  The coefficients
+// are read where they are used: as constants in the code they would fill registers all over the kernel.
+__device__ const double kInverseFactorials[14] = {1.0, 1.0, 1.0 / 2, 1.0 / 6, 1.0 / 24, 1.0 / 120, 1.0 / 720, 1.0 / 5040,
+                                                  1.0 / 40320, 1.0 / 362880, 1.0 / 3628800, 1.0 / 39916800,
+                                                  1.0 / 479001600, 1.0 / 6227020800};
+__device__ __forceinline__ double exp64(double x) {
+  typedef const __attribute__((address_space(4))) double* table_t;
+  uint64_t at = (uint64_t)(uintptr_t)kInverseFactorials;
+  asm volatile("" : "+s"(at));
+  const table_t c = (table_t)at;
+  x = fmin(fmax(x, -800.0), 800.0);  // 0 and Inf past that
+  const double n = rint(x * 0x1.71547652b82fep+0);
+  double r = __builtin_fma(n, -0x1.62e42fec00000p-1, x);
+  r = __builtin_fma(n, -0x1.d1cf79abc9e3bp-32, r);
+  double p = c[13];
+#pragma unroll
+  for (int k = 12; k >= 0; --k) p = __builtin_fma(p, r, c[k]);
+  return ldexp(p, (int)n);
 }
 
 // The choice for a row whose order FP32 leaves open, by a whole wave: every key in FP64, the largest taken k times.
@@ -242,7 +286,7 @@ __device__ __forceinline__ int choose_exact(const float* row, const float* bias,
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const bool live = key[i] > -INFINITY;
-      const double t = exp(SIGMOID ? -key[i] : key[i] - top);
+      const double t = exp64(SIGMOID ? -key[i] : key[i] - top);
       key[i] = live ? (SIGMOID ? 1.0 / (1.0 + t) : t) : -INFINITY;
       total += live ? t : 0.0;
     }
@@ -255,30 +299,41 @@ __device__ __forceinline__ int choose_exact(const float* row, const float* bias,
         if (!(key[i] > -INFINITY)) key[i] = -INFINITY;  // a bias of NaN
       }
   }
+  // the largest key as an unsigned integer of the same order, its upper word first, and of equal ones the lowest index
+  uint32_t hi[N], lo[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, key[i] + 0.0);
+    const uint64_t u = key[i] > -INFINITY ? b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull) : 0ull;
+    hi[i] = (uint32_t)(u >> 32), lo[i] = (uint32_t)u;
+  }
   int mine = -1;
   for (int j = 0; j < k; ++j) {
-    double best = key[0];
+    uint32_t top_hi = hi[0], top_lo = 0, at = 0;
 #pragma unroll
-    for (int i = 1; i < N; ++i) best = key[i] > best ? key[i] : best;
-    best = wave_max(best);
-    int at = 0x7fffffff;
+    for (int i = 1; i < N; ++i) top_hi = max(top_hi, hi[i]);
+    top_hi = max_of<64>(top_hi);
+    if (top_hi == 0) break;  // none is left
 #pragma unroll
-    for (int i = N - 1; i >= 0; --i)
-      if (key[i] == best) at = lane + 64 * i;
-    for (int o = 32; o >= 1; o >>= 1) at = min(at, __shfl_xor(at, o));
-    if (!(best > -INFINITY)) break;
+    for (int i = 0; i < N; ++i) top_lo = max(top_lo, hi[i] == top_hi ? lo[i] : 0u);
+    top_lo = max_of<64>(top_lo);
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (lane + 64 * i == at) key[i] = -INFINITY;
-    if (lane == j) mine = at;
+      at = max(at, hi[i] == top_hi && lo[i] == top_lo ? (uint32_t)(64 * N - (lane + 64 * i)) : 0u);
+    at = 64 * N - max_of<64>(at);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (lane + 64 * i == (int)at) hi[i] = lo[i] = 0;
+    if (lane == j) mine = (int)at;
   }
   return mine;
 }
 
 template <int L, int V, bool BF16, bool SIGMOID>
-__global__ void __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(L == 16 ? 4 : 2))) forward_kernel(const Args a) {
+__global__ void __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(L > 16 ? 2 : (SIGMOID ? 5 : 4)))) forward_kernel(const Args a) {
   constexpr int R = 64 / L;             // rows a wave works on
   constexpr int E = L * V;              // experts a row has room for
+  constexpr int D = V < 6 ? V : 5;      // how many of its largest keys a lane keeps
   constexpr uint32_t IDX = E - 1;       // low bits of a key: E - 1 - expert, so that ties go to the lower one
   __shared__ float s_x[kWaves * R][E];  // the rows at work; at the end their sums of scores
   __shared__ __attribute__((aligned(16))) float s_bias[E];
@@ -302,8 +357,9 @@ __global__ void __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_e
   const int first = (blockIdx.x * kWaves + wave) * R + grp;
   for (int base = first - grp; base < a.m; base += stride) {
     const int row = base + grp;
-    const bool on = row < a.m && (a.mask == nullptr || a.mask[row] != 0);
     float x[V], p[V];
+    const uint8_t there = a.mask != nullptr ? a.mask[min(row, a.m - 1)] : 1;
+    const bool on = row < a.m && there != 0;
     load_row<L, V, BF16>(a.logits + (int64_t)min(row, a.m - 1) * a.ld, a.e, a.vec, l, x);
     wave_sync();  // the last rows' reads are done
 #pragma unroll
@@ -311,19 +367,28 @@ __global__ void __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_e
       *reinterpret_cast<float4*>(xs + 4 * (l + L * c)) = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
     const Norm n = scores<L, V, SIGMOID>(x, p);
     if (stats && on) {
-      const float r = SIGMOID ? n.inv : 1.0f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) ps[i] += p[i] * r;
+      for (int i = 0; i < V; ++i) ps[i] += p[i] * n.inv;
     }
     // Keys: the value's leading bits, then the index.  What the index pushed out is looked at below.
     uint32_t key[V], lost = 0;
+    int lk = l;
+    asm volatile("" : "+v"(lk));
+    if (a.bias != nullptr) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      float v = x[i];
-      if (a.bias != nullptr) v = p[i] + s_bias[expert<L>(l, i)];
-      const uint32_t u = ordered(v + 0.0f);  // -0 and 0 are one value
-      lost |= __float_as_uint(v);
-      key[i] = (x[i] > -INFINITY && v > -INFINITY) ? (u & ~IDX) | (IDX - expert<L>(l, i)) : 0u;
+      for (int c = 0; c < V / 4; ++c) {
+        const float4 b = *reinterpret_cast<const float4*>(s_bias + 4 * (l + L * c));
+        const float v[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 4 * c; i < 4 * c + 4; ++i)
+          key[i] = (ordered(x[i] > -INFINITY ? (SIGMOID ? p[i] : p[i] * n.inv) + v[i & 3] : -INFINITY) & ~IDX) | (IDX - expert<L>(lk, i));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (!BF16) lost |= __float_as_uint(x[i]);
+        key[i] = (ordered(x[i]) & ~IDX) | (IDX - expert<L>(lk, i));
+      }
     }
     sort_desc<V>(key);
     wave_sync();
@@ -332,38 +397,42 @@ __global__ void __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_e
     auto take = [&]() {
       last = max_of<L>(key[0]);
       if (l == taken) mine = last;
-      const bool won = key[0] == last && last != 0;
+      const bool won = key[0] == last;
 #pragma unroll
-      for (int i = 0; i + 1 < V; ++i) key[i] = won ? key[i + 1] : key[i];
-      if (won) key[V - 1] = 0;
+      for (int i = 0; i + 1 < D; ++i) key[i] = won ? key[i + 1] : key[i];
+      if (won) key[D - 1] = 0;
       ++taken;
     };
     for (int j = 0; j < a.k; ++j) take();
     kth = last;
-    int id = mine != 0 ? (int)(IDX - (mine & IDX)) : -1;
+    int id = mine > kDead ? (int)(IDX - (mine & IDX)) : -1;
     // BF16 logits lose nothing, nor do FP32 ones whose last bits are zero
     const bool rough = a.bias != nullptr || (!BF16 && any_of<L>((lost & IDX) != 0, lane));
-    if (__any(rough)) {
+    // A lane whose kept keys are all taken may hide one that belongs to the chosen: left to the exact choice.
+    bool slow = D < V && any_of<L>(key[0] == 0, lane);
+    if (__any(rough || slow)) {
       // Take more until none of the rest can belong to the first k, as far as there are lanes for them.
       auto open = [&]() {
-        if (kth == 0 || last == 0) return false;
+        if (kth <= kDead || last <= kDead) return false;
         if (a.bias == nullptr) return (last | IDX) >= (kth & ~IDX);
         const float lo = unordered(kth & ~IDX), hi = unordered(last | IDX);
-        return !(lo - hi > 0x1p-18f * (1.0f + fabsf(lo)));
+        return !(lo - hi > kNear * (1.0f + fabsf(lo)));
       };
-      do take();
-      while (taken < L && __any(rough && open()));
-      bool slow = rough && open();
+      if (__any(rough)) {
+        do take();
+        while (taken < L && __any(rough && open()));
+        slow = slow || (rough && (open() || (D < V && any_of<L>(key[0] == 0, lane))));
+      }
       // the order of what was taken, by full FP32 values
-      id = mine != 0 ? (int)(IDX - (mine & IDX)) : -1;
+      id = mine > kDead ? (int)(IDX - (mine & IDX)) : -1;
       float xv = id >= 0 ? xs[id] : -INFINITY, bv = 0.f, v = xv;
       if (a.bias != nullptr && id >= 0) {
         bv = s_bias[id];
         v = score<SIGMOID>(xv, n) + bv;
       }
       for (int turn = 0; turn <= L; ++turn) {
-        const float up = __shfl_up(v, 1, L);
-        const int uid = __shfl_up(id, 1, L);
+        const float up = before<L>(v);
+        const int uid = (int)before<L>((uint32_t)id);
         const bool wrong = l > 0 && id >= 0 && (v > up || (v == up && id < uid));
         if (!__any(rough && wrong)) break;
         const bool high = (l + turn) & 1;  // of the pairs (odd, even) and (even, odd) by turns
@@ -375,8 +444,8 @@ __global__ void __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_e
         if (rough && pair && oid != id && (high ? !ahead : ahead)) v = ov, xv = ox, bv = ob, id = oid;
       }
       if (a.bias != nullptr) {
-        const float up = __shfl_up(v, 1, L), ux = __shfl_up(xv, 1, L), ub = __shfl_up(bv, 1, L);
-        const bool near = l > 0 && id >= 0 && !(up - v > 0x1p-18f * (1.0f + fabsf(v))) && !(xv == ux && bv == ub);
+        const float up = before<L>(v), ux = before<L>(xv), ub = before<L>(bv);
+        const bool near = l > 0 && id >= 0 && !(up - v > kNear * (1.0f + fabsf(v))) && !(xv == ux && bv == ub);
         slow = slow || any_of<L>(near, lane);
       }
       for (uint64_t left = __ballot(slow && on && l == 0); left != 0; left &= left - 1) {
@@ -436,11 +505,10 @@ __global__ void __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_e
 }
 
 // The workgroups' partial sums, kFinishCols experts to a workgroup; the last one to finish adds up the loss.
-__global__ void __launch_bounds__(512) finish_kernel(const Args a) {
-  constexpr int PARTS = 512 / kFinishCols;
-  __shared__ uint32_t s_c[PARTS][kFinishCols];
-  __shared__ double s_p[PARTS][kFinishCols];
-  __shared__ int s_last;
+__global__ void __launch_bounds__(1024) finish_kernel(const Args a) {
+  constexpr int PARTS = 1024 / kFinishCols;
+  __shared__ uint32_t s_c[16][kFinishCols];
+  __shared__ double s_p[16][kFinishCols];
   const int tid = threadIdx.x, col = tid % kFinishCols, part = tid / kFinishCols;
   const int e = blockIdx.x * kFinishCols + col;
   const uint32_t* part_counts = reinterpret_cast<const uint32_t*>(a.ws + kHeader);
@@ -454,19 +522,29 @@ __global__ void __launch_bounds__(512) finish_kernel(const Args a) {
       p += (double)part_probs[(size_t)b * a.e + e];
     }
   }
-  s_c[part][col] = n;
-  s_p[part][col] = p;
+  // the parts of a wave (lanes 16 and 32 apart), then the waves'
+  auto fold = [&]() {
+    for (int o = kFinishCols; o < 64; o <<= 1) n += __shfl_xor(n, o), p += __shfl_xor(p, o);
+  };
+  fold();
+  if ((tid & 63) < kFinishCols) s_c[tid >> 6][col] = n, s_p[tid >> 6][col] = p;
   __syncthreads();
   if (tid >= 64) return;
+  n = 0, p = 0;
+#pragma unroll
+  for (int i = 0; i < 16 / (64 / kFinishCols); ++i) {
+    const int w = part + i * (64 / kFinishCols);
+    n += s_c[w][col], p += s_p[w][col];
+  }
+  fold();
   double c = 0, cs = 0;
-  p = 0;
   if (tid < kFinishCols && e < a.e) {
-    n = 0;
-    for (int i = 0; i < PARTS; ++i) n += s_c[i][col], p += s_p[i][col];
     a.counts[e] = (int32_t)n;
     if (a.prob_sum != nullptr) a.prob_sum[e] = (float)p;
     c = n;
     cs = c * p;
+  } else {
+    p = 0;
   }
   if (a.loss == nullptr) return;
   for (int o = 32; o >= 1; o >>= 1) {
@@ -475,23 +553,29 @@ __global__ void __launch_bounds__(512) finish_kernel(const Args a) {
     cs += __shfl_xor(cs, o);
   }
   double* sums = reinterpret_cast<double*>(a.ws + 64);
+  int last = 0;
   if (tid == 0) {
     double* mine = sums + 3 * blockIdx.x;
     __hip_atomic_store(mine, c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     __hip_atomic_store(mine + 1, p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     __hip_atomic_store(mine + 2, cs, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    s_last = __hip_atomic_fetch_add(reinterpret_cast<uint32_t*>(a.ws), 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) + 1 ==
-             gridDim.x;
-    if (s_last) {
-      c = p = cs = 0;
-      for (uint32_t i = 0; i < gridDim.x; ++i) {
-        c += __hip_atomic_load(sums + 3 * i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        p += __hip_atomic_load(sums + 3 * i + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        cs += __hip_atomic_load(sums + 3 * i + 2, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      }
-      *a.loss = c * p == 0 ? 0.f : (float)(a.e * cs / (c * p));
-    }
+    last = __hip_atomic_fetch_add(reinterpret_cast<uint32_t*>(a.ws), 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) + 1 ==
+           gridDim.x;
   }
+  if (!__builtin_amdgcn_readfirstlane(last)) return;
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+  c = p = cs = 0;
+  if (tid < (int)gridDim.x) {  // at most 64 workgroups
+    c = __hip_atomic_load(sums + 3 * tid, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    p = __hip_atomic_load(sums + 3 * tid + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    cs = __hip_atomic_load(sums + 3 * tid + 2, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  for (int o = 32; o >= 1; o >>= 1) {
+    c += __shfl_xor(c, o);
+    p += __shfl_xor(p, o);
+    cs += __shfl_xor(cs, o);
+  }
+  if (tid == 0) *a.loss = c * p == 0 ? 0.f : (float)(a.e * cs / (c * p));
 }
 
 // A batch of no rows.
@@ -504,7 +588,7 @@ __global__ void __launch_bounds__(1024) zero_kernel(const Args a) {
 }
 
 template <int L, int V, bool BF16, bool SIGMOID>
-__global__ void __launch_bounds__(kWaves * 64) backward_kernel(const GradArgs a) {
+__global__ void __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(L > 16 ? 2 : 5))) backward_kernel(const GradArgs a) {
   constexpr int R = 64 / L, E = L * V;
   __shared__ float s_d[kWaves * R][E];  // the gradient by the chosen scores, 0 elsewhere
   __shared__ double s_red[2][kWaves];
@@ -516,8 +600,6 @@ __global__ void __launch_bounds__(kWaves * 64) backward_kernel(const GradArgs a)
   for (int i = 0; i < V; ++i) g[i] = 0.f;
   const int stride = gridDim.x * kWaves * R;
   const int first = (blockIdx.x * kWaves + wave) * R + grp;
-  float next[V];
-  load_row<L, V, BF16>(a.logits + (int64_t)min(first, a.m - 1) * a.ld, a.e, a.vec, l, next);
   if (a.counts != nullptr) {  // g_e = dloss * E * counts_e / (sum counts * sum prob_sum)
     double c = 0, s = 0;
     for (int e = tid; e < a.e; e += kWaves * 64) {
@@ -534,33 +616,34 @@ __global__ void __launch_bounds__(kWaves * 64) backward_kernel(const GradArgs a)
     for (int w = 0; w < kWaves; ++w) c += s_red[0][w], s += s_red[1][w];
     const float f = c * s == 0 ? 0.f : (float)((double)*a.dloss * a.e / (c * s));
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (expert<L>(l, i) < a.e) g[i] = f * (float)a.counts[expert<L>(l, i)];
+    for (int i = 0; i < V; ++i) g[i] = (float)a.counts[min(expert<L>(l, i), a.e - 1)];
+#pragma unroll
+    for (int i = 0; i < V; ++i) g[i] = expert<L>(l, i) < a.e ? f * g[i] : 0.f;
   }
   for (int base = first - grp; base < a.m; base += stride) {
     const int row = min(base + grp, a.m - 1);
     float x[V], p[V];
+    const int64_t slot = (int64_t)row * a.k + min(l, a.k - 1);
+    const int slot_id = a.ids[slot];
+    const float slot_dw = a.dw[slot];
+    load_row<L, V, BF16>(a.logits + row * a.ld, a.e, a.vec, l, x);
+    const int id = l < a.k && (uint32_t)slot_id < (uint32_t)a.e ? slot_id : -1;
+    float d = id >= 0 ? a.scale * slot_dw : 0.f;
+    wave_sync();
+    if (a.normalize) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = next[i];
-    int id = -1;
-    float d = 0.f, xv = -INFINITY;
-    if (l < a.k) {
-      id = a.ids[(int64_t)row * a.k + l];
-      if ((uint32_t)id >= (uint32_t)a.e) id = -1;
-      if (id >= 0) {
-        d = a.scale * a.dw[(int64_t)row * a.k + l];
-        xv = load1<BF16>(a.logits + (int64_t)row * a.ld, id);
-      }
+      for (int c = 0; c < V / 4; ++c)
+        *reinterpret_cast<float4*>(ds + 4 * (l + L * c)) = make_float4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
+      wave_sync();
     }
-    if (base + stride < a.m)
-      load_row<L, V, BF16>(a.logits + (int64_t)min(base + grp + stride, a.m - 1) * a.ld, a.e, a.vec, l, next);
+    const float xv = a.normalize && id >= 0 ? ds[id] : -INFINITY;
     wave_sync();
 #pragma unroll
     for (int c = 0; c < V / 4; ++c) *reinterpret_cast<float4*>(ds + 4 * (l + L * c)) = make_float4(0.f, 0.f, 0.f, 0.f);
     const Norm n = scores<L, V, SIGMOID>(x, p);
     const bool on = any_of<L>(id >= 0, lane);
     if (a.normalize) {
-      const float w = id >= 0 ? score<SIGMOID>(xv, n) : 0.f;
+      const float w = score<SIGMOID>(xv, n);  // 0 where there is no expert
       const float r = 1.0f / (sum_of<L>(w) + kTiny);
       d = (d - sum_of<L>(d * w) * r) * r;
     }
@@ -579,13 +662,12 @@ __global__ void __launch_bounds__(kWaves * 64) backward_kernel(const GradArgs a)
       dot = sum_of<L>(dot) * n.inv;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        // p (1 - p), the second factor without cancellation: t / (1 + t) or 1 / (1 + t)
-        const float q = x[i] >= 0.f ? __expf(-x[i]) * p[i] : __builtin_amdgcn_rcpf(1.0f + __expf(x[i]));
-        dp[i] = (dp[i] + (g[i] - dot) * n.inv) * p[i] * q;
+        dp[i] = (dp[i] + (g[i] - dot) * n.inv) * p[i] * sigmoid(-x[i]);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
+        p[i] *= n.inv;
         dp[i] += g[i];
         dot += dp[i] * p[i];
       }
@@ -703,11 +785,13 @@ dg_status dg_moe_router(const void* logits, int64_t ld, dg_dtype dtype, const fl
   } else {
     with_variant(num_experts, top_k, dtype, score, [&](auto l, auto v, auto bf, auto sg) {
       const int rows = route::rows_at_once(l), need = (m + rows - 1) / rows;
-      a.blocks = counts == nullptr ? need : std::min(need, blocks_of(m, num_experts));
+      // as many workgroups as give each the same number of rounds, at most
+      const int most = blocks_of(m, num_experts), rounds = (need + most - 1) / most;
+      a.blocks = counts == nullptr ? need : (need + rounds - 1) / rounds;
       hipLaunchKernelGGL((route::forward_kernel<l, v, bf, sg>), dim3(a.blocks), dim3(route::kWaves * 64), 0, stream, a);
     });
     if (counts != nullptr && a.blocks > 1)
-      hipLaunchKernelGGL(route::finish_kernel, dim3((num_experts + route::kFinishCols - 1) / route::kFinishCols), dim3(512), 0,
+      hipLaunchKernelGGL(route::finish_kernel, dim3((num_experts + route::kFinishCols - 1) / route::kFinishCols), dim3(1024), 0,
                          stream, a);
   }
   const hipError_t e = hipGetLastError();
@@ -735,7 +819,9 @@ dg_status dg_moe_router_backward(const void* logits, int64_t ld, dg_dtype dtype,
                           static_cast<uint8_t*>(dlogits), ldb, ldd, scale, m, num_experts, top_k, normalize, vec};
   with_variant(num_experts, top_k, dtype, score, [&](auto l, auto v, auto bf, auto sg) {
     const int rows = route::rows_at_once(l), need = (m + rows - 1) / rows;
-    hipLaunchKernelGGL((route::backward_kernel<l, v, bf, sg>), dim3(std::min(need, 1024)), dim3(route::kWaves * 64), 0, stream, a);
+    const int rounds = (need + route::kMaxBlocks - 1) / route::kMaxBlocks;
+    hipLaunchKernelGGL((route::backward_kernel<l, v, bf, sg>), dim3((need + rounds - 1) / rounds), dim3(route::kWaves * 64), 0,
+                       stream, a);
   });
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? DG_SUCCESS : dg::record_hip_error(e);
