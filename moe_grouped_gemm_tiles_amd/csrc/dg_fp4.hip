@@ -46,6 +46,17 @@ __device__ __forceinline__ f32x4 mfma(i32x4 x, i32x4 y, f32x4 c, int sx, int sy)
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, kE2M1, kE2M1, T, sx, T, sy);
 }
 
+// A lane's part of a 16-row fragment of a slab: blocks 2q and 2q + 1 of its row, and their two scale bytes.
+struct Frag {
+  i32x4 lo, hi;
+  int s;
+};
+
+// One persistent kernel for every entry point.  The schedule of a slab is the FP8 GEMM's: the operand with fewer fragments
+// per wave ("outer") stays in registers for the slab, the other ("inner") is streamed from LDS; the last HOLD inner fragments
+// are held back, so that after the slab's one barrier, placed between part 1 and part 2, the matrix cores run from registers
+// while the next slab's outer fragments are read and the loads of the slab after it go out.  Each step is two MFMAs on an
+// accumulator, the first halves of a fragment's products before the second ones, so that none waits for the one before.
 template <int BM, int BN, int WM, int WN, int MODE, bool BF16_OUT, bool HAS_C>
 __global__ void __launch_bounds__(WM * WN * 64) gemm_kernel(const Params pp) {
   const dg::Params& p = pp.g;
@@ -54,11 +65,19 @@ __global__ void __launch_bounds__(WM * WN * 64) gemm_kernel(const Params pp) {
   constexpr int FM = TM / 16, FN = TN / 16;
   constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
   constexpr int SA_OFF = A_BYTES + B_BYTES, SB_OFF = SA_OFF + 2 * BM * 4;
-  constexpr int STAGE = SB_OFF + 2 * BN * 4;
-  constexpr int A_LOADS = BM / 8 / NW, B_LOADS = BN / 8 / NW;
-  static_assert(A_LOADS * NW * 8 == BM && B_LOADS * NW * 8 == BN, "whole loads");
+  constexpr int STAGE = (SB_OFF + 2 * BN * 4 + 255) / 256 * 256;
+  constexpr int A_TOTAL = BM / 8, B_TOTAL = BN / 8;  // 1 KiB (8-row) direct loads of a slab
+  constexpr int A_LOADS = (A_TOTAL + NW - 1) / NW, B_LOADS = (B_TOTAL + NW - 1) / NW, LOADS = A_LOADS + B_LOADS;
+  constexpr bool A_OUTER = FM < FN;
+  constexpr int NO = A_OUTER ? FM : FN, NI = A_OUTER ? FN : FM;
+  constexpr int HOLD = 2, FIRST = NI - HOLD;
+  // the first half of a slab's loads goes out in part 2 of the slab two before it, the rest in the next part 1
+  constexpr int P1L = LOADS / 2, P2L = LOADS - P1L;
+  static_assert(TM % 16 == 0 && TN % 16 == 0 && BM % 8 == 0 && BN % 8 == 0, "whole MFMA tiles and loads");
   static_assert(NW >= 4, "the four scale loads ride on different waves");
   static_assert(BM <= 256 && BN <= 256, "a scale row is one load");
+  static_assert(FIRST >= HOLD && NO >= 2 && P2L <= 2 * NO * HOLD && P1L <= 2 * NO * FIRST, "two-part slab schedule");
+  static_assert(MODE != dg::MODE_CONTIG || BM == 128 || BM == 256, "contiguous tiles cover one or two 128-row blocks");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * STAGE];
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -67,107 +86,298 @@ __global__ void __launch_bounds__(WM * WN * 64) gemm_kernel(const Params pp) {
   const int r16 = lane & 15, q4 = lane >> 4;
   const int slabs = (pp.kw + 1) >> 1;
   const int tiles_mn = p.tiles_m * p.tiles_n;
-  // chunks 2 * q4 and 2 * q4 + 1 of a fragment's row, swizzled (rows of one fragment share r & 15)
+  // chunks 2 * q4 and 2 * q4 + 1 of a fragment's row, swizzled (the rows of a fragment share r16)
   const int f = ((r16 >> 1) & 1) | ((r16 >> 3) << 2);
   const int ch0 = ((2 * q4) ^ f) << 4, ch1 = ((2 * q4 + 1) ^ f) << 4;
-  // direct loads: LDS byte 16 * lane of a 1 KiB block (8 rows) is row lane / 8, chunk lane % 8
+  // direct loads: LDS byte 16 * lane of a 1 KiB block is row lane / 8, chunk lane % 8
   const int ld_row = lane >> 3;
+
+  // Work units: (tile, pass); a contiguous tile whose two 128-row halves belong to different groups takes one pass per group.
+  // Group data is read through the constant address space: scalar loads do not share the vector-memory counter with the
+  // slabs in flight.
+  const __attribute__((address_space(4))) int32_t* grp_s = (const __attribute__((address_space(4))) int32_t*)p.grp;
+  struct Unit {
+    int tile, more, g, halves, m0, n0, row_end;  // tile < 0: no unit; more: a second pass follows; halves: whose rows are g's
+  };
+  auto find_unit = [&](int tile, int pass) {
+    Unit u;
+    u.tile = -1;
+    for (; tile < p.num_tiles; tile += gridDim.x, pass = 0) {
+      int g = 0, t = tile;
+      if (MODE == dg::MODE_MASKED) {
+        g = t / tiles_mn;
+        t -= g * tiles_mn;
+      }
+      int mb, nb;
+      dg::raster<4>(t, p.tiles_m, p.tiles_n, mb, nb);
+      const int m0 = mb * BM;
+      int row_end = p.m, halves = 3, more = 0;
+      if (MODE == dg::MODE_MASKED) {
+        row_end = min(max(grp_s[g], 0), p.m);
+        if (m0 >= row_end) continue;
+      } else if (MODE == dg::MODE_CONTIG) {
+        int g0 = grp_s[m0];
+        int g1 = (BM == 256 && m0 + 128 < p.m) ? grp_s[m0 + 128] : -1;
+        if (g0 < 0 || g0 >= p.num_groups) g0 = -1;
+        if (g1 < 0 || g1 >= p.num_groups) g1 = -1;
+        if (g0 < 0 && g1 < 0) continue;
+        if (g0 < 0) g0 = g1;
+        if (g1 < 0) g1 = g0;
+        more = pass == 0 && g0 != g1;
+        g = pass == 0 ? g0 : g1;
+        halves = (g0 == g ? 1 : 0) | (g1 == g ? 2 : 0);
+      }
+      u.tile = tile;
+      u.more = more;
+      u.g = g;
+      u.halves = halves;
+      u.m0 = m0;
+      u.n0 = nb * BN;
+      u.row_end = row_end;
+      break;
+    }
+    return u;
+  };
+  auto next_unit = [&](const Unit& u) {
+    return u.more ? find_unit(u.tile, 1) : find_unit(u.tile + (int)gridDim.x, 0);
+  };
+
+  // A unit's descriptors, fixed over K: slab, block and scale row are part of the offsets.  Each ends at the unit's last row
+  // (its last scale), below 2^31, so that offsets from kPast on read zero.
+  constexpr uint32_t kPast = 0x80000000u;
+  struct Src {
+    __amdgpu_buffer_rsrc_t ra, rb, rs;  // rs: the scales that this wave loads, A's on waves 0 and 1, B's on 2 and 3
+  };
+  const uint32_t ld_s = (uint32_t)(wave < 2 ? p.ld_sfa : pp.ld_sfb) * 4;
+  auto src_of = [&](const Unit& u) {
+    Src r;
+    // (rows past masked_m are read as zeros, without memory)
+    const int a_rows = min(u.row_end - u.m0, BM), b_rows = min(p.n - u.n0, BN);
+    r.ra = dg::make_rsrc(p.a + (MODE == dg::MODE_MASKED ? u.g * p.a_gs : 0) + (int64_t)u.m0 * p.lda, (uint32_t)(a_rows * p.lda));
+    r.rb = dg::make_rsrc(p.b + (MODE != dg::MODE_DENSE ? u.g * p.b_gs : 0) + (int64_t)u.n0 * p.ldb, (uint32_t)(b_rows * p.ldb));
+    const float* s = wave < 2 ? p.sfa + (MODE == dg::MODE_MASKED ? u.g * p.sfa_gs : 0) + u.m0
+                              : p.sfb + (MODE != dg::MODE_DENSE ? u.g * p.sfb_gs : 0) + u.n0;
+    r.rs = dg::make_rsrc(s, pp.kw > 0 ? (uint32_t)(pp.kw - 1) * ld_s + 4u * (wave < 2 ? a_rows : b_rows) : 0u);
+    return r;
+  };
+
+  // Direct loads: the lane's row and chunk within an 8-row block; blocks alternate in the swizzle's upper bit.
+  const int chunk0 = (lane & 7) ^ ((ld_row >> 1) & 1);
+  const uint32_t a_off = (uint32_t)(ld_row * p.lda) + chunk0 * 16, b_off = (uint32_t)(ld_row * p.ldb) + chunk0 * 16;
+  const uint32_t a_blk = (uint32_t)(8 * p.lda), b_blk = (uint32_t)(8 * p.ldb);
+  const uint32_t odd_flip = chunk0 >= 4 ? (uint32_t)-64 : 64u;  // from chunk c to c ^ 4
+  // A slab past K is loaded too, from offsets that read zero, so that each slab issues the same loads; of a slab that K
+  // fills by half, so are the lanes that hold the second half (chunk >= 4).
+  auto load16 = [&](__amdgpu_buffer_rsrc_t r, uint8_t* to, uint32_t off, int blk, uint32_t blk_bytes, int slab) {
+    const bool odd = blk & 1;
+    uint32_t at = slab < slabs ? (uint32_t)blk * blk_bytes + (uint32_t)slab * 128 : kPast;
+    asm volatile("" : "+s"(at));  // added here, not kept as one sum per load in registers
+    uint32_t v = (odd ? off + odd_flip : off) + at;
+    if (2 * slab + 2 > pp.kw && ((chunk0 >= 4) != odd)) v = kPast;
+    dg::load_to_lds<16, false>(r, to, v);
+  };
+  auto issue_load = [&](const Src& r, int slab, int stage, int idx) {
+    uint8_t* base = lds + stage * STAGE;
+    if (idx < A_LOADS) {
+      const int blk = wave * A_LOADS + idx;
+      if (A_LOADS * NW == A_TOTAL || blk < A_TOTAL) load16(r.ra, base + blk * 1024, a_off, blk, a_blk, slab);
+    } else {
+      const int blk = wave * B_LOADS + idx - A_LOADS;
+      if (B_LOADS * NW == B_TOTAL || blk < B_TOTAL) load16(r.rb, base + A_BYTES + blk * 1024, b_off, blk, b_blk, slab);
+    }
+    if (idx == 0 && wave < 4) {
+      const int w = 2 * slab + (wave & 1), len = wave < 2 ? BM : BN;
+      if (lane < len / 4)
+        dg::load_to_lds<16, false>(r.rs, base + (wave < 2 ? SA_OFF : SB_OFF) + (wave & 1) * len * 4,
+                                   (w < pp.kw ? (uint32_t)w * ld_s : kPast) + lane * 16);
+    }
+  };
+  auto issue_slab = [&](const Src& r, int slab, int stage) {
+#pragma unroll
+    for (int idx = 0; idx < LOADS; ++idx) issue_load(r, slab, stage, idx);
+  };
+
+  const uint8_t* As0 = lds + (wm * TM + r16) * 128;
+  const uint8_t* Bs0 = lds + A_BYTES + (wn * TN + r16) * 128;
+  const uint8_t* Sa0 = lds + SA_OFF + (q4 >> 1) * BM * 4 + (wm * TM + r16) * 4 + (q4 & 1) * 2;
+  const uint8_t* Sb0 = lds + SB_OFF + (q4 >> 1) * BN * 4 + (wn * TN + r16) * 4 + (q4 & 1) * 2;
+  auto read_frag = [&](const uint8_t* rows, const uint8_t* scales, int i) {
+    Frag r;
+    r.lo = *reinterpret_cast<const i32x4*>(rows + i * 2048 + ch0);
+    r.hi = *reinterpret_cast<const i32x4*>(rows + i * 2048 + ch1);
+    r.s = *reinterpret_cast<const uint16_t*>(scales + i * 64);
+    return r;
+  };
+  const uint8_t *Is0 = A_OUTER ? Bs0 : As0, *Os0 = A_OUTER ? As0 : Bs0;
+  const uint8_t *Si0 = A_OUTER ? Sb0 : Sa0, *So0 = A_OUTER ? Sa0 : Sb0;
+
   const int vb = dg::xcd_remap(blockIdx.x, gridDim.x);
-  for (int unit = vb; unit < p.num_tiles; unit += gridDim.x) {
-    int g = 0, t = unit;
-    if (MODE == dg::MODE_MASKED) {
-      g = t / tiles_mn;
-      t -= g * tiles_mn;
-    }
-    int mb, nb;
-    dg::raster<4>(t, p.tiles_m, p.tiles_n, mb, nb);
-    const int m0 = mb * BM, n0 = nb * BN;
-    int row_end = p.m;
-    if (MODE == dg::MODE_MASKED) {
-      row_end = min(max(p.grp[g], 0), p.m);
-      if (m0 >= row_end) continue;
-    } else if (MODE == dg::MODE_CONTIG) {
-      g = p.grp[m0];
-      if (g < 0 || g >= p.num_groups) continue;
-    }
-    const uint8_t* A = p.a + (MODE == dg::MODE_MASKED ? g * p.a_gs : 0) + (int64_t)m0 * p.lda;
-    const uint8_t* B = p.b + (MODE != dg::MODE_DENSE ? g * p.b_gs : 0) + (int64_t)n0 * p.ldb;
-    const float* SA = p.sfa + (MODE == dg::MODE_MASKED ? g * p.sfa_gs : 0) + m0;
-    const float* SB = p.sfb + (MODE != dg::MODE_DENSE ? g * p.sfb_gs : 0) + n0;
-    const int a_rows = min(row_end - m0, BM), b_rows = min(p.n - n0, BN);
-
-    auto issue = [&](int slab, int stage) {
-      uint8_t* base = lds + stage * STAGE;
-      const bool half = 2 * slab + 2 > pp.kw;  // the slab's second 128 values are past K
-      const auto ra = dg::make_rsrc(A + slab * 128, dg::clamp_bytes(a_rows * p.lda - slab * 128));
-      const auto rb = dg::make_rsrc(B + slab * 128, dg::clamp_bytes(b_rows * p.ldb - slab * 128));
-#pragma unroll
-      for (int i = 0; i < A_LOADS; ++i) {
-        const int blk = wave * A_LOADS + i, chunk = (lane & 7) ^ (((ld_row >> 1) & 1) | ((blk & 1) << 2));
-        uint32_t off = (uint32_t)((blk * 8 + ld_row) * p.lda) + chunk * 16;
-        if (half && chunk >= 4) off = 0x80000000u;
-        dg::load_to_lds<16, false>(ra, base + blk * 1024, off);
-      }
-#pragma unroll
-      for (int i = 0; i < B_LOADS; ++i) {
-        const int blk = wave * B_LOADS + i, chunk = (lane & 7) ^ (((ld_row >> 1) & 1) | ((blk & 1) << 2));
-        uint32_t off = (uint32_t)((blk * 8 + ld_row) * p.ldb) + chunk * 16;
-        if (half && chunk >= 4) off = 0x80000000u;
-        dg::load_to_lds<16, false>(rb, base + A_BYTES + blk * 1024, off);
-      }
-      if (wave < 4) {
-        const int w = 2 * slab + (wave & 1), rows = wave < 2 ? a_rows : b_rows, bl = wave < 2 ? BM : BN;
-        const auto rs = dg::make_rsrc((wave < 2 ? SA + w * p.ld_sfa : SB + w * pp.ld_sfb),
-                                      w < pp.kw ? dg::clamp_bytes(rows * 4) : 0u);
-        if (lane < bl / 4)
-          dg::load_to_lds<16, false>(rs, base + (wave < 2 ? SA_OFF : SB_OFF) + (wave & 1) * bl * 4, lane * 16);
-      }
-    };
-
+  Unit u = find_unit(vb, 0), nx;
+  bool pre = false;  // slabs 0 and 1 of this unit have been issued
+  while (u.tile >= 0) {
+    const int g = u.g, m0 = u.m0, n0 = u.n0, row_end = u.row_end;
+    const int wrow0 = m0 + wm * TM;
+    bool wave_live = wrow0 < row_end;
+    if (MODE == dg::MODE_CONTIG && BM == 256) wave_live = wave_live && (u.halves >> ((wm * TM) >> 7) & 1);
+    const Src sr = src_of(u);
     f32x4 acc[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    __syncthreads();  // the last tile's reads are done
-    if (slabs > 0) issue(0, 0);
-    for (int it = 0; it < slabs; ++it) {
-      __syncthreads();  // slab it has landed (all loads waited for), slab it - 1 has been read
-      if (it + 1 < slabs) issue(it + 1, (it + 1) & 1);
-      const uint8_t* st = lds + (it & 1) * STAGE;
-      i32x4 b0[FN], b1[FN];
-      int sb[FN];
-#pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        const int row = wn * TN + j * 16 + r16;
-        b0[j] = *reinterpret_cast<const i32x4*>(st + A_BYTES + row * 128 + ch0);
-        b1[j] = *reinterpret_cast<const i32x4*>(st + A_BYTES + row * 128 + ch1);
-        sb[j] = *reinterpret_cast<const uint16_t*>(st + SB_OFF + (q4 >> 1) * BN * 4 + row * 4 + (q4 & 1) * 2);
+    auto mma = [&](int o, int n, int half, const Frag& x, const Frag& y) {
+      const int i = A_OUTER ? o : n, j = A_OUTER ? n : o;
+      const Frag &b = A_OUTER ? y : x, &a = A_OUTER ? x : y;
+      if (half == 0) acc[i][j] = mfma<0>(b.lo, a.lo, acc[i][j], b.s, a.s);
+      else acc[i][j] = mfma<1>(b.hi, a.hi, acc[i][j], b.s, a.s);
+    };
+    if (slabs > 0) {
+      if (!pre) {
+        issue_slab(sr, 0, 0);
+        dg::wait_vmcnt<0>();
+      } else {
+        dg::wait_vmcnt<0>();
       }
+      dg::stage_barrier();
+      if (!pre) issue_slab(sr, 1, 1);
+      dg::debug_fence();
+      Frag fo[NO], fh[HOLD];
+      fo[0] = read_frag(Os0, So0, 0);
+      Frag fi = read_frag(Is0, Si0, 0), fi_next = fi;
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int o = 1; o < NO; ++o) {
+        fo[o] = read_frag(Os0, So0, o);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      for (int it = 0; it < slabs; ++it) {
+        const int cur = it & 1, nxt = cur ^ 1;
+        const uint8_t *Is = Is0 + cur * STAGE, *Si = Si0 + cur * STAGE;
+        // the last P1L loads of slab it + 1 (slab 1 went out whole)
+        const bool late = it > 0;
+        if (wave_live) {
+#pragma unroll
+          for (int n = 0; n < FIRST; ++n) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int o = 0; o < NO; ++o) {
+                const int t = (n * 2 + h) * NO + o;
+                if (h == 0 && o == 0 && n + 1 < FIRST) fi_next = read_frag(Is, Si, n + 1);
+                if (h == 1 && o == 0 && n < HOLD) fh[n] = read_frag(Is, Si, FIRST + n);
+                mma(o, n, h, fo[o], fi);
+                if (t % 2 == 0 && t / 2 < P1L && late) issue_load(sr, it + 1, nxt, P2L + t / 2);
+              }
+            if (n + 1 < FIRST) fi = fi_next;
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        } else if (late) {
+#pragma unroll
+          for (int idx = P2L; idx < LOADS; ++idx) issue_load(sr, it + 1, nxt, idx);
+        }
+        dg::debug_fence();
+        dg::wait_vmcnt<0>();  // slab it + 1 has landed (this wave's part of it)
+        dg::stage_barrier();
+        if (wave_live) {
+          // (after the last slab the reads of the next stage are stale and unused)
+#pragma unroll
+          for (int o = 0; o < NO; ++o) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int n = 0; n < HOLD; ++n) {
+                const int t = (o * 2 + h) * HOLD + n;
+                mma(o, FIRST + n, h, fo[o], fh[n]);
+                if (t % 2 == 0 && t / 2 < P2L) issue_load(sr, it + 2, cur, t / 2);
+              }
+            fo[o] = read_frag(Os0 + nxt * STAGE, So0 + nxt * STAGE, o);
+            if (o == 0) fi = read_frag(Is0 + nxt * STAGE, Si0 + nxt * STAGE, 0);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+#pragma unroll
+          for (int idx = NO * HOLD; idx < P2L; ++idx) issue_load(sr, it + 2, cur, idx);
+        } else {
+#pragma unroll
+          for (int idx = 0; idx < P2L; ++idx) issue_load(sr, it + 2, cur, idx);
+        }
+        dg::debug_fence();
+      }
+    }
+    dg::stage_barrier();  // all LDS reads of this unit are done before the next unit's loads
+    dg::debug_fence();
+
+    // Contiguous: the group of each row this lane stores, loaded before the next unit's slabs (the vector-memory counter
+    // completes in order), at a clamped row, so that no load sits in a branch.
+    int row_grp[MODE == dg::MODE_CONTIG ? FM : 1];
+    if constexpr (MODE == dg::MODE_CONTIG) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i) row_grp[i] = p.grp[min(wrow0 + r16 + i * 16, row_end - 1)];
+      asm volatile("" ::: "memory");
+    }
+    // The next unit's first two slabs go out before this unit's stores (slabs past K, which read nothing, if there is none).
+    nx = next_unit(u);
+    pre = nx.tile >= 0;
+    const Src ns = src_of(pre ? nx : u);
+    issue_slab(ns, pre ? 0 : slabs, 0);
+    issue_slab(ns, pre ? 1 : slabs + 1, 1);
+    asm volatile("" ::: "memory");
+    if (wave_live) {
+      int row0 = wrow0 + r16;
+      asm volatile("" : "+v"(row0));  // row addresses are worked out here, not above the K loop
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
-        const int row = wm * TM + i * 16 + r16;
-        const i32x4 a0 = *reinterpret_cast<const i32x4*>(st + row * 128 + ch0);
-        const i32x4 a1 = *reinterpret_cast<const i32x4*>(st + row * 128 + ch1);
-        const int sa = *reinterpret_cast<const uint16_t*>(st + SA_OFF + (q4 >> 1) * BM * 4 + row * 4 + (q4 & 1) * 2);
+        const int gm = row0 + i * 16;
+        bool row_ok = gm < row_end;
+        if constexpr (MODE == dg::MODE_CONTIG) row_ok = row_ok && row_grp[i] == g;
+        const int64_t drow = (MODE == dg::MODE_MASKED ? g * p.d_gs : 0) + (int64_t)gm * p.ldd;
+        const int64_t crow = (int64_t)gm * p.ldc;
+        if constexpr (BF16_OUT) {
+          // Column fragments j, j + 1: a permlane16 swap per pair of words leaves each lane eight consecutive columns, one
+          // 16-byte store (as in the FP8 GEMM).  C is added in the MFMA layout first.
 #pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = mfma<0>(b0[j], a0, acc[i][j], sb[j], sa);
+          for (int j = 0; j + 1 < FN; j += 2) {
+            if (HAS_C && row_ok) {
 #pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = mfma<1>(b1[j], a1, acc[i][j], sb[j], sa);
+              for (int h = 0; h < 2; ++h) {
+                const int gc = n0 + wn * TN + (j + h) * 16 + 4 * q4;
+                if (gc < p.n) dg::add_c_bf16(p, crow, gc, acc[i][j + h]);
+              }
+            }
+            const auto s0 = __builtin_amdgcn_permlane16_swap(dg::bf16x2_rne_bits(acc[i][j][0], acc[i][j][1]),
+                                                             dg::bf16x2_rne_bits(acc[i][j + 1][0], acc[i][j + 1][1]), false, false);
+            const auto s1 = __builtin_amdgcn_permlane16_swap(dg::bf16x2_rne_bits(acc[i][j][2], acc[i][j][3]),
+                                                             dg::bf16x2_rne_bits(acc[i][j + 1][2], acc[i][j + 1][3]), false, false);
+            const int gn = n0 + wn * TN + (j + (q4 & 1)) * 16 + 8 * (q4 >> 1);
+            if (!row_ok || gn >= p.n) continue;
+            uint16_t* D = reinterpret_cast<uint16_t*>(p.d) + drow + gn;
+            const uint32_t w[4] = {s0[0], s1[0], s0[1], s1[1]};
+            if (gn + 8 <= p.n) {
+              *reinterpret_cast<uint4*>(D) = make_uint4(w[0], w[1], w[2], w[3]);
+            } else {
+#pragma unroll
+              for (int c = 0; c < 8; ++c)
+                if (gn + c < p.n) D[c] = (uint16_t)(w[c >> 1] >> (16 * (c & 1)));
+            }
+          }
+          if constexpr (FN % 2 == 1) {
+            const int gn = n0 + wn * TN + (FN - 1) * 16 + 4 * q4;
+            if (row_ok && gn < p.n) dg::store_out<BF16_OUT, HAS_C>(p, crow, gn, drow, acc[i][FN - 1]);
+          }
+        } else {
+          if (!row_ok) continue;
+#pragma unroll
+          for (int j = 0; j < FN; ++j) {
+            const int gn = n0 + wn * TN + j * 16 + 4 * q4;
+            if (gn < p.n) dg::store_out<BF16_OUT, HAS_C>(p, crow, gn, drow, acc[i][j]);
+          }
+        }
       }
     }
-#pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      const int gm = m0 + wm * TM + i * 16 + r16;
-      if (gm >= row_end || (MODE == dg::MODE_CONTIG && p.grp[gm] != g)) continue;
-      const int64_t drow = (MODE == dg::MODE_MASKED ? g * p.d_gs : 0) + (int64_t)gm * p.ldd;
-#pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        const int gn = n0 + wn * TN + j * 16 + 4 * q4;
-        if (gn < p.n) dg::store_out<BF16_OUT, HAS_C>(p, (int64_t)gm * p.ldc, gn, drow, acc[i][j]);
-      }
-    }
+    asm volatile("" ::: "memory");  // every store precedes the next unit's first wait
+    dg::debug_fence();
+    u = nx;
   }
+  dg::wait_vmcnt<0>();  // no direct load into this workgroup's LDS outlives it
 }
 
 }  // namespace fp4
@@ -175,29 +385,66 @@ __global__ void __launch_bounds__(WM * WN * 64) gemm_kernel(const Params pp) {
 inline bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 inline int cdiv(int a, int b) { return (a + b - 1) / b; }
 
+// Tile configurations, all on two slab stages: 256-row tiles on 8 waves, one workgroup per CU (136, 127 and 119 KiB of LDS
+// at 256, 224 and 192 columns), and 128 x 128 on 4 waves, two per CU (68 KiB).
+struct Cfg {
+  int bm, bn, per_cu, threads;
+};
+constexpr Cfg kCfg256{256, 256, 1, 512}, kCfg224{256, 224, 1, 512}, kCfg192{256, 192, 1, 512}, kCfg128{128, 128, 2, 256};
+
+using Kernel = void (*)(fp4::Params);
+
+template <int BM, int BN, int WM, int WN, int MODE>
+Kernel pick_out(bool bf16, bool has_c) {
+  if constexpr (MODE == dg::MODE_DENSE) {
+    if (has_c) return bf16 ? fp4::gemm_kernel<BM, BN, WM, WN, MODE, true, true> : fp4::gemm_kernel<BM, BN, WM, WN, MODE, false, true>;
+  }
+  return bf16 ? fp4::gemm_kernel<BM, BN, WM, WN, MODE, true, false> : fp4::gemm_kernel<BM, BN, WM, WN, MODE, false, false>;
+}
 template <int MODE>
-dg_status launch(fp4::Params& pp, dg_dtype t, int groups_for_tiles, hipStream_t stream) {
+Kernel pick(const Cfg& c, bool bf16, bool has_c) {
+  if (c.bm == 128) return pick_out<128, 128, 2, 2, MODE>(bf16, has_c);
+  if (c.bn == 224) return pick_out<256, 224, 4, 2, MODE>(bf16, has_c);
+  if (c.bn == 192) return pick_out<256, 192, 4, 2, MODE>(bf16, has_c);
+  return pick_out<256, 256, 2, 4, MODE>(bf16, has_c);
+}
+
+// Time of a call's rounds of tiles, in units of a 256-column tile: a narrower one costs a little more per column
+// (more LDS reads for each product), and a 128 x 128 tile, two of which share a CU, as much as half of a wide one.
+double rounds_cost(const Cfg& c, int64_t row_tiles, int n, int cus) {
+  const int64_t tiles = row_tiles * cdiv(n, c.bn), slots = static_cast<int64_t>(cus) * c.per_cu;
+  const double per_tile = c.bm == 128 ? 0.62 : c.bn / 256.0 * (c.bn == 256 ? 1.0 : (c.bn == 224 ? 1.04 : 1.06));
+  return static_cast<double>((tiles + slots - 1) / slots) * per_tile;
+}
+Cfg choose(int64_t groups, int rows, int n, int cus) {
+  const Cfg cands[4] = {kCfg256, kCfg224, kCfg192, kCfg128};
+  Cfg best = kCfg256;
+  double least = 1e300;
+  for (const Cfg& c : cands) {
+    const double cost = rounds_cost(c, groups * cdiv(rows, c.bm), n, cus);
+    if (cost < least - 1e-9) least = cost, best = c;
+  }
+  return best;
+}
+
+template <int MODE>
+dg_status launch(fp4::Params& pp, const Cfg& cfg, dg_dtype t, int groups_for_tiles, int cus, hipStream_t stream) {
   dg::Params& p = pp.g;
-  constexpr int BM = 128, BN = 128;
-  p.tiles_m = cdiv(p.m, BM);
-  p.tiles_n = cdiv(p.n, BN);
+  p.tiles_m = cdiv(p.m, cfg.bm);
+  p.tiles_n = cdiv(p.n, cfg.bn);
   const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n * groups_for_tiles;
   if (tiles > 0x7fffffff) return DG_ERROR_NOT_SUPPORTED;
   p.num_tiles = static_cast<int>(tiles);
-  const int slots = 2 * dg_get_num_cus();
+  const int slots = cus * cfg.per_cu;
   const int grid = p.num_tiles < slots ? p.num_tiles : slots;
-  void (*fn)(fp4::Params);
-  if constexpr (MODE == dg::MODE_DENSE) {
-    if (p.c != nullptr)
-      fn = t == DG_DTYPE_BF16 ? fp4::gemm_kernel<BM, BN, 2, 2, MODE, true, true> : fp4::gemm_kernel<BM, BN, 2, 2, MODE, false, true>;
-    else
-      fn = t == DG_DTYPE_BF16 ? fp4::gemm_kernel<BM, BN, 2, 2, MODE, true, false> : fp4::gemm_kernel<BM, BN, 2, 2, MODE, false, false>;
-  } else {
-    fn = t == DG_DTYPE_BF16 ? fp4::gemm_kernel<BM, BN, 2, 2, MODE, true, false> : fp4::gemm_kernel<BM, BN, 2, 2, MODE, false, false>;
-  }
-  hipLaunchKernelGGL(fn, dim3(grid), dim3(256), 0, stream, pp);
+  hipLaunchKernelGGL(pick<MODE>(cfg, t == DG_DTYPE_BF16, p.c != nullptr), dim3(grid), dim3(cfg.threads), 0, stream, pp);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? DG_SUCCESS : dg::record_hip_error(e);
+}
+
+inline int usable_cus() {
+  const int c = dg_get_num_cus();
+  return c > 0 ? c : 256;
 }
 
 // Operand checks shared by the entry points; rows = rows of A (M, M_total or M_max).
@@ -213,7 +460,9 @@ dg_status check(const void* a, int64_t lda, const void* sfa, int64_t ld_sfa, con
     if (!aligned(a, 16) || !aligned(b, 16) || !aligned(sfa, 16) || !aligned(sfb, 16)) return DG_ERROR_INVALID_VALUE;
     if (lda < k / 2 || ldb < k / 2 || lda % 16 != 0 || ldb % 16 != 0) return DG_ERROR_INVALID_VALUE;
     if (ld_sfa < rows || ld_sfa % 4 != 0 || ld_sfb < n || ld_sfb % 4 != 0) return DG_ERROR_INVALID_VALUE;
+    // offsets within a tile's rows, and among a group's scales, stay below 2^31
     if (lda * 256 >= (1ll << 31) || ldb * 256 >= (1ll << 31)) return DG_ERROR_NOT_SUPPORTED;
+    if (k / 128 * 4 * ld_sfa >= (1ll << 31) || k / 128 * 4 * ld_sfb >= (1ll << 31)) return DG_ERROR_NOT_SUPPORTED;
   }
   return DG_SUCCESS;
 }
@@ -265,7 +514,8 @@ dg_status dg_mxfp4_gemm_nt(const void* a, int64_t lda, const int32_t* sfa, int64
   fp4::Params pp = params(a, lda, sfa, ld_sfa, b, ldb, sfb, ld_sfb, d, ldd, m, n, k);
   pp.g.c = c;
   pp.g.ldc = ldc;
-  return launch<dg::MODE_DENSE>(pp, d_dtype, 1, stream);
+  const int cus = usable_cus();
+  return launch<dg::MODE_DENSE>(pp, choose(1, m, n, cus), d_dtype, 1, cus, stream);
 }
 
 dg_status dg_m_grouped_mxfp4_gemm_nt_contiguous(const void* a, const int32_t* sfa, int64_t ld_sfa, const void* b,
@@ -283,14 +533,14 @@ dg_status dg_m_grouped_mxfp4_gemm_nt_contiguous(const void* a, const int32_t* sf
   pp.g.num_groups = num_groups;
   pp.g.b_gs = static_cast<int64_t>(n) * (k / 2);
   pp.g.sfb_gs = pp.kw * ld_sfb;
-  return launch<dg::MODE_CONTIG>(pp, d_dtype, 1, stream);
+  const int cus = usable_cus();
+  return launch<dg::MODE_CONTIG>(pp, choose(1, m_total, n, cus), d_dtype, 1, cus, stream);
 }
 
 dg_status dg_m_grouped_mxfp4_gemm_nt_masked(const void* a, const int32_t* sfa, int64_t ld_sfa, const void* b,
                                             const int32_t* sfb, int64_t ld_sfb, void* d, dg_dtype d_dtype,
                                             const int32_t* masked_m, int num_groups, int m_max, int n, int k,
                                             int expected_m, hipStream_t stream) {
-  (void)expected_m;
   if (num_groups < 0) return DG_ERROR_INVALID_VALUE;
   const dg_status st = check(a, k / 2, sfa, ld_sfa, b, k / 2, sfb, ld_sfb, d, n, d_dtype, m_max, n, k);
   if (st != DG_SUCCESS) return st;
@@ -304,7 +554,9 @@ dg_status dg_m_grouped_mxfp4_gemm_nt_masked(const void* a, const int32_t* sfa, i
   pp.g.b_gs = static_cast<int64_t>(n) * (k / 2);
   pp.g.sfb_gs = pp.kw * ld_sfb;
   pp.g.d_gs = static_cast<int64_t>(m_max) * n;
-  return launch<dg::MODE_MASKED>(pp, d_dtype, num_groups, stream);
+  const int cus = usable_cus();
+  const int rows = expected_m > 0 && expected_m < m_max ? expected_m : m_max;
+  return launch<dg::MODE_MASKED>(pp, choose(num_groups, rows, n, cus), d_dtype, num_groups, cus, stream);
 }
 
 }  // extern "C"
