@@ -17,6 +17,7 @@
 //   * B is the product's first operand, so a lane's four results are four consecutive columns.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "dg.h"
@@ -380,64 +381,349 @@ __global__ void __launch_bounds__(WM * WN * 64) gemm_kernel(const Params pp) {
   dg::wait_vmcnt<0>();  // no direct load into this workgroup's LDS outlives it
 }
 
+// For calls that wait for memory rather than for the matrix cores: few rows, so that the reading of B is the work, or few
+// tiles.  BM x 128 tiles (BM = 32, 64 or 128) on four waves of BM x 32, a ring of STAGES slabs in all of a CU's LDS and
+// counted waits, so that STAGES - 1 slabs are always on their way (the 256-row tile waits for the slab it has just asked
+// for unless its products take as long as a memory access: 8 rows of 16 experts of 4096 x 7168 took 77 us with it).  Dense
+// calls split K over workgroups: each writes its FP32 partial tile to the workspace and counts itself; the one that
+// completes a tile adds the partials in the order of the splits, so the result does not depend on who comes last.
+template <int BM, int STAGES, int MODE, bool BF16_OUT, bool HAS_C>
+__global__ void __launch_bounds__(256) stream_kernel(const Params pp) {
+  const dg::Params& p = pp.g;
+  constexpr int BN = 128, NW = 4, TN = BN / NW, FM = BM / 16, FN = TN / 16;
+  constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
+  constexpr int SA_OFF = A_BYTES + B_BYTES, SB_OFF = SA_OFF + 2 * BM * 4;
+  constexpr int STAGE = (SB_OFF + 2 * BN * 4 + 255) / 256 * 256;
+  constexpr int A_LOADS = BM / 8 / NW, B_LOADS = BN / 8 / NW, LOADS = A_LOADS + B_LOADS + 1;  // and one of scales
+  static_assert(A_LOADS * NW * 8 == BM, "the same loads on each wave");
+  static_assert((STAGES - 2) * LOADS < 64, "counted waits");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[STAGES * STAGE];
+  __shared__ int s_last;
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r16 = lane & 15, q4 = lane >> 4, ld_row = lane >> 3;
+  const int all_slabs = (pp.kw + 1) >> 1;
+  const int tiles_mn = p.tiles_m * p.tiles_n;
+  const int f = ((r16 >> 1) & 1) | ((r16 >> 3) << 2);
+  const int ch0 = ((2 * q4) ^ f) << 4, ch1 = ((2 * q4 + 1) ^ f) << 4;
+  const __attribute__((address_space(4))) int32_t* grp_s = (const __attribute__((address_space(4))) int32_t*)p.grp;
+
+  constexpr uint32_t kPast = 0x80000000u;  // from here on every descriptor reads zero
+  const uint32_t ld_s = (uint32_t)(wave < 2 ? p.ld_sfa : pp.ld_sfb) * 4;
+  const int chunk0 = (lane & 7) ^ ((ld_row >> 1) & 1);
+  const uint32_t a_off = (uint32_t)(ld_row * p.lda) + chunk0 * 16, b_off = (uint32_t)(ld_row * p.ldb) + chunk0 * 16;
+  const uint32_t a_blk = (uint32_t)(8 * p.lda), b_blk = (uint32_t)(8 * p.ldb);
+  const uint32_t odd_flip = chunk0 >= 4 ? (uint32_t)-64 : 64u;
+
+  struct Unit {
+    int tile, g, m0, n0, row_end, begin, end, split, tmn;  // tile < 0: no unit
+  };
+  auto find_unit = [&](int tile) {
+    Unit u;
+    u.tile = -1;
+    for (; tile < p.num_tiles; tile += gridDim.x) {
+      int g = 0, t = tile, split = 0;
+      if (MODE == dg::MODE_MASKED) g = t / tiles_mn, t -= g * tiles_mn;
+      if (MODE == dg::MODE_DENSE) split = t / tiles_mn, t -= split * tiles_mn;
+      int mb, nb;
+      dg::raster<4>(t, p.tiles_m, p.tiles_n, mb, nb);
+      u.m0 = mb * BM;
+      u.row_end = p.m;
+      if (MODE == dg::MODE_MASKED) {
+        u.row_end = min(max(grp_s[g], 0), p.m);
+        if (u.m0 >= u.row_end) continue;
+      }
+      u.tile = tile;
+      u.g = g;
+      u.n0 = nb * BN;
+      u.begin = split * p.slabs_per_split;
+      u.end = min(all_slabs, u.begin + p.slabs_per_split);
+      u.split = split;
+      u.tmn = t;
+      break;
+    }
+    return u;
+  };
+  struct Src {
+    __amdgpu_buffer_rsrc_t ra, rb, rs;
+  };
+  auto src_of = [&](const Unit& u) {
+    Src r;
+    const int a_rows = min(u.row_end - u.m0, BM), b_rows = min(p.n - u.n0, BN);
+    r.ra = dg::make_rsrc(p.a + (MODE == dg::MODE_MASKED ? u.g * p.a_gs : 0) + (int64_t)u.m0 * p.lda, (uint32_t)(a_rows * p.lda));
+    r.rb = dg::make_rsrc(p.b + (MODE != dg::MODE_DENSE ? u.g * p.b_gs : 0) + (int64_t)u.n0 * p.ldb, (uint32_t)(b_rows * p.ldb));
+    const float* s = wave < 2 ? p.sfa + (MODE == dg::MODE_MASKED ? u.g * p.sfa_gs : 0) + u.m0
+                              : p.sfb + (MODE != dg::MODE_DENSE ? u.g * p.sfb_gs : 0) + u.n0;
+    r.rs = dg::make_rsrc(s, (uint32_t)(pp.kw - 1) * ld_s + 4u * (wave < 2 ? a_rows : b_rows));
+    return r;
+  };
+  auto load16 = [&](__amdgpu_buffer_rsrc_t r, uint8_t* to, uint32_t off, int blk, uint32_t blk_bytes, int slab, bool live) {
+    const bool odd = blk & 1;
+    uint32_t at = live ? (uint32_t)blk * blk_bytes + (uint32_t)slab * 128 : kPast;
+    asm volatile("" : "+s"(at));
+    uint32_t v = (odd ? off + odd_flip : off) + at;
+    if (2 * slab + 2 > pp.kw && ((chunk0 >= 4) != odd)) v = kPast;
+    dg::load_to_lds<16, true>(r, to, v);
+  };
+  // Slab number `slab` of K into its stage; one that is not live is loaded from offsets that read zero.
+  auto issue = [&](const Src& r, int slab, int stage, bool live) {
+    uint8_t* base = lds + stage * STAGE;
+#pragma unroll
+    for (int i = 0; i < B_LOADS; ++i) {
+      const int blk = wave * B_LOADS + i;
+      load16(r.rb, base + A_BYTES + blk * 1024, b_off, blk, b_blk, slab, live);
+    }
+#pragma unroll
+    for (int i = 0; i < A_LOADS; ++i) {
+      const int blk = wave * A_LOADS + i;
+      load16(r.ra, base + blk * 1024, a_off, blk, a_blk, slab, live);
+    }
+    const int w = 2 * slab + (wave & 1), len = wave < 2 ? BM : BN;
+    if (lane < len / 4)
+      dg::load_to_lds<16, true>(r.rs, base + (wave < 2 ? SA_OFF : SB_OFF) + (wave & 1) * len * 4,
+                                (live && w < pp.kw ? (uint32_t)w * ld_s : kPast) + lane * 16);
+  };
+
+  const uint8_t* As0 = lds + r16 * 128;
+  const uint8_t* Bs0 = lds + A_BYTES + (wave * TN + r16) * 128;
+  const uint8_t* Sa0 = lds + SA_OFF + (q4 >> 1) * BM * 4 + r16 * 4 + (q4 & 1) * 2;
+  const uint8_t* Sb0 = lds + SB_OFF + (q4 >> 1) * BN * 4 + (wave * TN + r16) * 4 + (q4 & 1) * 2;
+  auto read_frag = [&](const uint8_t* rows, const uint8_t* scales, int i) {
+    Frag r;
+    r.lo = *reinterpret_cast<const i32x4*>(rows + i * 2048 + ch0);
+    r.hi = *reinterpret_cast<const i32x4*>(rows + i * 2048 + ch1);
+    r.s = *reinterpret_cast<const uint16_t*>(scales + i * 64);
+    return r;
+  };
+
+  Unit u = find_unit(dg::xcd_remap(blockIdx.x, gridDim.x)), nx;
+  bool pre = false;
+  while (u.tile >= 0) {
+    const int g = u.g, m0 = u.m0, n0 = u.n0, row_end = u.row_end, slabs = u.end - u.begin;
+    const Src sr = src_of(u);
+    const int live_fm = min(FM, (row_end - m0 + 15) >> 4);  // fragments with rows
+    f32x4 acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (!pre) {
+#pragma unroll
+      for (int i = 0; i < STAGES - 1; ++i) issue(sr, u.begin + i, i, i < slabs);
+    }
+    int stage = 0, fill = STAGES - 1;
+    for (int it = 0; it < slabs; ++it) {
+      // this wave's part of slab it has landed (with stores in between, all of what is on its way)
+      if (pre && it == 0) dg::wait_vmcnt<0>();
+      else dg::wait_vmcnt<(STAGES - 2) * LOADS>();
+      dg::stage_barrier();  // everybody's; and slab it - 1 has been read, so its stage is free
+      issue(sr, u.begin + it + STAGES - 1, fill, it + STAGES - 1 < slabs);
+      const int at = stage * STAGE;
+      Frag b[FN];
+#pragma unroll
+      for (int j = 0; j < FN; ++j) b[j] = read_frag(Bs0 + at, Sb0 + at, j);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        if (i >= live_fm) break;
+        const Frag a = read_frag(As0 + at, Sa0 + at, i);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = mfma<0>(b[j].lo, a.lo, acc[i][j], b[j].s, a.s);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = mfma<1>(b[j].hi, a.hi, acc[i][j], b[j].s, a.s);
+      }
+      stage = stage + 1 == STAGES ? 0 : stage + 1;
+      fill = fill + 1 == STAGES ? 0 : fill + 1;
+      dg::debug_fence();
+    }
+    dg::stage_barrier();  // all LDS reads of this unit are done before the next unit's loads
+    nx = find_unit(u.tile + (int)gridDim.x);
+    pre = nx.tile >= 0;
+    if (pre) {
+      dg::wait_vmcnt<0>();  // (the last slabs' empty loads write to the stages too)
+      const Src ns = src_of(nx);
+#pragma unroll
+      for (int i = 0; i < STAGES - 1; ++i) issue(ns, nx.begin + i, i, i < nx.end - nx.begin);
+    }
+
+    bool finish = true;
+    if (MODE == dg::MODE_DENSE && p.splits > 1) {
+      // Partials go through device-scope accesses (sc1), so that workgroups on different XCDs may share a tile; one is
+      // complete once its stores have been acknowledged.
+      constexpr int SC1 = 16;
+      constexpr int64_t TILE = (int64_t)BM * BN;
+      const uint32_t loff = (uint32_t)(wave * FM * FN * 64 + lane) * 16;
+      auto part = [&](int s) { return dg::make_rsrc(p.ws + ((int64_t)s * tiles_mn + u.tmn) * TILE, (uint32_t)(TILE * 4)); };
+      {
+        const auto rw = part(u.split);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(i32x4, acc[i][j]), rw, loff + (i * FN + j) * 1024, 0, SC1);
+      }
+      dg::wait_vmcnt<0>();
+      __syncthreads();
+      if (tid == 0) {
+        const uint32_t arrived = __hip_atomic_fetch_add(p.ctr + u.tmn, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u;
+        const int last = arrived >= (uint32_t)p.splits;
+        if (last) __hip_atomic_store(p.ctr + u.tmn, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        s_last = last;
+      }
+      __syncthreads();
+      finish = s_last != 0;
+      if (finish) {
+        constexpr int RD = BM == 32 ? 8 : (BM == 64 ? 4 : 2);  // partials in flight
+        f32x4 buf[RD][FM][FN];
+        for (int s0 = 0; s0 < p.splits; s0 += RD) {
+#pragma unroll
+          for (int r = 0; r < RD; ++r) {
+            const auto rs = s0 + r < p.splits ? part(s0 + r) : dg::make_rsrc(p.ws, 0u);
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+              for (int j = 0; j < FN; ++j)
+                buf[r][i][j] = __builtin_bit_cast(
+                    f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, loff + (i * FN + j) * 1024, 0, SC1));
+          }
+#pragma unroll
+          for (int r = 0; r < RD; ++r)
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+#pragma unroll
+              for (int j = 0; j < FN; ++j)  // (partials past the last are zeros)
+                acc[i][j] = s0 + r == 0 ? buf[r][i][j] : acc[i][j] + buf[r][i][j];
+        }
+      }
+    }
+    if (finish) {
+      int row0 = m0 + r16;
+      asm volatile("" : "+v"(row0));
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        const int gm = row0 + i * 16;
+        if (gm >= row_end) continue;
+        const int64_t drow = (MODE == dg::MODE_MASKED ? g * p.d_gs : 0) + (int64_t)gm * p.ldd;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          const int gn = n0 + wave * TN + j * 16 + 4 * q4;
+          if (gn < p.n) dg::store_out<BF16_OUT, HAS_C>(p, (int64_t)gm * p.ldc, gn, drow, acc[i][j]);
+        }
+      }
+    }
+    asm volatile("" ::: "memory");
+    dg::debug_fence();
+    u = nx;
+  }
+  dg::wait_vmcnt<0>();  // no direct load into this workgroup's LDS outlives it
+}
+
 }  // namespace fp4
 
 inline bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 inline int cdiv(int a, int b) { return (a + b - 1) / b; }
 
-// Tile configurations, all on two slab stages: 256-row tiles on 8 waves, one workgroup per CU (136, 127 and 119 KiB of LDS
-// at 256, 224 and 192 columns), and 128 x 128 on 4 waves, two per CU (68 KiB).
+// Tile configurations: 256-row tiles on 8 waves, one workgroup per CU (136, 127 and 119 KiB of LDS at 256, 224 and 192
+// columns), and 128 x 128 on 4 waves, two per CU (68 KiB), on two slab stages; and the streaming tiles, one per CU, on a ring
+// of 7, 6 or 4 (149, 154 and 139 KiB at 32, 64 and 128 rows).
 struct Cfg {
   int bm, bn, per_cu, threads;
+  bool stream;
+  double slab_us;  // of a workgroup (of two sharing a CU): measured on MI355X, operands in the last-level cache
 };
-constexpr Cfg kCfg256{256, 256, 1, 512}, kCfg224{256, 224, 1, 512}, kCfg192{256, 192, 1, 512}, kCfg128{128, 128, 2, 256};
+constexpr Cfg kWide[4] = {{256, 256, 1, 512, false, 1.83}, {256, 224, 1, 512, false, 1.66}, {256, 192, 1, 512, false, 1.46},
+                          {128, 128, 2, 256, false, 1.12}};
+constexpr Cfg kStream[3] = {{32, 128, 1, 256, true, 0.5}, {64, 128, 1, 256, true, 0.6}, {128, 128, 1, 256, true, 0.85}};
 
 using Kernel = void (*)(fp4::Params);
 
 template <int BM, int BN, int WM, int WN, int MODE>
-Kernel pick_out(bool bf16, bool has_c) {
+Kernel pick_wide(bool bf16, bool has_c) {
   if constexpr (MODE == dg::MODE_DENSE) {
     if (has_c) return bf16 ? fp4::gemm_kernel<BM, BN, WM, WN, MODE, true, true> : fp4::gemm_kernel<BM, BN, WM, WN, MODE, false, true>;
   }
   return bf16 ? fp4::gemm_kernel<BM, BN, WM, WN, MODE, true, false> : fp4::gemm_kernel<BM, BN, WM, WN, MODE, false, false>;
 }
+template <int BM, int STAGES, int MODE>
+Kernel pick_stream(bool bf16, bool has_c) {
+  if constexpr (MODE == dg::MODE_DENSE) {
+    if (has_c) return bf16 ? fp4::stream_kernel<BM, STAGES, MODE, true, true> : fp4::stream_kernel<BM, STAGES, MODE, false, true>;
+  }
+  return bf16 ? fp4::stream_kernel<BM, STAGES, MODE, true, false> : fp4::stream_kernel<BM, STAGES, MODE, false, false>;
+}
 template <int MODE>
 Kernel pick(const Cfg& c, bool bf16, bool has_c) {
-  if (c.bm == 128) return pick_out<128, 128, 2, 2, MODE>(bf16, has_c);
-  if (c.bn == 224) return pick_out<256, 224, 4, 2, MODE>(bf16, has_c);
-  if (c.bn == 192) return pick_out<256, 192, 4, 2, MODE>(bf16, has_c);
-  return pick_out<256, 256, 2, 4, MODE>(bf16, has_c);
+  if constexpr (MODE != dg::MODE_CONTIG) {
+    if (c.stream && c.bm == 32) return pick_stream<32, 7, MODE>(bf16, has_c);
+    if (c.stream && c.bm == 64) return pick_stream<64, 6, MODE>(bf16, has_c);
+    if (c.stream) return pick_stream<128, 4, MODE>(bf16, has_c);
+  }
+  if (c.bm == 128) return pick_wide<128, 128, 2, 2, MODE>(bf16, has_c);
+  if (c.bn == 224) return pick_wide<256, 224, 4, 2, MODE>(bf16, has_c);
+  if (c.bn == 192) return pick_wide<256, 192, 4, 2, MODE>(bf16, has_c);
+  return pick_wide<256, 256, 2, 4, MODE>(bf16, has_c);
 }
 
-// Time of a call's rounds of tiles, in units of a 256-column tile: a narrower one costs a little more per column
-// (more LDS reads for each product), and a 128 x 128 tile, two of which share a CU, as much as half of a wide one.
-double rounds_cost(const Cfg& c, int64_t row_tiles, int n, int cus) {
-  const int64_t tiles = row_tiles * cdiv(n, c.bn), slots = static_cast<int64_t>(cus) * c.per_cu;
-  const double per_tile = c.bm == 128 ? 0.62 : c.bn / 256.0 * (c.bn == 256 ? 1.0 : (c.bn == 224 ? 1.04 : 1.06));
-  return static_cast<double>((tiles + slots - 1) / slots) * per_tile;
-}
-Cfg choose(int64_t groups, int rows, int n, int cus) {
-  const Cfg cands[4] = {kCfg256, kCfg224, kCfg192, kCfg128};
-  Cfg best = kCfg256;
+// Split-K workspace of a dense call: counters (zero between calls) at a fixed place, then the partial tiles.
+constexpr int kCtrWords = 16384;
+constexpr size_t kCtrBytes = kCtrWords * sizeof(uint32_t);
+constexpr size_t kMaxPartialBytes = size_t(32) << 20;
+
+struct Plan {
+  Cfg cfg;
+  int splits, slabs_per_split;
+  size_t ws_bytes;  // 0: no split
+};
+
+// The configuration (and, for a dense call, the K split) with the least estimated time, in microseconds.  A workgroup takes
+// about 3 us to its first slab, then one slab_us per slab; units beyond one per slot wait for a round.  A split adds 2 us to
+// publish a partial and count it, and the last workgroup's reading of a tile's partials at 85 GB/s.  Whatever the
+// configuration, the calls' bytes come at 6 TB/s at most (with the partials, written and read).
+Plan plan(int mode, int64_t groups, int rows, int n, int k, int cus) {
+  const int slabs = (k / 128 + 1) / 2;
+  const double bytes = (static_cast<double>(groups) * n + (mode == dg::MODE_MASKED ? groups * static_cast<double>(rows) : rows)) *
+                       k * 0.53;
+  Plan best{kWide[0], 1, slabs, 0};
   double least = 1e300;
-  for (const Cfg& c : cands) {
-    const double cost = rounds_cost(c, groups * cdiv(rows, c.bm), n, cus);
-    if (cost < least - 1e-9) least = cost, best = c;
+  auto consider = [&](const Cfg& c, int64_t tiles, int s) {
+    const int sps = cdiv(slabs, s);
+    const int64_t slots = static_cast<int64_t>(cus) * c.per_cu, rounds = (tiles * s + slots - 1) / slots;
+    const double part = s > 1 ? static_cast<double>(s) * tiles * c.bm * c.bn * 4 : 0;
+    const double us = std::max(rounds * (3.0 + sps * c.slab_us), (bytes + 2 * part) / 6e6) +
+                      (s > 1 ? 2.0 + s * (c.bm * c.bn * 4 / 85e3) : 0.0);
+    if (us < least - 1e-9) {
+      least = us;
+      best = Plan{c, s, sps, s > 1 ? kCtrBytes + static_cast<size_t>(part) : 0};
+    }
+  };
+  for (const Cfg& c : kWide) consider(c, groups * cdiv(rows, c.bm) * cdiv(n, c.bn), 1);
+  if (mode == dg::MODE_CONTIG || k == 0) return best;
+  for (const Cfg& c : kStream) {
+    const int64_t tiles = groups * cdiv(rows, c.bm) * cdiv(n, c.bn);
+    consider(c, tiles, 1);
+    if (mode != dg::MODE_DENSE || tiles > kCtrWords) continue;
+    for (int s = 2; s <= slabs && tiles * s <= 2ll * cus; ++s) {
+      if (cdiv(slabs, cdiv(slabs, s)) != s) continue;  // each split once, as its slabs per split
+      if (static_cast<size_t>(s) * tiles * c.bm * c.bn * 4 > kMaxPartialBytes) break;
+      consider(c, tiles, s);
+    }
   }
   return best;
 }
 
 template <int MODE>
-dg_status launch(fp4::Params& pp, const Cfg& cfg, dg_dtype t, int groups_for_tiles, int cus, hipStream_t stream) {
+dg_status launch(fp4::Params& pp, const Plan& pl, dg_dtype t, int groups_for_tiles, int cus, hipStream_t stream) {
   dg::Params& p = pp.g;
-  p.tiles_m = cdiv(p.m, cfg.bm);
-  p.tiles_n = cdiv(p.n, cfg.bn);
-  const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n * groups_for_tiles;
+  p.tiles_m = cdiv(p.m, pl.cfg.bm);
+  p.tiles_n = cdiv(p.n, pl.cfg.bn);
+  p.splits = pl.splits;
+  p.slabs_per_split = pl.slabs_per_split;
+  const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n * groups_for_tiles * pl.splits;
   if (tiles > 0x7fffffff) return DG_ERROR_NOT_SUPPORTED;
   p.num_tiles = static_cast<int>(tiles);
-  const int slots = cus * cfg.per_cu;
+  const int slots = cus * pl.cfg.per_cu;
   const int grid = p.num_tiles < slots ? p.num_tiles : slots;
-  hipLaunchKernelGGL(pick<MODE>(cfg, t == DG_DTYPE_BF16, p.c != nullptr), dim3(grid), dim3(cfg.threads), 0, stream, pp);
+  hipLaunchKernelGGL(pick<MODE>(pl.cfg, t == DG_DTYPE_BF16, p.c != nullptr), dim3(grid), dim3(pl.cfg.threads), 0, stream, pp);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? DG_SUCCESS : dg::record_hip_error(e);
 }
@@ -495,18 +781,14 @@ fp4::Params params(const void* a, int64_t lda, const int32_t* sfa, int64_t ld_sf
 extern "C" {
 
 size_t dg_get_mxfp4_workspace_size(int m, int n, int k) {
-  (void)m;
-  (void)n;
-  (void)k;
-  return 0;
+  if (m <= 0 || n <= 0 || k <= 0 || k % 128 != 0) return 0;
+  return plan(dg::MODE_DENSE, 1, m, n, k, usable_cus()).ws_bytes;
 }
 
 dg_status dg_mxfp4_gemm_nt(const void* a, int64_t lda, const int32_t* sfa, int64_t ld_sfa, const void* b, int64_t ldb,
                            const int32_t* sfb, int64_t ld_sfb, const void* c, int64_t ldc, void* d, int64_t ldd,
                            dg_dtype d_dtype, int m, int n, int k, void* workspace, size_t workspace_bytes,
                            hipStream_t stream) {
-  (void)workspace;
-  (void)workspace_bytes;
   const dg_status st = check(a, lda, sfa, ld_sfa, b, ldb, sfb, ld_sfb, d, ldd, d_dtype, m, n, k);
   if (st != DG_SUCCESS || m == 0 || n == 0) return st;
   const int64_t es = d_dtype == DG_DTYPE_BF16 ? 2 : 4;
@@ -515,7 +797,13 @@ dg_status dg_mxfp4_gemm_nt(const void* a, int64_t lda, const int32_t* sfa, int64
   pp.g.c = c;
   pp.g.ldc = ldc;
   const int cus = usable_cus();
-  return launch<dg::MODE_DENSE>(pp, choose(1, m, n, cus), d_dtype, 1, cus, stream);
+  const Plan pl = plan(dg::MODE_DENSE, 1, m, n, k, cus);
+  if (pl.ws_bytes > 0) {
+    if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < pl.ws_bytes) return DG_ERROR_WORKSPACE;
+    pp.g.ctr = static_cast<uint32_t*>(workspace);
+    pp.g.ws = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kCtrBytes);
+  }
+  return launch<dg::MODE_DENSE>(pp, pl, d_dtype, 1, cus, stream);
 }
 
 dg_status dg_m_grouped_mxfp4_gemm_nt_contiguous(const void* a, const int32_t* sfa, int64_t ld_sfa, const void* b,
@@ -534,7 +822,7 @@ dg_status dg_m_grouped_mxfp4_gemm_nt_contiguous(const void* a, const int32_t* sf
   pp.g.b_gs = static_cast<int64_t>(n) * (k / 2);
   pp.g.sfb_gs = pp.kw * ld_sfb;
   const int cus = usable_cus();
-  return launch<dg::MODE_CONTIG>(pp, choose(1, m_total, n, cus), d_dtype, 1, cus, stream);
+  return launch<dg::MODE_CONTIG>(pp, plan(dg::MODE_CONTIG, 1, m_total, n, k, cus), d_dtype, 1, cus, stream);
 }
 
 dg_status dg_m_grouped_mxfp4_gemm_nt_masked(const void* a, const int32_t* sfa, int64_t ld_sfa, const void* b,
@@ -556,7 +844,7 @@ dg_status dg_m_grouped_mxfp4_gemm_nt_masked(const void* a, const int32_t* sfa, i
   pp.g.d_gs = static_cast<int64_t>(m_max) * n;
   const int cus = usable_cus();
   const int rows = expected_m > 0 && expected_m < m_max ? expected_m : m_max;
-  return launch<dg::MODE_MASKED>(pp, choose(num_groups, rows, n, cus), d_dtype, num_groups, cus, stream);
+  return launch<dg::MODE_MASKED>(pp, plan(dg::MODE_MASKED, num_groups, rows, n, k, cus), d_dtype, num_groups, cus, stream);
 }
 
 }  // extern "C"
