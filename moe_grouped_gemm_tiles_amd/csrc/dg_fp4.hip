@@ -18,6 +18,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 
 #include "dg.h"
@@ -382,26 +383,27 @@ __global__ void __launch_bounds__(WM * WN * 64) gemm_kernel(const Params pp) {
 }
 
 // For calls that wait for memory rather than for the matrix cores: few rows, so that the reading of B is the work, or few
-// tiles.  BM x 128 tiles (BM = 32, 64 or 128) on four waves of BM x 32, a ring of STAGES slabs in all of a CU's LDS and
+// tiles.  BM x 128 tiles (BM = 32, 64, 128 or 256) on four or eight waves, a ring of STAGES slabs in all of a CU's LDS and
 // counted waits, so that STAGES - 1 slabs are always on their way (the 256-row tile waits for the slab it has just asked
 // for unless its products take as long as a memory access: 8 rows of 16 experts of 4096 x 7168 took 77 us with it).  Dense
 // calls split K over workgroups: each writes its FP32 partial tile to the workspace and counts itself; the one that
 // completes a tile adds the partials in the order of the splits, so the result does not depend on who comes last.
-template <int BM, int STAGES, int MODE, bool BF16_OUT, bool HAS_C>
-__global__ void __launch_bounds__(256) stream_kernel(const Params pp) {
+template <int BM, int WM, int STAGES, int MODE, bool BF16_OUT, bool HAS_C>
+__global__ void __launch_bounds__(WM * 256) stream_kernel(const Params pp) {
   const dg::Params& p = pp.g;
-  constexpr int BN = 128, NW = 4, TN = BN / NW, FM = BM / 16, FN = TN / 16;
+  constexpr int BN = 128, WN = 4, NW = WM * WN, TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
   constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
   constexpr int SA_OFF = A_BYTES + B_BYTES, SB_OFF = SA_OFF + 2 * BM * 4;
   constexpr int STAGE = (SB_OFF + 2 * BN * 4 + 255) / 256 * 256;
   constexpr int A_LOADS = BM / 8 / NW, B_LOADS = BN / 8 / NW, LOADS = A_LOADS + B_LOADS + 1;  // and one of scales
-  static_assert(A_LOADS * NW * 8 == BM, "the same loads on each wave");
+  static_assert(A_LOADS * NW * 8 == BM && B_LOADS * NW * 8 == BN, "the same loads on each wave");
   static_assert((STAGES - 2) * LOADS < 64, "counted waits");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[STAGES * STAGE];
   __shared__ int s_last;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
   const int r16 = lane & 15, q4 = lane >> 4, ld_row = lane >> 3;
   const int all_slabs = (pp.kw + 1) >> 1;
   const int tiles_mn = p.tiles_m * p.tiles_n;
@@ -410,7 +412,8 @@ __global__ void __launch_bounds__(256) stream_kernel(const Params pp) {
   const __attribute__((address_space(4))) int32_t* grp_s = (const __attribute__((address_space(4))) int32_t*)p.grp;
 
   constexpr uint32_t kPast = 0x80000000u;  // from here on every descriptor reads zero
-  const uint32_t ld_s = (uint32_t)(wave < 2 ? p.ld_sfa : pp.ld_sfb) * 4;
+  const bool a_scales = wn < 2;  // waves wn = 0, 1 load A's two scale rows of a slab, 2 and 3 B's; wm halves a row
+  const uint32_t ld_s = (uint32_t)(a_scales ? p.ld_sfa : pp.ld_sfb) * 4;
   const int chunk0 = (lane & 7) ^ ((ld_row >> 1) & 1);
   const uint32_t a_off = (uint32_t)(ld_row * p.lda) + chunk0 * 16, b_off = (uint32_t)(ld_row * p.ldb) + chunk0 * 16;
   const uint32_t a_blk = (uint32_t)(8 * p.lda), b_blk = (uint32_t)(8 * p.ldb);
@@ -453,9 +456,9 @@ __global__ void __launch_bounds__(256) stream_kernel(const Params pp) {
     const int a_rows = min(u.row_end - u.m0, BM), b_rows = min(p.n - u.n0, BN);
     r.ra = dg::make_rsrc(p.a + (MODE == dg::MODE_MASKED ? u.g * p.a_gs : 0) + (int64_t)u.m0 * p.lda, (uint32_t)(a_rows * p.lda));
     r.rb = dg::make_rsrc(p.b + (MODE != dg::MODE_DENSE ? u.g * p.b_gs : 0) + (int64_t)u.n0 * p.ldb, (uint32_t)(b_rows * p.ldb));
-    const float* s = wave < 2 ? p.sfa + (MODE == dg::MODE_MASKED ? u.g * p.sfa_gs : 0) + u.m0
+    const float* s = a_scales ? p.sfa + (MODE == dg::MODE_MASKED ? u.g * p.sfa_gs : 0) + u.m0
                               : p.sfb + (MODE != dg::MODE_DENSE ? u.g * p.sfb_gs : 0) + u.n0;
-    r.rs = dg::make_rsrc(s, (uint32_t)(pp.kw - 1) * ld_s + 4u * (wave < 2 ? a_rows : b_rows));
+    r.rs = dg::make_rsrc(s, (uint32_t)(pp.kw - 1) * ld_s + 4u * (a_scales ? a_rows : b_rows));
     return r;
   };
   auto load16 = [&](__amdgpu_buffer_rsrc_t r, uint8_t* to, uint32_t off, int blk, uint32_t blk_bytes, int slab, bool live) {
@@ -479,16 +482,16 @@ __global__ void __launch_bounds__(256) stream_kernel(const Params pp) {
       const int blk = wave * A_LOADS + i;
       load16(r.ra, base + blk * 1024, a_off, blk, a_blk, slab, live);
     }
-    const int w = 2 * slab + (wave & 1), len = wave < 2 ? BM : BN;
-    if (lane < len / 4)
-      dg::load_to_lds<16, true>(r.rs, base + (wave < 2 ? SA_OFF : SB_OFF) + (wave & 1) * len * 4,
-                                (live && w < pp.kw ? (uint32_t)w * ld_s : kPast) + lane * 16);
+    const int w = 2 * slab + (wn & 1), len = a_scales ? BM : BN, part = len * 4 / WM;
+    if (lane < part / 16)
+      dg::load_to_lds<16, true>(r.rs, base + (a_scales ? SA_OFF : SB_OFF) + (wn & 1) * len * 4 + wm * part,
+                                (live && w < pp.kw ? (uint32_t)w * ld_s : kPast) + wm * part + lane * 16);
   };
 
-  const uint8_t* As0 = lds + r16 * 128;
-  const uint8_t* Bs0 = lds + A_BYTES + (wave * TN + r16) * 128;
-  const uint8_t* Sa0 = lds + SA_OFF + (q4 >> 1) * BM * 4 + r16 * 4 + (q4 & 1) * 2;
-  const uint8_t* Sb0 = lds + SB_OFF + (q4 >> 1) * BN * 4 + (wave * TN + r16) * 4 + (q4 & 1) * 2;
+  const uint8_t* As0 = lds + (wm * TM + r16) * 128;
+  const uint8_t* Bs0 = lds + A_BYTES + (wn * TN + r16) * 128;
+  const uint8_t* Sa0 = lds + SA_OFF + (q4 >> 1) * BM * 4 + (wm * TM + r16) * 4 + (q4 & 1) * 2;
+  const uint8_t* Sb0 = lds + SB_OFF + (q4 >> 1) * BN * 4 + (wn * TN + r16) * 4 + (q4 & 1) * 2;
   auto read_frag = [&](const uint8_t* rows, const uint8_t* scales, int i) {
     Frag r;
     r.lo = *reinterpret_cast<const i32x4*>(rows + i * 2048 + ch0);
@@ -502,7 +505,6 @@ __global__ void __launch_bounds__(256) stream_kernel(const Params pp) {
   while (u.tile >= 0) {
     const int g = u.g, m0 = u.m0, n0 = u.n0, row_end = u.row_end, slabs = u.end - u.begin;
     const Src sr = src_of(u);
-    const int live_fm = min(FM, (row_end - m0 + 15) >> 4);  // fragments with rows
     f32x4 acc[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
@@ -520,18 +522,21 @@ __global__ void __launch_bounds__(256) stream_kernel(const Params pp) {
       dg::stage_barrier();  // everybody's; and slab it - 1 has been read, so its stage is free
       issue(sr, u.begin + it + STAGES - 1, fill, it + STAGES - 1 < slabs);
       const int at = stage * STAGE;
-      Frag b[FN];
+      // all fragments first, so that their latency passes once a slab (rows that are not there too)
+      Frag a[FM], b[FN];
 #pragma unroll
       for (int j = 0; j < FN; ++j) b[j] = read_frag(Bs0 + at, Sb0 + at, j);
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
-        if (i >= live_fm) break;
-        const Frag a = read_frag(As0 + at, Sa0 + at, i);
+      for (int i = 0; i < FM; ++i) a[i] = read_frag(As0 + at, Sa0 + at, i);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = mfma<0>(b[j].lo, a.lo, acc[i][j], b[j].s, a.s);
+      for (int i = 0; i < FM; ++i)
 #pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = mfma<1>(b[j].hi, a.hi, acc[i][j], b[j].s, a.s);
-      }
+        for (int j = 0; j < FN; ++j) acc[i][j] = mfma<0>(b[j].lo, a[i].lo, acc[i][j], b[j].s, a[i].s);
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = mfma<1>(b[j].hi, a[i].hi, acc[i][j], b[j].s, a[i].s);
       stage = stage + 1 == STAGES ? 0 : stage + 1;
       fill = fill + 1 == STAGES ? 0 : fill + 1;
       dg::debug_fence();
@@ -573,7 +578,7 @@ __global__ void __launch_bounds__(256) stream_kernel(const Params pp) {
       __syncthreads();
       finish = s_last != 0;
       if (finish) {
-        constexpr int RD = BM == 32 ? 8 : (BM == 64 ? 4 : 2);  // partials in flight
+        constexpr int RD = BM == 32 ? 8 : (BM == 64 ? 4 : (BM == 128 ? 2 : 1));  // partials in flight
         f32x4 buf[RD][FM][FN];
         for (int s0 = 0; s0 < p.splits; s0 += RD) {
 #pragma unroll
@@ -597,7 +602,7 @@ __global__ void __launch_bounds__(256) stream_kernel(const Params pp) {
       }
     }
     if (finish) {
-      int row0 = m0 + r16;
+      int row0 = m0 + wm * TM + r16;
       asm volatile("" : "+v"(row0));
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
@@ -606,7 +611,7 @@ __global__ void __launch_bounds__(256) stream_kernel(const Params pp) {
         const int64_t drow = (MODE == dg::MODE_MASKED ? g * p.d_gs : 0) + (int64_t)gm * p.ldd;
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
-          const int gn = n0 + wave * TN + j * 16 + 4 * q4;
+          const int gn = n0 + wn * TN + j * 16 + 4 * q4;
           if (gn < p.n) dg::store_out<BF16_OUT, HAS_C>(p, (int64_t)gm * p.ldc, gn, drow, acc[i][j]);
         }
       }
@@ -625,15 +630,15 @@ inline int cdiv(int a, int b) { return (a + b - 1) / b; }
 
 // Tile configurations: 256-row tiles on 8 waves, one workgroup per CU (136, 127 and 119 KiB of LDS at 256, 224 and 192
 // columns), and 128 x 128 on 4 waves, two per CU (68 KiB), on two slab stages; and the streaming tiles, one per CU, on a ring
-// of 7, 6 or 4 (149, 154 and 139 KiB at 32, 64 and 128 rows).
+// of 7, 6, 4 or 3 (149, 154, 136 and 153 KiB at 32, 64, 128 and 256 rows).
 struct Cfg {
   int bm, bn, per_cu, threads;
-  bool stream;
-  double slab_us;  // of a workgroup (of two sharing a CU): measured on MI355X, operands in the last-level cache
+  double alone_us, full_us;  // per slab with few and with all CUs at work (the clock falls); streaming tiles: 0
 };
-constexpr Cfg kWide[4] = {{256, 256, 1, 512, false, 1.83}, {256, 224, 1, 512, false, 1.66}, {256, 192, 1, 512, false, 1.46},
-                          {128, 128, 2, 256, false, 1.12}};
-constexpr Cfg kStream[3] = {{32, 128, 1, 256, true, 0.5}, {64, 128, 1, 256, true, 0.6}, {128, 128, 1, 256, true, 0.85}};
+constexpr Cfg kWide[4] = {{256, 256, 1, 512, 1.4, 1.9}, {256, 224, 1, 512, 1.35, 1.7}, {256, 192, 1, 512, 1.1, 1.5},
+                          {128, 128, 2, 256, 0.84, 1.25}};
+constexpr Cfg kStream[4] = {{32, 128, 1, 256, 0, 0}, {64, 128, 1, 512, 0, 0}, {128, 128, 1, 512, 0, 0}, {256, 128, 1, 512, 0, 0}};
+inline bool is_stream(const Cfg& c) { return c.full_us == 0; }
 
 using Kernel = void (*)(fp4::Params);
 
@@ -644,19 +649,21 @@ Kernel pick_wide(bool bf16, bool has_c) {
   }
   return bf16 ? fp4::gemm_kernel<BM, BN, WM, WN, MODE, true, false> : fp4::gemm_kernel<BM, BN, WM, WN, MODE, false, false>;
 }
-template <int BM, int STAGES, int MODE>
+template <int BM, int WM, int STAGES, int MODE>
 Kernel pick_stream(bool bf16, bool has_c) {
   if constexpr (MODE == dg::MODE_DENSE) {
-    if (has_c) return bf16 ? fp4::stream_kernel<BM, STAGES, MODE, true, true> : fp4::stream_kernel<BM, STAGES, MODE, false, true>;
+    if (has_c) return bf16 ? fp4::stream_kernel<BM, WM, STAGES, MODE, true, true> : fp4::stream_kernel<BM, WM, STAGES, MODE, false, true>;
   }
-  return bf16 ? fp4::stream_kernel<BM, STAGES, MODE, true, false> : fp4::stream_kernel<BM, STAGES, MODE, false, false>;
+  return bf16 ? fp4::stream_kernel<BM, WM, STAGES, MODE, true, false> : fp4::stream_kernel<BM, WM, STAGES, MODE, false, false>;
 }
 template <int MODE>
 Kernel pick(const Cfg& c, bool bf16, bool has_c) {
   if constexpr (MODE != dg::MODE_CONTIG) {
-    if (c.stream && c.bm == 32) return pick_stream<32, 7, MODE>(bf16, has_c);
-    if (c.stream && c.bm == 64) return pick_stream<64, 6, MODE>(bf16, has_c);
-    if (c.stream) return pick_stream<128, 4, MODE>(bf16, has_c);
+    if (is_stream(c) && c.bm == 32) return pick_stream<32, 1, 7, MODE>(bf16, has_c);
+    if (is_stream(c) && c.bm == 64) return pick_stream<64, 2, 6, MODE>(bf16, has_c);
+    if (is_stream(c) && c.bm == 128) return pick_stream<128, 2, 4, MODE>(bf16, has_c);
+    if constexpr (MODE == dg::MODE_MASKED)
+      if (is_stream(c)) return pick_stream<256, 2, 3, MODE>(bf16, has_c);
   }
   if (c.bm == 128) return pick_wide<128, 128, 2, 2, MODE>(bf16, has_c);
   if (c.bn == 224) return pick_wide<256, 224, 4, 2, MODE>(bf16, has_c);
@@ -675,37 +682,52 @@ struct Plan {
   size_t ws_bytes;  // 0: no split
 };
 
-// The configuration (and, for a dense call, the K split) with the least estimated time, in microseconds.  A workgroup takes
-// about 3 us to its first slab, then one slab_us per slab; units beyond one per slot wait for a round.  A split adds 2 us to
-// publish a partial and count it, and the last workgroup's reading of a tile's partials at 85 GB/s.  Whatever the
-// configuration, the calls' bytes come at 6 TB/s at most (with the partials, written and read).
-Plan plan(int mode, int64_t groups, int rows, int n, int k, int cus) {
+// The configuration (and, for a dense call, the K split) with the least estimated time, in microseconds, fitted to sweeps of
+// 25 shapes on MI355X (within 10 % of the measured time of the best candidates): 4 us from launch to the first slab and for
+// the last stores, 1 us a round of workgroups, the slabs at a rate of the tile's own (streaming tiles: 40 GB/s a CU), and not
+// less than the operands' bytes at 5.5 TB/s.  A split adds 1.2 us to publish and count partials, their bytes at 6 TB/s twice,
+// and the last workgroup's reading of a tile's at 85 GB/s.  rows: of A, or of a group's (masked: the expected number; groups
+// are taken to have up to twice as many, each as likely).
+Plan plan(int mode, int64_t groups, int rows, int most_rows, int n, int k, int cus) {
   const int slabs = (k / 128 + 1) / 2;
-  const double bytes = (static_cast<double>(groups) * n + (mode == dg::MODE_MASKED ? groups * static_cast<double>(rows) : rows)) *
-                       k * 0.53;
+  const bool masked = mode == dg::MODE_MASKED;
+  const double bytes = (static_cast<double>(groups) * n + static_cast<double>(masked ? groups : 1) * rows) * k * 0.53;
   Plan best{kWide[0], 1, slabs, 0};
   double least = 1e300;
-  auto consider = [&](const Cfg& c, int64_t tiles, int s) {
+  // row tiles of a call
+  auto row_tiles = [&](int bm) {
+    if (!masked) return static_cast<double>(cdiv(rows, bm));
+    const double up_to = std::min<double>(2.0 * rows, most_rows);
+    double t = 0;
+    for (int j = 0; j * static_cast<double>(bm) < up_to && j < 4096; ++j) t += 1.0 - j * bm / up_to;
+    return groups * t;
+  };
+  auto consider = [&](const Cfg& c, int s) {
+    const double units = std::ceil(row_tiles(c.bm)) * cdiv(n, c.bn) * s, slots = static_cast<double>(cus) * c.per_cu;
+    const double rounds = std::ceil(units / slots), busy = std::min(1.0, units / cus);
     const int sps = cdiv(slabs, s);
-    const int64_t slots = static_cast<int64_t>(cus) * c.per_cu, rounds = (tiles * s + slots - 1) / slots;
-    const double part = s > 1 ? static_cast<double>(s) * tiles * c.bm * c.bn * 4 : 0;
-    const double us = std::max(rounds * (3.0 + sps * c.slab_us), (bytes + 2 * part) / 6e6) +
-                      (s > 1 ? 2.0 + s * (c.bm * c.bn * 4 / 85e3) : 0.0);
+    double slab_us = is_stream(c) ? (std::min(c.bm, rows) + 128) * 136 / 40e3 : c.alone_us + (c.full_us - c.alone_us) * busy;
+    if (!is_stream(c) && masked && rows <= 256) slab_us += 0.6;  // B from memory, waited for
+    if (c.per_cu == 2 && units <= cus) slab_us = c.alone_us;     // one to a CU
+    const double part = s > 1 ? units * c.bm * c.bn * 4 : 0;
+    const double us = 4.0 + std::max(rounds * (1.0 + sps * slab_us), bytes / 5.5e6) +
+                      (s > 1 ? 1.2 + s * (c.bm * c.bn * 4 / 85e3) + 2 * part / 6e6 : 0.0);
     if (us < least - 1e-9) {
       least = us;
       best = Plan{c, s, sps, s > 1 ? kCtrBytes + static_cast<size_t>(part) : 0};
     }
   };
-  for (const Cfg& c : kWide) consider(c, groups * cdiv(rows, c.bm) * cdiv(n, c.bn), 1);
+  for (const Cfg& c : kWide) consider(c, 1);
   if (mode == dg::MODE_CONTIG || k == 0) return best;
   for (const Cfg& c : kStream) {
-    const int64_t tiles = groups * cdiv(rows, c.bm) * cdiv(n, c.bn);
-    consider(c, tiles, 1);
-    if (mode != dg::MODE_DENSE || tiles > kCtrWords) continue;
+    if (c.bm == 256 && !masked) continue;
+    consider(c, 1);
+    const int64_t tiles = static_cast<int64_t>(cdiv(rows, c.bm)) * cdiv(n, c.bn);
+    if (masked || tiles > kCtrWords) continue;
     for (int s = 2; s <= slabs && tiles * s <= 2ll * cus; ++s) {
       if (cdiv(slabs, cdiv(slabs, s)) != s) continue;  // each split once, as its slabs per split
       if (static_cast<size_t>(s) * tiles * c.bm * c.bn * 4 > kMaxPartialBytes) break;
-      consider(c, tiles, s);
+      consider(c, s);
     }
   }
   return best;
@@ -782,7 +804,7 @@ extern "C" {
 
 size_t dg_get_mxfp4_workspace_size(int m, int n, int k) {
   if (m <= 0 || n <= 0 || k <= 0 || k % 128 != 0) return 0;
-  return plan(dg::MODE_DENSE, 1, m, n, k, usable_cus()).ws_bytes;
+  return plan(dg::MODE_DENSE, 1, m, m, n, k, usable_cus()).ws_bytes;
 }
 
 dg_status dg_mxfp4_gemm_nt(const void* a, int64_t lda, const int32_t* sfa, int64_t ld_sfa, const void* b, int64_t ldb,
@@ -797,7 +819,7 @@ dg_status dg_mxfp4_gemm_nt(const void* a, int64_t lda, const int32_t* sfa, int64
   pp.g.c = c;
   pp.g.ldc = ldc;
   const int cus = usable_cus();
-  const Plan pl = plan(dg::MODE_DENSE, 1, m, n, k, cus);
+  const Plan pl = plan(dg::MODE_DENSE, 1, m, m, n, k, cus);
   if (pl.ws_bytes > 0) {
     if (workspace == nullptr || !aligned(workspace, 256) || workspace_bytes < pl.ws_bytes) return DG_ERROR_WORKSPACE;
     pp.g.ctr = static_cast<uint32_t*>(workspace);
@@ -822,7 +844,7 @@ dg_status dg_m_grouped_mxfp4_gemm_nt_contiguous(const void* a, const int32_t* sf
   pp.g.b_gs = static_cast<int64_t>(n) * (k / 2);
   pp.g.sfb_gs = pp.kw * ld_sfb;
   const int cus = usable_cus();
-  return launch<dg::MODE_CONTIG>(pp, plan(dg::MODE_CONTIG, 1, m_total, n, k, cus), d_dtype, 1, cus, stream);
+  return launch<dg::MODE_CONTIG>(pp, plan(dg::MODE_CONTIG, 1, m_total, m_total, n, k, cus), d_dtype, 1, cus, stream);
 }
 
 dg_status dg_m_grouped_mxfp4_gemm_nt_masked(const void* a, const int32_t* sfa, int64_t ld_sfa, const void* b,
@@ -843,8 +865,8 @@ dg_status dg_m_grouped_mxfp4_gemm_nt_masked(const void* a, const int32_t* sfa, i
   pp.g.sfb_gs = pp.kw * ld_sfb;
   pp.g.d_gs = static_cast<int64_t>(m_max) * n;
   const int cus = usable_cus();
-  const int rows = expected_m > 0 && expected_m < m_max ? expected_m : m_max;
-  return launch<dg::MODE_MASKED>(pp, plan(dg::MODE_MASKED, num_groups, rows, n, k, cus), d_dtype, num_groups, cus, stream);
+  const int rows = expected_m > 0 && expected_m < m_max ? expected_m : (m_max + 1) / 2;
+  return launch<dg::MODE_MASKED>(pp, plan(dg::MODE_MASKED, num_groups, rows, m_max, n, k, cus), d_dtype, num_groups, cus, stream);
 }
 
 }  // extern "C"
