@@ -54,6 +54,66 @@ struct Frag {
   int s;
 };
 
+// Masked groups: the tiles that have rows, numbered through, so that they spread evenly over the workgroups whatever the
+// groups' row counts are (numbering all tiles instead leaves the rows that are there to the same few workgroups: 8 rows of 16
+// groups in 32-row tiles took 228 us, numbered through 55).  first[i] = the row tiles of the groups before i * per.
+constexpr int kGroupSlots = 1024;
+struct LiveTiles {
+  int first[kGroupSlots + 1];
+  int wave_total[8];
+};
+template <int BM, int NW>
+__device__ __forceinline__ void number_live_tiles(LiveTiles& t, const dg::Params& p) {
+  constexpr int MINE = kGroupSlots / (NW * 64);
+  const int per = (p.num_groups + kGroupSlots - 1) / kGroupSlots;
+  const int tid = threadIdx.x, lane = tid & 63;
+  int n[MINE], sum = 0;
+#pragma unroll
+  for (int i = 0; i < MINE; ++i) {
+    const int at = (tid * MINE + i) * per;
+    n[i] = 0;
+    for (int g = at; g < min(at + per, p.num_groups); ++g) n[i] += (min(max(p.grp[g], 0), p.m) + BM - 1) / BM;
+    sum += n[i];
+  }
+  int upto = sum;  // of the wave's lanes up to this one
+  for (int o = 1; o < 64; o <<= 1) {
+    const int v = __shfl_up(upto, o);
+    if (lane >= o) upto += v;
+  }
+  if (lane == 63) t.wave_total[tid >> 6] = upto;
+  __syncthreads();
+  int before = upto - sum;
+  for (int w = 0; w < (tid >> 6); ++w) before += t.wave_total[w];
+#pragma unroll
+  for (int i = 0; i < MINE; ++i) {
+    t.first[tid * MINE + i] = before;
+    before += n[i];
+  }
+  if (tid == NW * 64 - 1) t.first[kGroupSlots] = before;
+  __syncthreads();
+}
+// The group of live tile `id` (of tiles_n for each row tile), its number within the group and the group's row tiles; false
+// past the last one.
+template <int BM>
+__device__ __forceinline__ bool live_tile(const LiveTiles& t, const dg::Params& p, int id, int& g, int& local, int& tiles_m) {
+  const __attribute__((address_space(4))) int32_t* grp = (const __attribute__((address_space(4))) int32_t*)p.grp;
+  const int per = (p.num_groups + kGroupSlots - 1) / kGroupSlots;
+  const int row_tile = id / p.tiles_n;
+  if (row_tile >= __builtin_amdgcn_readfirstlane(t.first[kGroupSlots])) return false;
+  int at = 0;  // the last slot that starts at or before row_tile (of empty ones the last: it is the one with rows)
+  for (int step = kGroupSlots / 2; step >= 1; step >>= 1)
+    if (__builtin_amdgcn_readfirstlane(t.first[at + step]) <= row_tile) at += step;
+  int before = __builtin_amdgcn_readfirstlane(t.first[at]);
+  for (g = at * per;; ++g) {
+    if (g >= p.num_groups) return false;
+    tiles_m = (min(max(grp[g], 0), p.m) + BM - 1) / BM;
+    if (row_tile < before + tiles_m) break;
+    before += tiles_m;
+  }
+  local = id - before * p.tiles_n;
+  return true;
+}
+
 // One persistent kernel for every entry point.  The schedule of a slab is the FP8 GEMM's: the operand with fewer fragments
 // per wave ("outer") stays in registers for the slab, the other ("inner") is streamed from LDS; the last HOLD inner fragments
 // are held back, so that after the slab's one barrier, placed between part 1 and part 2, the matrix cores run from registers
@@ -87,12 +147,15 @@ __global__ void __launch_bounds__(WM * WN * 64) gemm_kernel(const Params pp) {
   const int wm = wave / WN, wn = wave % WN;
   const int r16 = lane & 15, q4 = lane >> 4;
   const int slabs = (pp.kw + 1) >> 1;
-  const int tiles_mn = p.tiles_m * p.tiles_n;
+  __shared__ LiveTiles live;
+  if constexpr (MODE == dg::MODE_MASKED) number_live_tiles<BM, NW>(live, p);
   // chunks 2 * q4 and 2 * q4 + 1 of a fragment's row, swizzled (the rows of a fragment share r16)
   const int f = ((r16 >> 1) & 1) | ((r16 >> 3) << 2);
   const int ch0 = ((2 * q4) ^ f) << 4, ch1 = ((2 * q4 + 1) ^ f) << 4;
   // direct loads: LDS byte 16 * lane of a 1 KiB block is row lane / 8, chunk lane % 8
   const int ld_row = lane >> 3;
+  // (masked: the loads are issued where the compiler does not see them; in a kernel that also loads into registers and reads
+  // other LDS, it has each LDS read wait for all of them)
 
   // Work units: (tile, pass); a contiguous tile whose two 128-row halves belong to different groups takes one pass per group.
   // Group data is read through the constant address space: scalar loads do not share the vector-memory counter with the
@@ -105,18 +168,16 @@ __global__ void __launch_bounds__(WM * WN * 64) gemm_kernel(const Params pp) {
     Unit u;
     u.tile = -1;
     for (; tile < p.num_tiles; tile += gridDim.x, pass = 0) {
-      int g = 0, t = tile;
-      if (MODE == dg::MODE_MASKED) {
-        g = t / tiles_mn;
-        t -= g * tiles_mn;
+      int g = 0, t = tile, tiles_m = p.tiles_m;
+      if constexpr (MODE == dg::MODE_MASKED) {
+        if (!live_tile<BM>(live, p, tile, g, t, tiles_m)) break;
       }
       int mb, nb;
-      dg::raster<4>(t, p.tiles_m, p.tiles_n, mb, nb);
+      dg::raster<4>(t, tiles_m, p.tiles_n, mb, nb);
       const int m0 = mb * BM;
       int row_end = p.m, halves = 3, more = 0;
       if (MODE == dg::MODE_MASKED) {
         row_end = min(max(grp_s[g], 0), p.m);
-        if (m0 >= row_end) continue;
       } else if (MODE == dg::MODE_CONTIG) {
         int g0 = grp_s[m0];
         int g1 = (BM == 256 && m0 + 128 < p.m) ? grp_s[m0 + 128] : -1;
@@ -176,7 +237,7 @@ __global__ void __launch_bounds__(WM * WN * 64) gemm_kernel(const Params pp) {
     asm volatile("" : "+s"(at));  // added here, not kept as one sum per load in registers
     uint32_t v = (odd ? off + odd_flip : off) + at;
     if (2 * slab + 2 > pp.kw && ((chunk0 >= 4) != odd)) v = kPast;
-    dg::load_to_lds<16, false>(r, to, v);
+    dg::load_to_lds<16, MODE == dg::MODE_MASKED>(r, to, v);
   };
   auto issue_load = [&](const Src& r, int slab, int stage, int idx) {
     uint8_t* base = lds + stage * STAGE;
@@ -190,7 +251,7 @@ __global__ void __launch_bounds__(WM * WN * 64) gemm_kernel(const Params pp) {
     if (idx == 0 && wave < 4) {
       const int w = 2 * slab + (wave & 1), len = wave < 2 ? BM : BN;
       if (lane < len / 4)
-        dg::load_to_lds<16, false>(r.rs, base + (wave < 2 ? SA_OFF : SB_OFF) + (wave & 1) * len * 4,
+        dg::load_to_lds<16, MODE == dg::MODE_MASKED>(r.rs, base + (wave < 2 ? SA_OFF : SB_OFF) + (wave & 1) * len * 4,
                                    (w < pp.kw ? (uint32_t)w * ld_s : kPast) + lane * 16);
     }
   };
@@ -400,6 +461,8 @@ __global__ void __launch_bounds__(WM * 256) stream_kernel(const Params pp) {
   static_assert((STAGES - 2) * LOADS < 64, "counted waits");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[STAGES * STAGE];
   __shared__ int s_last;
+  __shared__ LiveTiles live;
+  if constexpr (MODE == dg::MODE_MASKED) number_live_tiles<BM, NW>(live, p);
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -427,16 +490,15 @@ __global__ void __launch_bounds__(WM * 256) stream_kernel(const Params pp) {
     u.tile = -1;
     for (; tile < p.num_tiles; tile += gridDim.x) {
       int g = 0, t = tile, split = 0;
-      if (MODE == dg::MODE_MASKED) g = t / tiles_mn, t -= g * tiles_mn;
+      int tiles_m = p.tiles_m;
+      if constexpr (MODE == dg::MODE_MASKED) {
+        if (!live_tile<BM>(live, p, tile, g, t, tiles_m)) break;
+      }
       if (MODE == dg::MODE_DENSE) split = t / tiles_mn, t -= split * tiles_mn;
       int mb, nb;
-      dg::raster<4>(t, p.tiles_m, p.tiles_n, mb, nb);
+      dg::raster<4>(t, tiles_m, p.tiles_n, mb, nb);
       u.m0 = mb * BM;
-      u.row_end = p.m;
-      if (MODE == dg::MODE_MASKED) {
-        u.row_end = min(max(grp_s[g], 0), p.m);
-        if (u.m0 >= u.row_end) continue;
-      }
+      u.row_end = MODE == dg::MODE_MASKED ? min(max(grp_s[g], 0), p.m) : p.m;
       u.tile = tile;
       u.g = g;
       u.n0 = nb * BN;
@@ -683,7 +745,7 @@ struct Plan {
 };
 
 // The configuration (and, for a dense call, the K split) with the least estimated time, in microseconds, fitted to sweeps of
-// 25 shapes on MI355X (within 10 % of the measured time of the best candidates): 4 us from launch to the first slab and for
+// 28 dense and 5 masked calls on MI355X (the choice within 10 % of the best candidate's time in all but two of them): 4 us from launch to the first slab and for
 // the last stores, 1 us a round of workgroups, the slabs at a rate of the tile's own (streaming tiles: 40 GB/s a CU), and not
 // less than the operands' bytes at 5.5 TB/s.  A split adds 1.2 us to publish and count partials, their bytes at 6 TB/s twice,
 // and the last workgroup's reading of a tile's at 85 GB/s.  rows: of A, or of a group's (masked: the expected number; groups
@@ -707,8 +769,9 @@ Plan plan(int mode, int64_t groups, int rows, int most_rows, int n, int k, int c
     const double rounds = std::ceil(units / slots), busy = std::min(1.0, units / cus);
     const int sps = cdiv(slabs, s);
     double slab_us = is_stream(c) ? (std::min(c.bm, rows) + 128) * 136 / 40e3 : c.alone_us + (c.full_us - c.alone_us) * busy;
-    if (!is_stream(c) && masked && rows <= 256) slab_us += 0.6;  // B from memory, waited for
-    if (c.per_cu == 2 && units <= cus) slab_us = c.alone_us;     // one to a CU
+    if (c.per_cu == 2 && units <= cus) slab_us = c.alone_us;  // one to a CU
+    if (!is_stream(c) && masked)                              // B from memory, waited for
+      slab_us = std::max(slab_us, c.per_cu == 2 ? 2.4 : c.bn / 256.0 * (1.8 + 0.65 * std::min(rows, 256) / 256));
     const double part = s > 1 ? units * c.bm * c.bn * 4 : 0;
     const double us = 4.0 + std::max(rounds * (1.0 + sps * slab_us), bytes / 5.5e6) +
                       (s > 1 ? 1.2 + s * (c.bm * c.bn * 4 / 85e3) + 2 * part / 6e6 : 0.0);
