@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(WM * WN * 64) gemm_kernel(const Params pp) {
 }
 
 // For calls that wait for memory rather than for the matrix cores: few rows, so that the reading of B is the work, or few
-// tiles.  BM x 128 tiles (BM = 32, 64, 128 or 256) on four or eight waves, a ring of STAGES slabs in all of a CU's LDS and
+// tiles.  BM x 128 tiles (BM = 32, 64 or 128) on four or eight waves, a ring of STAGES slabs in all of a CU's LDS and
 // counted waits, so that STAGES - 1 slabs are always on their way (the 256-row tile waits for the slab it has just asked
 // for unless its products take as long as a memory access: 8 rows of 16 experts of 4096 x 7168 took 77 us with it).  Dense
 // calls split K over workgroups: each writes its FP32 partial tile to the workspace and counts itself; the one that
@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(WM * 256) stream_kernel(const Params pp) {
       __syncthreads();
       finish = s_last != 0;
       if (finish) {
-        constexpr int RD = BM == 32 ? 8 : (BM == 64 ? 4 : (BM == 128 ? 2 : 1));  // partials in flight
+        constexpr int RD = BM == 32 ? 8 : (BM == 64 ? 4 : 2);  // partials in flight
         f32x4 buf[RD][FM][FN];
         for (int s0 = 0; s0 < p.splits; s0 += RD) {
 #pragma unroll
@@ -692,14 +692,14 @@ inline int cdiv(int a, int b) { return (a + b - 1) / b; }
 
 // Tile configurations: 256-row tiles on 8 waves, one workgroup per CU (136, 127 and 119 KiB of LDS at 256, 224 and 192
 // columns), and 128 x 128 on 4 waves, two per CU (68 KiB), on two slab stages; and the streaming tiles, one per CU, on a ring
-// of 7, 6, 4 or 3 (149, 154, 136 and 153 KiB at 32, 64, 128 and 256 rows).
+// of 7, 6 or 4 (149, 153 and 136 KiB at 32, 64 and 128 rows).
 struct Cfg {
   int bm, bn, per_cu, threads;
   double alone_us, full_us;  // per slab with few and with all CUs at work (the clock falls); streaming tiles: 0
 };
 constexpr Cfg kWide[4] = {{256, 256, 1, 512, 1.4, 1.9}, {256, 224, 1, 512, 1.35, 1.7}, {256, 192, 1, 512, 1.1, 1.5},
                           {128, 128, 2, 256, 0.84, 1.25}};
-constexpr Cfg kStream[4] = {{32, 128, 1, 256, 0, 0}, {64, 128, 1, 512, 0, 0}, {128, 128, 1, 512, 0, 0}, {256, 128, 1, 512, 0, 0}};
+constexpr Cfg kStream[3] = {{32, 128, 1, 256, 0, 0}, {64, 128, 1, 512, 0, 0}, {128, 128, 1, 512, 0, 0}};
 inline bool is_stream(const Cfg& c) { return c.full_us == 0; }
 
 using Kernel = void (*)(fp4::Params);
@@ -723,9 +723,7 @@ Kernel pick(const Cfg& c, bool bf16, bool has_c) {
   if constexpr (MODE != dg::MODE_CONTIG) {
     if (is_stream(c) && c.bm == 32) return pick_stream<32, 1, 7, MODE>(bf16, has_c);
     if (is_stream(c) && c.bm == 64) return pick_stream<64, 2, 6, MODE>(bf16, has_c);
-    if (is_stream(c) && c.bm == 128) return pick_stream<128, 2, 4, MODE>(bf16, has_c);
-    if constexpr (MODE == dg::MODE_MASKED)
-      if (is_stream(c)) return pick_stream<256, 2, 3, MODE>(bf16, has_c);
+    if (is_stream(c)) return pick_stream<128, 2, 4, MODE>(bf16, has_c);
   }
   if (c.bm == 128) return pick_wide<128, 128, 2, 2, MODE>(bf16, has_c);
   if (c.bn == 224) return pick_wide<256, 224, 4, 2, MODE>(bf16, has_c);
@@ -783,7 +781,6 @@ Plan plan(int mode, int64_t groups, int rows, int most_rows, int n, int k, int c
   for (const Cfg& c : kWide) consider(c, 1);
   if (mode == dg::MODE_CONTIG || k == 0) return best;
   for (const Cfg& c : kStream) {
-    if (c.bm == 256 && !masked) continue;
     consider(c, 1);
     const int64_t tiles = static_cast<int64_t>(cdiv(rows, c.bm)) * cdiv(n, c.bn);
     if (masked || tiles > kCtrWords) continue;
