@@ -466,8 +466,8 @@ size_t dg_get_clip_workspace_size(void);
  *            scale 255, Inf for 2^128, to which inputs past 3.5 * 2^126 round.  May equal x.
  * masked_m   optional DEVICE int32 [num_groups]: only the first masked_m[g] rows of a
  *            group are read and written (clamped to [0, m]).
- * k % 128 != 0 or more than 65535 groups -> DG_ERROR_NOT_SUPPORTED; an empty size ->
- * DG_SUCCESS.
+ * k % 128 != 0, more than 65535 groups or more than 2^38 values a group ->
+ * DG_ERROR_NOT_SUPPORTED; an empty size -> DG_SUCCESS.
  */
 dg_status dg_cast_to_mxfp4(const void* x, int64_t ldx, dg_dtype x_dtype, void* q, int64_t ldq, int32_t* sf,
                            int64_t ld_sf, void* y, int64_t ldy, const int32_t* masked_m, int num_groups, int m, int k,

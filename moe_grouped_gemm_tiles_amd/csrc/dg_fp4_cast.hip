@@ -13,7 +13,8 @@
 // conversion instructions with a scale (checked against the definition for every BF16 value and
 // scale byte).
 //
-// HBM-bound: reads 2 or 4 bytes, writes half a byte, 1/32 and, with y, 2 or 4 per value.  A workgroup
+// HBM-bound: reads 2 or 4 bytes, writes half a byte, 1/32 and, with y, 2 or 4 per value (8 x 4096 x 7168 BF16 with y, 1.06 GB:
+// 208 us, 5.1 TB/s; the same without streaming accesses 213).  A workgroup
 // owns 64 rows x 512 columns; a lane takes 8 values of a row, so a wave reads 1 KiB (BF16) runs, four
 // rows in flight, and a block's amax is two exchanges among four lanes.  The 4 x 64 scale words go
 // through LDS and leave as 256-byte runs of the transposed layout.
@@ -34,6 +35,7 @@ constexpr int kBatch = 4;   // rows a wave has in flight
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 // v with the lanes of each group of four exchanged by a quad permutation.
 template <int CTRL>
@@ -42,13 +44,26 @@ __device__ __forceinline__ uint32_t dpp(uint32_t v) {
 }
 constexpr int kQuadXor1 = 0xB1, kQuadXor2 = 0x4E, kRowRor4 = 0x124, kRowRor8 = 0x128;
 
+// 16-byte accesses, marked as streaming where NT.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+template <bool NT>
+__device__ __forceinline__ u32x4 load16(const uint8_t* p) {
+  if constexpr (NT) return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+  else return *reinterpret_cast<const u32x4*>(p);
+}
+template <bool NT, typename T>
+__device__ __forceinline__ void store(uint8_t* p, T v) {
+  if constexpr (NT) __builtin_nontemporal_store(v, reinterpret_cast<T*>(p));
+  else *reinterpret_cast<T*>(p) = v;
+}
+
 // Eight values as the conversion instructions take them.
-template <bool BF16>
+template <bool BF16, bool NT>
 struct Eight;
-template <>
-struct Eight<true> {
-  uint4 w;
-  __device__ __forceinline__ void load(const uint8_t* p) { w = *reinterpret_cast<const uint4*>(p); }
+template <bool NT>
+struct Eight<true, NT> {
+  u32x4 w;
+  __device__ __forceinline__ void load(const uint8_t* p) { w = load16<NT>(p); }
   // Bits of the largest magnitude, as FP32.
   __device__ __forceinline__ uint32_t amax() const {
     const uint32_t v[4] = {w.x, w.y, w.z, w.w};
@@ -70,21 +85,21 @@ struct Eight<true> {
     return r;
   }
   static __device__ __forceinline__ void store_values(uint8_t* p, uint32_t r, float s, bool nan) {
-    uint4 o;
+    u32x4 o;
     o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(r, s, 0));
     o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(r, s, 1));
     o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(r, s, 2));
     o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(r, s, 3));
-    if (nan) o = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
-    *reinterpret_cast<uint4*>(p) = o;
+    if (nan) o = u32x4{0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u};
+    store<NT>(p, o);
   }
 };
-template <>
-struct Eight<false> {
-  float4 lo, hi;
+template <bool NT>
+struct Eight<false, NT> {
+  f32x4 lo, hi;
   __device__ __forceinline__ void load(const uint8_t* p) {
-    lo = *reinterpret_cast<const float4*>(p);
-    hi = *(reinterpret_cast<const float4*>(p) + 1);
+    lo = __builtin_bit_cast(f32x4, load16<NT>(p));
+    hi = __builtin_bit_cast(f32x4, load16<NT>(p + 16));
   }
   __device__ __forceinline__ uint32_t amax() const {
     const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
@@ -105,8 +120,8 @@ struct Eight<false> {
     const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(r, s, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(r, s, 1);
     const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(r, s, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(r, s, 3);
     const float q = __uint_as_float(0x7fc00000u);
-    *reinterpret_cast<float4*>(p) = nan ? make_float4(q, q, q, q) : make_float4(a[0], a[1], b[0], b[1]);
-    *(reinterpret_cast<float4*>(p) + 1) = nan ? make_float4(q, q, q, q) : make_float4(c[0], c[1], d[0], d[1]);
+    store<NT>(p, nan ? f32x4{q, q, q, q} : f32x4{a[0], a[1], b[0], b[1]});
+    store<NT>(p + 16, nan ? f32x4{q, q, q, q} : f32x4{c[0], c[1], d[0], d[1]});
   }
 };
 
@@ -126,13 +141,15 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
   return amax == 0u ? 127u : (amax >= 0x7f800000u ? 255u : (uint32_t)max(e, 0));
 }
 
-template <bool BF16, bool VALUES>
+template <bool BF16, bool VALUES, bool NT>
 __global__ void __launch_bounds__(256) cast_kernel(const Args a) {
   __shared__ uint32_t s_word[4][kRows];
   constexpr int ES = BF16 ? 2 : 4;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int g = blockIdx.z;
-  const int m0 = blockIdx.x * kRows, c0 = blockIdx.y * kCols;
+  const int g = blockIdx.y;
+  const int col_blocks = (a.k + kCols - 1) / kCols;  // neighbours take the same rows' next columns
+  const int row_block = blockIdx.x / col_blocks;
+  const int m0 = row_block * kRows, c0 = (blockIdx.x - row_block * col_blocks) * kCols;
   const int rows = min(a.masked_m != nullptr ? min(max(a.masked_m[g], 0), a.m) : a.m, m0 + kRows);
   if (m0 >= rows) return;
   const int col = c0 + 8 * lane;
@@ -142,7 +159,7 @@ __global__ void __launch_bounds__(256) cast_kernel(const Args a) {
   uint8_t* q = a.q + (int64_t)g * a.m * a.ldq + (col >> 1);
   uint8_t* y = VALUES ? a.y + (int64_t)g * a.m * a.ldy_bytes + (int64_t)col * ES : nullptr;
   for (int r0 = wave * kBatch; r0 < kRows; r0 += 4 * kBatch) {
-    Eight<BF16> v[kBatch];
+    Eight<BF16, NT> v[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int row = m0 + r0 + i;
@@ -165,8 +182,8 @@ __global__ void __launch_bounds__(256) cast_kernel(const Args a) {
       word |= dpp<kRowRor4>(word);
       word |= dpp<kRowRor8>(word);
       if (in) {
-        *reinterpret_cast<uint32_t*>(q + (int64_t)row * a.ldq) = codes;
-        if (VALUES) Eight<BF16>::store_values(y + (int64_t)row * a.ldy_bytes, codes, s, nan);
+        store<NT>(q + (int64_t)row * a.ldq, codes);
+        if (VALUES) Eight<BF16, NT>::store_values(y + (int64_t)row * a.ldy_bytes, codes, s, nan);
         if ((lane & 15) == 0) s_word[lane >> 4][r0 + i] = word;
       }
     }
@@ -199,17 +216,24 @@ dg_status dg_cast_to_mxfp4(const void* x, int64_t ldx, dg_dtype x_dtype, void* q
     return DG_ERROR_INVALID_VALUE;
   if (ldx < k || (ldx * es) % 16 != 0 || ldq < k / 2 || ldq % 4 != 0 || ld_sf < m) return DG_ERROR_INVALID_VALUE;
   if (y != nullptr && (!aligned_to(y, 16) || ldy < k || (ldy * es) % 16 != 0)) return DG_ERROR_INVALID_VALUE;
-  const dim3 grid((m + fp4c::kRows - 1) / fp4c::kRows, (k + fp4c::kCols - 1) / fp4c::kCols, num_groups);
-  if (grid.y > 65535 || grid.z > 65535) return DG_ERROR_NOT_SUPPORTED;
+  const int64_t col_blocks = (static_cast<int64_t>(k) + fp4c::kCols - 1) / fp4c::kCols;
+  const int64_t blocks = (static_cast<int64_t>(m) + fp4c::kRows - 1) / fp4c::kRows * col_blocks;
+  if (col_blocks > 65535 || blocks > (1 << 23) || num_groups > 65535) return DG_ERROR_NOT_SUPPORTED;
+  const dim3 grid(static_cast<unsigned>(blocks), num_groups);
   const fp4c::Args a{static_cast<const uint8_t*>(x), static_cast<uint8_t*>(q), sf, static_cast<uint8_t*>(y), masked_m,
                      ldx * es, ldq, ld_sf, ldy * es, m, k};
-  if (x_dtype == DG_DTYPE_BF16) {
-    if (y) hipLaunchKernelGGL((fp4c::cast_kernel<true, true>), grid, dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL((fp4c::cast_kernel<true, false>), grid, dim3(256), 0, stream, a);
-  } else {
-    if (y) hipLaunchKernelGGL((fp4c::cast_kernel<false, true>), grid, dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL((fp4c::cast_kernel<false, false>), grid, dim3(256), 0, stream, a);
-  }
+  // operands past the last-level cache's 256 MiB are streamed (smaller ones are left there for their readers: 4099 x 1408 FP32
+  // with y, called again and again, takes 12 us, streamed 18)
+  const int64_t bytes = static_cast<int64_t>(num_groups) * m * k * (y ? 2 * es + 1 : es + 1);
+  const bool nt = bytes > (int64_t)256 << 20;
+  void (*fn)(fp4c::Args);
+  if (x_dtype == DG_DTYPE_BF16)
+    fn = y ? (nt ? fp4c::cast_kernel<true, true, true> : fp4c::cast_kernel<true, true, false>)
+           : (nt ? fp4c::cast_kernel<true, false, true> : fp4c::cast_kernel<true, false, false>);
+  else
+    fn = y ? (nt ? fp4c::cast_kernel<false, true, true> : fp4c::cast_kernel<false, true, false>)
+           : (nt ? fp4c::cast_kernel<false, false, true> : fp4c::cast_kernel<false, false, false>);
+  hipLaunchKernelGGL(fn, grid, dim3(256), 0, stream, a);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? DG_SUCCESS : dg::record_hip_error(e);
 }
