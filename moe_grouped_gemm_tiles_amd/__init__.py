@@ -189,6 +189,7 @@ _SIGNATURES = {
     "dg_get_num_cus": (_i32, []),
     "dg_internal_set_tile_n": (_i32, [_i32]),
     "dg_internal_dense_plan": (_i32, [_i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp]),
+    "dg_internal_mxfp4_plan": (_i32, [_i32, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp]),
     "dg_status_string": (ctypes.c_char_p, [_i32]),
     "dg_last_hip_error": (ctypes.c_char_p, []),
 }
@@ -1123,6 +1124,16 @@ def _dense_plan_for_tests(m: int, n: int, k: int, cus: int) -> dict:
     _check(load_library().dg_internal_dense_plan(m, n, k, cus, *[ctypes.byref(v) for v in vals], ctypes.byref(ws)))
     bm, bn, splits, sps = (v.value for v in vals)
     return dict(bm=bm, bn=bn, splits=splits, slabs_per_split=sps, ws_bytes=ws.value)
+
+
+def _mxfp4_plan_for_tests(mode: str, rows: int, n: int, k: int, cus: int = 256, groups: int = 1, most_rows: int = 0) -> dict:
+    """The tile, K split and workspace size a 4-bit call gets.  Not part of the API: the tests pin the planner."""
+    vals = [ctypes.c_int(0) for _ in range(4)]
+    ws = ctypes.c_size_t(0)
+    _check(load_library().dg_internal_mxfp4_plan(("dense", "contiguous", "masked").index(mode), groups, rows, max(rows, most_rows),
+                                                 n, k, cus, *[ctypes.byref(v) for v in vals], ctypes.byref(ws)))
+    bm, bn, streaming, splits = (v.value for v in vals)
+    return dict(bm=bm, bn=bn, streaming=bool(streaming), splits=splits, ws_bytes=ws.value)
 
 
 # The README's names for the same utilities ("Utilities": set_num_sms / get_num_sms cap the

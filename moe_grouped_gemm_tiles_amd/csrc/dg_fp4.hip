@@ -23,6 +23,7 @@
 
 #include "dg.h"
 #include "dg_common.hpp"
+#include "dg_internal.h"
 #include "dg_kernels.hpp"
 
 namespace {
@@ -927,6 +928,20 @@ dg_status dg_m_grouped_mxfp4_gemm_nt_masked(const void* a, const int32_t* sfa, i
   const int cus = usable_cus();
   const int rows = expected_m > 0 && expected_m < m_max ? expected_m : (m_max + 1) / 2;
   return launch<dg::MODE_MASKED>(pp, plan(dg::MODE_MASKED, num_groups, rows, m_max, n, k, cus), d_dtype, num_groups, cus, stream);
+}
+
+dg_status dg_internal_mxfp4_plan(int mode, int groups, int rows, int most_rows, int n, int k, int cus, int* bm, int* bn,
+                                 int* streaming, int* splits, size_t* ws_bytes) {
+  if (mode < 0 || mode > 2 || groups <= 0 || rows <= 0 || most_rows < rows || n <= 0 || k <= 0 || k % 128 != 0 || cus <= 0 ||
+      bm == nullptr || bn == nullptr || streaming == nullptr || splits == nullptr || ws_bytes == nullptr)
+    return DG_ERROR_INVALID_VALUE;
+  const Plan pl = plan(mode, groups, rows, most_rows, n, k, cus);
+  *bm = pl.cfg.bm;
+  *bn = pl.cfg.bn;
+  *streaming = is_stream(pl.cfg);
+  *splits = pl.splits;
+  *ws_bytes = pl.ws_bytes;
+  return DG_SUCCESS;
 }
 
 }  // extern "C"
