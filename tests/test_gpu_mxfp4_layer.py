@@ -26,7 +26,8 @@ DENSE = [((4000, 3600, 384), (256, 256, False, False)), ((4090, 7168, 640), (256
 CONTIGUOUS = [((8, 4096, 384, 512), (256, 256)), ((16, 3584, 640, 512), (256, 224)), ((10, 2304, 384, 512), (256, 192)),
               ((5, 1008, 1408, 400), (128, 128))]
 MASKED = [((16, 4096, 640, 250, 256), (256, 256, False)), ((24, 1792, 640, 200, 256), (256, 192, False)),
-          ((40, 2048, 640, 10, 64), (32, 128, True)), ((40, 2048, 640, 50, 64), (64, 128, True))]
+          ((16, 3584, 640, 240, 256), (256, 224, False)), ((40, 2048, 640, 10, 64), (32, 128, True)),
+          ((40, 2048, 640, 50, 64), (64, 128, True)), ((16, 4096, 640, 64, 256), (128, 128, True))]
 
 
 def test_shapes_reach_every_configuration():

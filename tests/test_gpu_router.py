@@ -117,6 +117,25 @@ def test_router_random_bias_orders_like_fp64(score):
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("e,k,lanes", [(256, 8, 16), (256, 12, 16), (128, 8, 16), (256, 20, 32), (512, 10, 32), (1000, 16, 64)])
+def test_router_chosen_experts_of_one_lane(e, k, lanes, score, dtype):
+    """The chosen experts lie where one lane holds them all (4 in a row, every 4 * lanes), more than it keeps at hand; in
+    every fourth row spread over two lanes, and in others ties among them."""
+    rng = np.random.default_rng(9)
+    x = rng.standard_normal((120, e))
+    for t in range(len(x)):
+        lane = int(rng.integers(0, lanes - 1))
+        for one in ([lane] if t % 4 else [lane, lane + 1]):
+            at = [i for i in range(e) if (i // 4) % lanes == one]
+            x[t, at] = 5 + (rng.integers(0, 3, len(at)) if t % 3 == 0 else rng.random(len(at)))
+    t = torch.from_numpy(x.astype(np.float32)).to(DT[dtype]).to(DEV)
+    for bias in (None, (0.01 * rng.standard_normal(e)).astype(np.float32)):
+        check_forward(forward(t, k, score=score, bias=None if bias is None else torch.from_numpy(bias).to(DEV)), as_f64(t), k,
+                      score=score, bias=bias)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_router_dead_experts_and_empty_rows(score, dtype):
     x = logits(50, 40, dtype, dead=30)
     x[7] = -float("inf")
