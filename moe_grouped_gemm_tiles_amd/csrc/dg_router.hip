@@ -7,6 +7,18 @@
 //   share  = p / (sum over all + 1e-20)           (softmax: p itself)
 //   counts = how often an expert is chosen, prob_sum = sum over rows of share
 //   loss   = E * sum_e counts_e prob_sum_e / (sum counts * sum prob_sum)
+//
+// Forward: 16 lanes hold a row of up to 256 experts (32 or 64 lanes past that, or for more than 15 chosen), so that a wave
+// works on four rows and reductions stay in a DPP row.  A key is one register: the value's leading bits in an unsigned order,
+// and the index below them, so that a maximum finds value and tie-break at once.  Each lane sorts its keys and keeps five; the
+// largest head is taken top_k times.  Where the bits that the index pushed out, or FP32's errors in score + bias, leave the
+// order open, more are taken and sorted by full values, and at last all keys are compared in FP64 by the whole wave.
+// Sums of scores are held in registers per lane and expert; each workgroup leaves one partial row, which a second kernel adds
+// in FP64 in a fixed order (integer atomics would do for the counts, but FP ones would change the sums from run to run).
+//
+// 33280 x 256 FP32, sigmoid, bias, mask, top 8, loss: 21 us and 7 us for the second kernel (a wave per row with FP64 keys: 258);
+// 34 MB of logits are 5 us of HBM, so the 700 vector instructions for four rows bound it (8 us of them issue alone).  Gradient,
+// BF16: 15 us (510 instructions for four rows).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
