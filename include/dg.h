@@ -466,7 +466,7 @@ size_t dg_get_clip_workspace_size(void);
  *            scale 255, Inf for 2^128, to which inputs past 3.5 * 2^126 round.  May equal x.
  * masked_m   optional DEVICE int32 [num_groups]: only the first masked_m[g] rows of a
  *            group are read and written (clamped to [0, m]).
- * k % 128 != 0, more than 65535 groups or more than 2^38 values a group ->
+ * k % 128 != 0, more than 65535 groups or more than 2^36 values a group ->
  * DG_ERROR_NOT_SUPPORTED; an empty size -> DG_SUCCESS.
  */
 dg_status dg_cast_to_mxfp4(const void* x, int64_t ldx, dg_dtype x_dtype, void* q, int64_t ldq, int32_t* sf,
@@ -484,7 +484,8 @@ dg_status dg_cast_to_mxfp4(const void* x, int64_t ldx, dg_dtype x_dtype, void* q
  *              of 4, 16-B aligned.
  *   workspace  dg_get_mxfp4_workspace_size(m, n, k) bytes for the dense form, as
  *              described at the top.
- * A block whose scale is 255 makes its row of A (of B: its column of D) NaN.
+ * Rows of 8 MiB or more (lda, ldb) and scale arrays of 2 GiB or more ->
+ * DG_ERROR_NOT_SUPPORTED.  A block whose scale is 255 makes its row of A (of B: its column of D) NaN.
  * All of K accumulates in the matrix cores' FP32; C is added in FP32 and D rounded
  * once.  The same bits every time for a shape and CU count.
  */

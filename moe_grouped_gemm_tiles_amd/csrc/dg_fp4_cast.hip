@@ -13,11 +13,11 @@
 // conversion instructions with a scale (checked against the definition for every BF16 value and
 // scale byte).
 //
-// HBM-bound: reads 2 or 4 bytes, writes half a byte, 1/32 and, with y, 2 or 4 per value (8 x 4096 x 7168 BF16 with y, 1.06 GB:
-// 208 us, 5.1 TB/s; the same without streaming accesses 213).  A workgroup
-// owns 64 rows x 512 columns; a lane takes 8 values of a row, so a wave reads 1 KiB (BF16) runs, four
-// rows in flight, and a block's amax is two exchanges among four lanes.  The 4 x 64 scale words go
-// through LDS and leave as 256-byte runs of the transposed layout.
+// HBM-bound: reads 2 or 4 bytes, writes half a byte, 1/32 and, with y, 2 or 4 per value.  A workgroup owns 16 rows x 512
+// columns; a lane takes 8 values of a row, so a wave reads 1 KiB (BF16) runs, its four rows in flight at once, and a block's
+// amax is two exchanges among four lanes.  The 4 x 16 scale words go through LDS and leave as 64-byte runs of the transposed
+// layout.  8 x 4096 x 7168 BF16 with y, 1.06 GB: 171 us, 6.2 TB/s (32 rows per workgroup 185, 64 rows 207: fewer rows keep a
+// workgroup's reads and writes close together in time).
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -29,7 +29,7 @@ namespace {
 
 namespace fp4c {
 
-constexpr int kRows = 64;   // rows per workgroup
+constexpr int kRows = 16;   // rows per workgroup, kBatch for each wave
 constexpr int kCols = 512;  // columns per workgroup (four scale words)
 constexpr int kBatch = 4;   // rows a wave has in flight
 
@@ -158,7 +158,9 @@ __global__ void __launch_bounds__(256) cast_kernel(const Args a) {
   const uint8_t* x = a.x + (int64_t)g * a.m * a.ldx_bytes + (int64_t)col * ES;
   uint8_t* q = a.q + (int64_t)g * a.m * a.ldq + (col >> 1);
   uint8_t* y = VALUES ? a.y + (int64_t)g * a.m * a.ldy_bytes + (int64_t)col * ES : nullptr;
-  for (int r0 = wave * kBatch; r0 < kRows; r0 += 4 * kBatch) {
+  static_assert(kRows == 4 * kBatch, "a wave takes its rows at once");
+  {
+    const int r0 = wave * kBatch;
     Eight<BF16, NT> v[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
@@ -189,9 +191,9 @@ __global__ void __launch_bounds__(256) cast_kernel(const Args a) {
     }
   }
   __syncthreads();
-  const int w = tid >> 6, r = tid & 63;
+  const int w = tid / kRows, r = tid % kRows;
   const int wk = (c0 >> 7) + w;
-  if (wk < kw && m0 + r < rows)
+  if (w < 4 && wk < kw && m0 + r < rows)
     a.sf[((int64_t)g * kw + wk) * a.ld_sf + m0 + r] = (int32_t)s_word[w][r];
 }
 
