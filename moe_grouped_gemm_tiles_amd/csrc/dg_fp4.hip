@@ -829,14 +829,16 @@ dg_status check(const void* a, int64_t lda, const void* sfa, int64_t ld_sfa, con
   if (rows == 0 || n == 0) return DG_SUCCESS;  // empty tensors may have no address
   const int64_t es = t == DG_DTYPE_BF16 ? 2 : 4;
   if (d == nullptr || !aligned(d, 16) || ldd < n || (ldd * es) % 16 != 0) return DG_ERROR_INVALID_VALUE;
+  // for any K: an empty product's kernel builds its descriptors from the strides too
+  if (lda < k / 2 || ldb < k / 2 || lda % 16 != 0 || ldb % 16 != 0) return DG_ERROR_INVALID_VALUE;
+  // offsets within a tile's rows, among a group's scales, and row and column numbers of the tiles stay below 2^31
+  if (lda >= (1ll << 23) || ldb >= (1ll << 23) || rows >= (1 << 29) || n >= (1 << 29)) return DG_ERROR_NOT_SUPPORTED;
   if (k > 0) {
     if (a == nullptr || b == nullptr || sfa == nullptr || sfb == nullptr) return DG_ERROR_INVALID_VALUE;
     if (!aligned(a, 16) || !aligned(b, 16) || !aligned(sfa, 16) || !aligned(sfb, 16)) return DG_ERROR_INVALID_VALUE;
-    if (lda < k / 2 || ldb < k / 2 || lda % 16 != 0 || ldb % 16 != 0) return DG_ERROR_INVALID_VALUE;
     if (ld_sfa < rows || ld_sfa % 4 != 0 || ld_sfb < n || ld_sfb % 4 != 0) return DG_ERROR_INVALID_VALUE;
-    // offsets within a tile's rows, and among a group's scales, stay below 2^31
-    if (lda * 256 >= (1ll << 31) || ldb * 256 >= (1ll << 31)) return DG_ERROR_NOT_SUPPORTED;
-    if (k / 128 * 4 * ld_sfa >= (1ll << 31) || k / 128 * 4 * ld_sfb >= (1ll << 31)) return DG_ERROR_NOT_SUPPORTED;
+    const int64_t most = ((1ll << 31) - 1) / (k / 128 * 4);
+    if (ld_sfa > most || ld_sfb > most) return DG_ERROR_NOT_SUPPORTED;
   }
   return DG_SUCCESS;
 }
@@ -850,8 +852,8 @@ fp4::Params params(const void* a, int64_t lda, const int32_t* sfa, int64_t ld_sf
   p.sfa = reinterpret_cast<const float*>(sfa);
   p.sfb = reinterpret_cast<const float*>(sfb);
   p.d = d;
-  p.lda = lda;
-  p.ldb = ldb;
+  p.lda = k > 0 ? lda : 0;  // k == 0: descriptors of no bytes, whatever the pointers are
+  p.ldb = k > 0 ? ldb : 0;
   p.ldd = ldd;
   p.ld_sfa = ld_sfa;
   p.m = m;
@@ -869,7 +871,7 @@ fp4::Params params(const void* a, int64_t lda, const int32_t* sfa, int64_t ld_sf
 extern "C" {
 
 size_t dg_get_mxfp4_workspace_size(int m, int n, int k) {
-  if (m <= 0 || n <= 0 || k <= 0 || k % 128 != 0) return 0;
+  if (m <= 0 || n <= 0 || k <= 0 || k % 128 != 0 || m >= (1 << 29) || n >= (1 << 29)) return 0;
   return plan(dg::MODE_DENSE, 1, m, m, n, k, usable_cus()).ws_bytes;
 }
 
