@@ -35,6 +35,7 @@ namespace route {
 constexpr float kTiny = 1e-20f;
 constexpr int kWaves = 4;         // waves per workgroup
 constexpr int kMaxBlocks = 1280;  // workgroups of a large batch, each with its own partial sums
+constexpr int kMaxAlone = 1 << 20;  // and of one without sums: a grid holds fewer than 2^32 threads
 constexpr int kFinishCols = 16;  // experts per workgroup of the second kernel
 
 // Workspace: a header (the count of finished workgroups, then three sums for each workgroup of the second kernel),
@@ -364,15 +365,15 @@ __global__ void __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_e
   float ps[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) ps[i] = 0.f;
-  const int stride = gridDim.x * kWaves * R;
+  // unsigned: a row number plus the grid's rows passes 2^31 in a batch near that
+  const uint32_t m = a.m, stride = gridDim.x * kWaves * R;
   // rows past the end repeat the last one and store nothing
-  const int first = (blockIdx.x * kWaves + wave) * R + grp;
-  for (int base = first - grp; base < a.m; base += stride) {
-    const int row = base + grp;
+  for (uint32_t base = (blockIdx.x * kWaves + wave) * R; base < m; base += stride) {
+    const uint32_t row = base + grp;
     float x[V], p[V];
-    const uint8_t there = a.mask != nullptr ? a.mask[min(row, a.m - 1)] : 1;
-    const bool on = row < a.m && there != 0;
-    load_row<L, V, BF16>(a.logits + (int64_t)min(row, a.m - 1) * a.ld, a.e, a.vec, l, x);
+    const uint8_t there = a.mask != nullptr ? a.mask[min(row, m - 1)] : 1;
+    const bool on = row < m && there != 0;
+    load_row<L, V, BF16>(a.logits + (int64_t)min(row, m - 1) * a.ld, a.e, a.vec, l, x);
     wave_sync();  // the last rows' reads are done
 #pragma unroll
     for (int c = 0; c < V / 4; ++c)
@@ -469,7 +470,7 @@ __global__ void __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_e
     if (l >= a.k || !on) id = -1;
     const float w = id >= 0 ? score<SIGMOID>(xs[id], n) : 0.f;
     const float f = a.normalize ? a.scale / (sum_of<L>(w) + kTiny) : a.scale;
-    if (l < a.k && row < a.m) {
+    if (l < a.k && row < m) {
       a.ids[(int64_t)row * a.k + l] = id;
       a.weights[(int64_t)row * a.k + l] = w * f;
     }
@@ -610,8 +611,7 @@ __global__ void __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_e
   float g[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) g[i] = 0.f;
-  const int stride = gridDim.x * kWaves * R;
-  const int first = (blockIdx.x * kWaves + wave) * R + grp;
+  const uint32_t m = a.m, stride = gridDim.x * kWaves * R;
   if (a.counts != nullptr) {  // g_e = dloss * E * counts_e / (sum counts * sum prob_sum)
     double c = 0, s = 0;
     for (int e = tid; e < a.e; e += kWaves * 64) {
@@ -632,8 +632,8 @@ __global__ void __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_e
 #pragma unroll
     for (int i = 0; i < V; ++i) g[i] = expert<L>(l, i) < a.e ? f * g[i] : 0.f;
   }
-  for (int base = first - grp; base < a.m; base += stride) {
-    const int row = min(base + grp, a.m - 1);
+  for (uint32_t base = (blockIdx.x * kWaves + wave) * R; base < m; base += stride) {
+    const uint32_t row = min(base + grp, m - 1);
     float x[V], p[V];
     const int64_t slot = (int64_t)row * a.k + min(l, a.k - 1);
     const int slot_id = a.ids[slot];
@@ -687,7 +687,7 @@ __global__ void __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_e
 #pragma unroll
       for (int i = 0; i < V; ++i) dp[i] = p[i] * (dp[i] - dot);
     }
-    if (base + grp < a.m) {
+    if (base + grp < m) {
       uint8_t* out = a.dx + (int64_t)row * a.ld_dx;
 #pragma unroll
       for (int i = 0; i < V; ++i) dp[i] = on ? dp[i] : 0.f;
@@ -740,9 +740,10 @@ dg_status sizes(int m, int e, int k, dg_dtype t, dg_score s) {
   return DG_SUCCESS;
 }
 
+inline int ceil_div(int a, int b) { return static_cast<int>((static_cast<int64_t>(a) + b - 1) / b); }
+
 inline int blocks_of(int m, int e) {
-  const int rows = route::rows_at_once(route::lanes_of(e, 1));
-  const int b = (m + rows - 1) / rows;
+  const int b = ceil_div(m, route::rows_at_once(route::lanes_of(e, 1)));
   return b < 1 ? 1 : (b > route::kMaxBlocks ? route::kMaxBlocks : b);
 }
 
@@ -796,10 +797,10 @@ dg_status dg_moe_router(const void* logits, int64_t ld, dg_dtype dtype, const fl
     hipLaunchKernelGGL(route::zero_kernel, dim3(1), dim3(1024), 0, stream, a);
   } else {
     with_variant(num_experts, top_k, dtype, score, [&](auto l, auto v, auto bf, auto sg) {
-      const int rows = route::rows_at_once(l), need = (m + rows - 1) / rows;
+      const int need = ceil_div(m, route::rows_at_once(l));
       // as many workgroups as give each the same number of rounds, at most
-      const int most = blocks_of(m, num_experts), rounds = (need + most - 1) / most;
-      a.blocks = counts == nullptr ? need : (need + rounds - 1) / rounds;
+      const int most = counts == nullptr ? route::kMaxAlone : blocks_of(m, num_experts), rounds = ceil_div(need, most);
+      a.blocks = ceil_div(need, rounds);
       hipLaunchKernelGGL((route::forward_kernel<l, v, bf, sg>), dim3(a.blocks), dim3(route::kWaves * 64), 0, stream, a);
     });
     if (counts != nullptr && a.blocks > 1)
@@ -830,9 +831,8 @@ dg_status dg_moe_router_backward(const void* logits, int64_t ld, dg_dtype dtype,
   const route::GradArgs a{static_cast<const uint8_t*>(logits), topk_ids, dweights, counts, prob_sum, dloss,
                           static_cast<uint8_t*>(dlogits), ldb, ldd, scale, m, num_experts, top_k, normalize, vec};
   with_variant(num_experts, top_k, dtype, score, [&](auto l, auto v, auto bf, auto sg) {
-    const int rows = route::rows_at_once(l), need = (m + rows - 1) / rows;
-    const int rounds = (need + route::kMaxBlocks - 1) / route::kMaxBlocks;
-    hipLaunchKernelGGL((route::backward_kernel<l, v, bf, sg>), dim3((need + rounds - 1) / rounds), dim3(route::kWaves * 64), 0,
+    const int need = ceil_div(m, route::rows_at_once(l)), rounds = ceil_div(need, route::kMaxBlocks);
+    hipLaunchKernelGGL((route::backward_kernel<l, v, bf, sg>), dim3(ceil_div(need, rounds)), dim3(route::kWaves * 64), 0,
                        stream, a);
   });
   const hipError_t e = hipGetLastError();
