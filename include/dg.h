@@ -517,8 +517,9 @@ dg_status dg_m_grouped_mxfp4_gemm_nt_masked(const void* a, const int32_t* sfa, i
  *            (1 when every expert is chosen equally often; 0 where nothing is chosen)
  * An expert whose logit is -inf (or whose key is -inf or NaN) is never chosen; slots
  * without an expert get id -1 and weight 0, as do all slots of a masked row, which
- * adds nothing to counts and prob_sum.  A NaN or +inf logit gives the NaNs that the
- * formulas give; ids are in range whatever the logits.
+ * adds nothing to counts and prob_sum.  A NaN logit makes its row's share NaN, and
+ * in a softmax, where +inf does too, all of its p; a sigmoid of +inf is 1.  prob_sum
+ * and loss become NaN with a row's share; ids are in range whatever the logits.
  *
  * logits        [m, num_experts], BF16 or FP32, row stride ld, aligned to its type.
  * bias          optional FP32 [num_experts]; steers the choice only.

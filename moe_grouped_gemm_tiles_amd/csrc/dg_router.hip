@@ -472,7 +472,7 @@ __global__ void __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_e
     const float f = a.normalize ? a.scale / (sum_of<L>(w) + kTiny) : a.scale;
     if (l < a.k && row < m) {
       a.ids[(int64_t)row * a.k + l] = id;
-      a.weights[(int64_t)row * a.k + l] = w * f;
+      a.weights[(int64_t)row * a.k + l] = id >= 0 ? w * f : 0.f;  // (f may be Inf or NaN)
     }
     if (stats && id >= 0) atomicAdd(&s_counts[id], 1u);
   }

@@ -11,9 +11,10 @@ def _scores(x: np.ndarray, score: str):
     """(p, share) of logits x [m, E]."""
     if score == "softmax":
         top = x.max(1, keepdims=True)
-        e = np.exp(x - np.where(np.isinf(top), 0.0, top))
+        with np.errstate(invalid="ignore"):  # a NaN or +inf makes its whole row NaN
+            e = np.exp(x - np.where(top == -np.inf, 0.0, top))
         total = e.sum(1, keepdims=True)
-        p = np.divide(e, total, out=np.zeros_like(e), where=total > 0)
+        p = np.divide(e, total, out=np.zeros_like(e), where=total != 0)
         return p, p
     e = np.exp(-np.abs(x))
     p = np.where(x >= 0, 1.0, e) / (1.0 + e)
@@ -25,7 +26,7 @@ def ref_router(logits, top_k, score="softmax", bias=None, mask=None, normalize=T
     x = np.asarray(logits, dtype=np.float64)
     m, e = x.shape
     p, share = _scores(x, score)
-    key = x if bias is None else np.where(np.isinf(x), x, p + np.asarray(bias, dtype=np.float64))
+    key = x if bias is None else np.where(x == -np.inf, x, p + np.asarray(bias, dtype=np.float64))
     ids = np.full((m, top_k), -1, dtype=np.int64)
     weights = np.zeros((m, top_k))
     on = np.ones(m, dtype=bool) if mask is None else np.asarray(mask, dtype=bool)
@@ -36,11 +37,11 @@ def ref_router(logits, top_k, score="softmax", bias=None, mask=None, normalize=T
             left.remove(best)
             ids[t, slot], weights[t, slot] = best, p[t, best]
     if normalize:
-        weights = weights / (weights.sum(1, keepdims=True) + TINY)
+        weights = np.where(ids >= 0, weights / (weights.sum(1, keepdims=True) + TINY), 0.0)
     counts = np.bincount(ids[ids >= 0], minlength=e)
     prob_sum = share[on].sum(0)
     den = counts.sum() * prob_sum.sum()
-    loss = e * (counts * prob_sum).sum() / den if den > 0 else 0.0
+    loss = e * (counts * prob_sum).sum() / den if den != 0 else 0.0
     return dict(ids=ids, weights=weights * scale, counts=counts, prob_sum=prob_sum, loss=loss)
 
 
