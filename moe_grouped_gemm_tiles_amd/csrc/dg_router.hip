@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_e
     __syncthreads();
     if (tid == 0) {
       for (int w = 1; w < kWaves; ++w) c += s_red[0][w], s += s_red[1][w], cs += s_red[2][w];
-      *a.loss = c * s == 0 ? 0.f : (float)(a.e * cs / (c * s));
+      *a.loss = c == 0 || s == 0 ? 0.f : (float)(a.e * cs / (c * s));
     }
   }
 }
@@ -588,7 +588,7 @@ __global__ void __launch_bounds__(1024) finish_kernel(const Args a) {
     p += __shfl_xor(p, o);
     cs += __shfl_xor(cs, o);
   }
-  if (tid == 0) *a.loss = c * p == 0 ? 0.f : (float)(a.e * cs / (c * p));
+  if (tid == 0) *a.loss = c == 0 || p == 0 ? 0.f : (float)(a.e * cs / (c * p));
 }
 
 // A batch of no rows.

@@ -41,7 +41,7 @@ def ref_router(logits, top_k, score="softmax", bias=None, mask=None, normalize=T
     counts = np.bincount(ids[ids >= 0], minlength=e)
     prob_sum = share[on].sum(0)
     den = counts.sum() * prob_sum.sum()
-    loss = e * (counts * prob_sum).sum() / den if den != 0 else 0.0
+    loss = e * (counts * prob_sum).sum() / den if counts.sum() > 0 and den != 0 else 0.0
     return dict(ids=ids, weights=weights * scale, counts=counts, prob_sum=prob_sum, loss=loss)
 
 

@@ -54,6 +54,20 @@ def test_nan_and_inf_logits(e, k, score, normalize, dtype):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("m", [30, 3000])
+def test_no_loss_where_nothing_is_chosen(score, m):
+    """A bias of NaN takes every expert out; the rows' shares may still be NaN."""
+    x = logits(m, 20, "fp32")
+    bias = torch.full((20,), float("nan"), device=DEV)
+    for nan in (False, True):
+        if nan:
+            x[5, 3] = float("nan")
+        out = forward(x, 4, score=score, bias=bias)
+        assert (out["ids"] == -1).all() and not out["weights"].any() and not out["counts"].any() and float(out["loss"]) == 0.0
+        assert bool(torch.isnan(out["prob_sum"]).all()) == nan
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_slots_without_an_expert_weigh_nothing_at_any_scale(score):
     x = logits(50, 16, "fp32", dead=13)
     mask = torch.rand(50, generator=torch.Generator().manual_seed(1)).to(DEV) < 0.5
