@@ -549,7 +549,8 @@ size_t dg_get_moe_router_workspace_size(int m, int num_experts);
  * the call: then this is a rank's part of the gradient of the whole batch's loss.
  *
  * topk_ids      the forward's; slots outside [0, num_experts) have no gradient, and a
- *               row without any (a masked one) gets zeros.
+ *               row without any (a masked one) gets zeros.  In other rows a NaN logit makes
+ *               NaN of its own gradient and, in a softmax (+inf too) or with dloss, of the row's.
  * counts, prob_sum, dloss (FP32 [1])  all or none.
  * dlogits       [m, num_experts], logits' dtype, row stride ld_dlogits; may equal logits.
  * Sizes as above.

@@ -671,10 +671,12 @@ __global__ void __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_e
     if constexpr (SIGMOID) {
 #pragma unroll
       for (int i = 0; i < V; ++i) dot += g[i] * p[i];
-      dot = sum_of<L>(dot) * n.inv;
+      // without the loss nothing depends on the row's sum, which may be NaN
+      const float inv = a.counts != nullptr ? n.inv : 0.f;
+      dot = a.counts != nullptr ? sum_of<L>(dot) * inv : 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        dp[i] = (dp[i] + (g[i] - dot) * n.inv) * p[i] * sigmoid(-x[i]);
+        dp[i] = (dp[i] + (g[i] - dot) * inv) * p[i] * sigmoid(-x[i]);
       }
     } else {
 #pragma unroll

@@ -71,8 +71,9 @@ def ref_router_backward(logits, ids, dweights, counts=None, prob_sum=None, dloss
             dx[t] = p[t] * (dp - (p[t] * dp).sum())
             mag[t] = p[t] * (dm + (p[t] * dm).sum())
         else:
-            q = p[t].sum() + TINY
-            dp, dm = dp + (g - (g * share[t]).sum()) / q, dm + (np.abs(g) + (np.abs(g) * share[t]).sum()) / q
+            if counts is not None:
+                q = p[t].sum() + TINY
+                dp, dm = dp + (g - (g * share[t]).sum()) / q, dm + (np.abs(g) + (np.abs(g) * share[t]).sum()) / q
             slope = p[t] * _scores(-x[t:t + 1], "sigmoid")[0][0]
             dx[t], mag[t] = dp * slope, dm * slope
     return dx, mag

@@ -12,7 +12,7 @@ pytestmark = pytest.mark.gpu
 
 if torch.cuda.is_available():  # pragma: no cover - GPU only
     from tests._gpu_harness import DEV, as_f64
-    from tests.test_gpu_router import forward, logits, tolerance
+    from tests.test_gpu_router import STEP, backward, forward, logits, tolerance
 
 # experts and top_k of each number of lanes a row has, with and without room for all experts among the chosen
 LAYOUTS = [(12, 12), (60, 4), (200, 15), (256, 20), (400, 6), (1000, 64)]
@@ -75,3 +75,28 @@ def test_slots_without_an_expert_weigh_nothing_at_any_scale(score):
         out = forward(x, 6, score=score, mask=mask, scale=scale)
         assert bool(((out["ids"] >= 0).sum(1) == torch.where(mask, 3, 0)).all())
         assert not out["weights"][out["ids"] < 0].any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("score,normalize", itertools.product(["softmax", "sigmoid"], [True, False]))
+@pytest.mark.parametrize("e,k", LAYOUTS)
+def test_gradient_of_nan_and_inf_logits(e, k, score, normalize, dtype):
+    """NaN where the formula has it.  Without the loss a sigmoid's NaN is its own expert's alone."""
+    x = bad_logits(e, dtype)
+    ok = torch.from_numpy(np.isfinite(as_f64(x)).all(1)).to(DEV)
+    f, sums = forward(x, k, score=score, normalize=normalize), forward(x, k, score=score, normalize=normalize, mask=ok)
+    dw = torch.randn(40, k, generator=torch.Generator().manual_seed(2)).to(DEV)
+    for stats in ((sums["counts"], sums["prob_sum"], torch.tensor([100.0], device=DEV)), None):
+        c, s, dl = (None, None, 0.0) if stats is None else (stats[0].cpu().numpy(), as_f64(stats[1]), float(stats[2]))
+        with np.errstate(invalid="ignore"):
+            ref, mag = oracle.ref_router_backward(as_f64(x), f["ids"].cpu().numpy(), as_f64(dw), c, s, dl, score=score, normalize=normalize)
+        got = as_f64(backward(x, f["ids"], dw, stats, score=score, normalize=normalize))
+        np.testing.assert_array_equal(np.isnan(got), np.isnan(ref))
+        # four factors of a score and three sums of at most 1 + 22 + top_k roundings, and BF16's own
+        tol = (4 * tolerance(as_f64(x)) + 3 * (30 + k) * STEP) * mag + 1e-37
+        if dtype == "bf16":
+            tol = tol + 2.0 ** -8 * (np.abs(ref) + tol) + 2.0 ** -133
+        live = ~np.isnan(ref)
+        assert (np.abs(got - ref)[live] <= tol[live]).all()
+        if score == "sigmoid" and stats is None:
+            assert not np.isnan(got[np.isfinite(as_f64(x))]).any()
