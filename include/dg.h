@@ -463,7 +463,8 @@ size_t dg_get_clip_workspace_size(void);
  * sf         [num_groups][k / 128][ld_sf] words, ld_sf >= m.
  * y          optional [num_groups][m][k], x's dtype: the values that codes and scales
  *            stand for (exact), for a straight-through forward; NaN in blocks with
- *            scale 255, Inf for 2^128, to which inputs past 3.5 * 2^126 round.  May equal x.
+ *            scale 255, Inf for 2^128, to which inputs past 3.5 * 2^126 round.  May equal x
+ *            (with x's row stride).
  * masked_m   optional DEVICE int32 [num_groups]: only the first masked_m[g] rows of a
  *            group are read and written (clamped to [0, m]).
  * k % 128 != 0, more than 65535 groups or more than 2^36 values a group ->
@@ -552,7 +553,8 @@ size_t dg_get_moe_router_workspace_size(int m, int num_experts);
  *               row without any (a masked one) gets zeros.  In other rows a NaN logit makes
  *               NaN of its own gradient and, in a softmax (+inf too) or with dloss, of the row's.
  * counts, prob_sum, dloss (FP32 [1])  all or none.
- * dlogits       [m, num_experts], logits' dtype, row stride ld_dlogits; may equal logits.
+ * dlogits       [m, num_experts], logits' dtype, row stride ld_dlogits; may equal logits
+ *               (with the same row stride).
  * Sizes as above.
  */
 dg_status dg_moe_router_backward(const void* logits, int64_t ld, dg_dtype dtype, dg_score score, int normalize, float scale,

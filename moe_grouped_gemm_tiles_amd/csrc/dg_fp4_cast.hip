@@ -218,6 +218,7 @@ dg_status dg_cast_to_mxfp4(const void* x, int64_t ldx, dg_dtype x_dtype, void* q
     return DG_ERROR_INVALID_VALUE;
   if (ldx < k || (ldx * es) % 16 != 0 || ldq < k / 2 || ldq % 4 != 0 || ld_sf < m) return DG_ERROR_INVALID_VALUE;
   if (y != nullptr && (!aligned_to(y, 16) || ldy < k || (ldy * es) % 16 != 0)) return DG_ERROR_INVALID_VALUE;
+  if (y == x && ldy != ldx && (m > 1 || num_groups > 1)) return DG_ERROR_INVALID_VALUE;  // rows over other rows not yet read
   const int64_t col_blocks = (static_cast<int64_t>(k) + fp4c::kCols - 1) / fp4c::kCols;
   const int64_t blocks = (static_cast<int64_t>(m) + fp4c::kRows - 1) / fp4c::kRows * col_blocks;
   if (col_blocks > 65535 || blocks > (1 << 23) || num_groups > 65535) return DG_ERROR_NOT_SUPPORTED;

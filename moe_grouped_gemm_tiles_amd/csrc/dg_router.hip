@@ -827,6 +827,7 @@ dg_status dg_moe_router_backward(const void* logits, int64_t ld, dg_dtype dtype,
   if (logits == nullptr || !aligned(logits, es) || dlogits == nullptr || !aligned(dlogits, es) || topk_ids == nullptr ||
       !aligned(topk_ids, 4) || dweights == nullptr || !aligned(dweights, 4) || ld < num_experts || ld_dlogits < num_experts)
     return DG_ERROR_INVALID_VALUE;
+  if (dlogits == logits && m > 1 && ld != ld_dlogits) return DG_ERROR_INVALID_VALUE;  // rows over other rows not yet read
   const int64_t ldb = ld * es, ldd = ld_dlogits * es;
   const int vec = num_experts % 4 == 0 && aligned(logits, 4 * es) && ldb % (4 * es) == 0 && aligned(dlogits, 4 * es) &&
                   ldd % (4 * es) == 0;

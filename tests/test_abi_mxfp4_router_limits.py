@@ -6,7 +6,7 @@ import os
 import pytest
 
 import moe_grouped_gemm_tiles_amd as dg
-from tests.test_abi_mxfp4_router import INVALID, UNSUPPORTED, _contiguous, _dense, _masked
+from tests.test_abi_mxfp4_router import INVALID, P, UNSUPPORTED, _cast, _contiguous, _dense, _grad, _masked
 
 
 @pytest.fixture(scope="module")
@@ -43,3 +43,9 @@ def test_scale_arrays_past_their_limit(lib):
     for ld in (1 << 27, 1 << 40, 1 << 61, (1 << 62) - 4):
         assert _dense(lib, ld_sfa=ld) == UNSUPPORTED and _dense(lib, ld_sfb=ld) == UNSUPPORTED
         assert _contiguous(lib, ld_sfa=ld) == UNSUPPORTED and _masked(lib, ld_sfb=ld) == UNSUPPORTED
+
+
+def test_outputs_in_place_need_the_inputs_row_stride(lib):
+    assert _cast(lib, y=P, ldx=512, ldy=520) == INVALID
+    assert _cast(lib, y=P, ldx=512, ldy=520, m=1, g=2) == INVALID
+    assert _grad(lib, x=P, dx=P, ld=64, ld_dx=72) == INVALID
