@@ -467,7 +467,7 @@ size_t dg_get_clip_workspace_size(void);
  *            (with x's row stride).
  * masked_m   optional DEVICE int32 [num_groups]: only the first masked_m[g] rows of a
  *            group are read and written (clamped to [0, m]).
- * k % 128 != 0, more than 65535 groups or more than 2^36 values a group ->
+ * k % 128 != 0, k > 2^25, more than 65535 groups or 2^36 and more values a group ->
  * DG_ERROR_NOT_SUPPORTED; an empty size -> DG_SUCCESS.
  */
 dg_status dg_cast_to_mxfp4(const void* x, int64_t ldx, dg_dtype x_dtype, void* q, int64_t ldq, int32_t* sf,

@@ -32,6 +32,7 @@ namespace fp4c {
 constexpr int kRows = 16;   // rows per workgroup, kBatch for each wave
 constexpr int kCols = 512;  // columns per workgroup (four scale words)
 constexpr int kBatch = 4;   // rows a wave has in flight
+constexpr int kMaxBlocks = 1 << 23;  // workgroups of a launch and group
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
@@ -132,7 +133,7 @@ struct Args {
   uint8_t* y;
   const int32_t* masked_m;
   int64_t ldx_bytes, ldq, ld_sf, ldy_bytes;
-  int m, k;
+  int m, k, first;  // first: of the rows of each group that this launch takes
 };
 
 // Scale byte of a block from the bits of its amax.
@@ -149,7 +150,7 @@ __global__ void __launch_bounds__(256) cast_kernel(const Args a) {
   const int g = blockIdx.y;
   const int col_blocks = (a.k + kCols - 1) / kCols;  // neighbours take the same rows' next columns
   const int row_block = blockIdx.x / col_blocks;
-  const int m0 = row_block * kRows, c0 = (blockIdx.x - row_block * col_blocks) * kCols;
+  const int m0 = a.first + row_block * kRows, c0 = (blockIdx.x - row_block * col_blocks) * kCols;
   const int rows = min(a.masked_m != nullptr ? min(max(a.masked_m[g], 0), a.m) : a.m, m0 + kRows);
   if (m0 >= rows) return;
   const int col = c0 + 8 * lane;
@@ -220,11 +221,10 @@ dg_status dg_cast_to_mxfp4(const void* x, int64_t ldx, dg_dtype x_dtype, void* q
   if (y != nullptr && (!aligned_to(y, 16) || ldy < k || (ldy * es) % 16 != 0)) return DG_ERROR_INVALID_VALUE;
   if (y == x && ldy != ldx && (m > 1 || num_groups > 1)) return DG_ERROR_INVALID_VALUE;  // rows over other rows not yet read
   const int64_t col_blocks = (static_cast<int64_t>(k) + fp4c::kCols - 1) / fp4c::kCols;
-  const int64_t blocks = (static_cast<int64_t>(m) + fp4c::kRows - 1) / fp4c::kRows * col_blocks;
-  if (col_blocks > 65535 || blocks > (1 << 23) || num_groups > 65535) return DG_ERROR_NOT_SUPPORTED;
-  const dim3 grid(static_cast<unsigned>(blocks), num_groups);
-  const fp4c::Args a{static_cast<const uint8_t*>(x), static_cast<uint8_t*>(q), sf, static_cast<uint8_t*>(y), masked_m,
-                     ldx * es, ldq, ld_sf, ldy * es, m, k};
+  const int64_t row_blocks = (static_cast<int64_t>(m) + fp4c::kRows - 1) / fp4c::kRows;
+  if (k > (1 << 25) || static_cast<int64_t>(m) * k >= (1ll << 36) || num_groups > 65535) return DG_ERROR_NOT_SUPPORTED;
+  fp4c::Args a{static_cast<const uint8_t*>(x), static_cast<uint8_t*>(q), sf, static_cast<uint8_t*>(y), masked_m,
+               ldx * es, ldq, ld_sf, ldy * es, m, k, 0};
   // operands past the last-level cache's 256 MiB are streamed (smaller ones are left there for their readers: 4099 x 1408 FP32
   // with y, called again and again, takes 12 us, streamed 18)
   const int64_t bytes = static_cast<int64_t>(num_groups) * m * k * (y ? 2 * es + 1 : es + 1);
@@ -236,9 +236,16 @@ dg_status dg_cast_to_mxfp4(const void* x, int64_t ldx, dg_dtype x_dtype, void* q
   else
     fn = y ? (nt ? fp4c::cast_kernel<false, true, true> : fp4c::cast_kernel<false, true, false>)
            : (nt ? fp4c::cast_kernel<false, false, true> : fp4c::cast_kernel<false, false, false>);
-  hipLaunchKernelGGL(fn, grid, dim3(256), 0, stream, a);
-  const hipError_t e = hipGetLastError();
-  return e == hipSuccess ? DG_SUCCESS : dg::record_hip_error(e);
+  // a grid holds fewer than 2^32 threads: rows past its share take another launch
+  const int64_t most = fp4c::kMaxBlocks / col_blocks;
+  for (int64_t at = 0; at < row_blocks; at += most) {
+    a.first = static_cast<int>(at) * fp4c::kRows;
+    const int64_t blocks = (row_blocks - at < most ? row_blocks - at : most) * col_blocks;
+    hipLaunchKernelGGL(fn, dim3(static_cast<unsigned>(blocks), num_groups), dim3(256), 0, stream, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return dg::record_hip_error(e);
+  }
+  return DG_SUCCESS;
 }
 
 }  // extern "C"

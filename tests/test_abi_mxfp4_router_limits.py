@@ -49,3 +49,10 @@ def test_outputs_in_place_need_the_inputs_row_stride(lib):
     assert _cast(lib, y=P, ldx=512, ldy=520) == INVALID
     assert _cast(lib, y=P, ldx=512, ldy=520, m=1, g=2) == INVALID
     assert _grad(lib, x=P, dx=P, ld=64, ld_dx=72) == INVALID
+
+
+def test_cast_past_its_limits(lib):
+    """The limits are on K, on the values of a group and on groups alone."""
+    for bad in (dict(k=(1 << 25) + 128, m=1), dict(k=128, m=1 << 29), dict(k=1 << 25, m=1 << 11), dict(k=512, m=1 << 27)):
+        k = bad["k"]
+        assert _cast(lib, ldx=k, ldq=k // 2, ld_sf=bad["m"], **bad) == UNSUPPORTED, bad
