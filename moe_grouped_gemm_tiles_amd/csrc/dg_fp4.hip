@@ -752,8 +752,8 @@ struct Plan {
 // 28 dense and 5 masked calls on MI355X (the choice within 10 % of the best candidate's time in all but two of them): 4 us from launch to the first slab and for
 // the last stores, 1 us a round of workgroups, the slabs at a rate of the tile's own (streaming tiles: 40 GB/s a CU), and not
 // less than the operands' bytes at 5.5 TB/s.  A split adds 1.2 us to publish and count partials, their bytes at 6 TB/s twice,
-// and the last workgroup's reading of a tile's at 85 GB/s.  rows: of A, or of a group's (masked: the expected number; groups
-// are taken to have up to twice as many, each as likely).
+// and the last workgroup's reading of a tile's at 85 GB/s.  rows: of A, or of a group's (masked: the expected number, taken
+// to be the mean of evenly spread ones, from 0 up to twice it, or of as wide a spread below most_rows).
 Plan plan(int mode, int64_t groups, int rows, int most_rows, int n, int k, int cus) {
   const int slabs = (k / 128 + 1) / 2;
   const bool masked = mode == dg::MODE_MASKED;
@@ -763,9 +763,10 @@ Plan plan(int mode, int64_t groups, int rows, int most_rows, int n, int k, int c
   // row tiles of a call
   auto row_tiles = [&](int bm) {
     if (!masked) return static_cast<double>(cdiv(rows, bm));
-    const double up_to = std::min<double>(2.0 * rows, most_rows);
+    const double up_to = std::min<double>(2.0 * rows, most_rows), from = 2.0 * rows - up_to;
     double t = 0;
-    for (int j = 0; j * static_cast<double>(bm) < up_to && j < 4096; ++j) t += 1.0 - j * bm / up_to;
+    for (int j = 0; j * static_cast<double>(bm) < up_to && j < 4096; ++j)
+      t += j * bm < from ? 1.0 : (up_to - j * bm) / std::max(up_to - from, 1.0);
     return groups * t;
   };
   auto consider = [&](const Cfg& c, int s) {
@@ -797,6 +798,11 @@ Plan plan(int mode, int64_t groups, int rows, int most_rows, int n, int k, int c
     }
   }
   return best;
+}
+
+// Rows of a masked call's groups, as the caller expects them; half of the room where it does not say.
+inline int rows_of_group(int expected_m, int m_max) {
+  return expected_m > 0 ? std::min(expected_m, m_max) : (m_max + 1) / 2;
 }
 
 template <int MODE>
@@ -933,16 +939,16 @@ dg_status dg_m_grouped_mxfp4_gemm_nt_masked(const void* a, const int32_t* sfa, i
   pp.g.sfb_gs = pp.kw * ld_sfb;
   pp.g.d_gs = static_cast<int64_t>(m_max) * n;
   const int cus = usable_cus();
-  const int rows = expected_m > 0 && expected_m < m_max ? expected_m : (m_max + 1) / 2;
-  return launch<dg::MODE_MASKED>(pp, plan(dg::MODE_MASKED, num_groups, rows, m_max, n, k, cus), d_dtype, num_groups, cus, stream);
+  const Plan pl = plan(dg::MODE_MASKED, num_groups, rows_of_group(expected_m, m_max), m_max, n, k, cus);
+  return launch<dg::MODE_MASKED>(pp, pl, d_dtype, num_groups, cus, stream);
 }
 
 dg_status dg_internal_mxfp4_plan(int mode, int groups, int rows, int most_rows, int n, int k, int cus, int* bm, int* bn,
                                  int* streaming, int* splits, size_t* ws_bytes) {
-  if (mode < 0 || mode > 2 || groups <= 0 || rows <= 0 || most_rows < rows || n <= 0 || k <= 0 || k % 128 != 0 || cus <= 0 ||
+  if (mode < 0 || mode > 2 || groups <= 0 || (rows <= 0 && mode != dg::MODE_MASKED) || most_rows < rows || most_rows <= 0 || n <= 0 || k <= 0 || k % 128 != 0 || cus <= 0 ||
       bm == nullptr || bn == nullptr || streaming == nullptr || splits == nullptr || ws_bytes == nullptr)
     return DG_ERROR_INVALID_VALUE;
-  const Plan pl = plan(mode, groups, rows, most_rows, n, k, cus);
+  const Plan pl = plan(mode, groups, mode == dg::MODE_MASKED ? rows_of_group(rows, most_rows) : rows, most_rows, n, k, cus);
   *bm = pl.cfg.bm;
   *bn = pl.cfg.bn;
   *streaming = is_stream(pl.cfg);

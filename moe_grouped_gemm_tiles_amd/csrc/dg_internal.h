@@ -22,7 +22,7 @@ dg_status dg_internal_dense_plan(int m, int n, int k, int cus, int* bm, int* bn,
                                  size_t* ws_bytes);
 
 // The configuration of a 4-bit call on a device with `cus` usable CUs: mode 0 dense, 1 contiguous, 2 masked; rows of A (masked:
-// the expected rows of a group, of at most most_rows).  Host arithmetic only.  Bad sizes or null outputs ->
+// the call's expected_m, <= 0 where there is none, of at most most_rows).  Host arithmetic only.  Bad sizes or null outputs ->
 // DG_ERROR_INVALID_VALUE.
 dg_status dg_internal_mxfp4_plan(int mode, int groups, int rows, int most_rows, int n, int k, int cus, int* bm, int* bn,
                                  int* streaming, int* splits, size_t* ws_bytes);
