@@ -13,8 +13,8 @@
 // and the index below them, so that a maximum finds value and tie-break at once.  Each lane sorts its keys and keeps five; the
 // largest head is taken top_k times.  Where the bits that the index pushed out, or FP32's errors in score + bias, leave the
 // order open, more are taken and sorted by full values, and at last all keys are compared in FP64 by the whole wave.
-// Sums of scores are held in registers per lane and expert; each workgroup leaves one partial row, which a second kernel adds
-// in FP64 in a fixed order (integer atomics would do for the counts, but FP ones would change the sums from run to run).
+// Sums of scores are held in FP32 registers per lane and expert (one rounding for each of the lane's rows, 20480 rows apart,
+// and for the workgroup's 16 lanes); each workgroup leaves one partial row, which a second kernel adds in FP64 in a fixed order (integer atomics would do for the counts, but FP ones would change the sums from run to run).
 //
 // 33280 x 256 FP32, sigmoid, bias, mask, top 8, loss: 21 us and 7 us for the second kernel (a wave per row with FP64 keys: 258);
 // 34 MB of logits are 5 us of HBM, so the 700 vector instructions for four rows bound it (8 us of them issue alone).  Gradient,
@@ -169,21 +169,41 @@ __device__ __forceinline__ void load_row(const uint8_t* row, int e, int vec, int
   }
 }
 
-// What turns a row's logits into scores: the largest (0 for a row of -inf alone) and 1 / sum of the exponentials.
+// What turns a row's logits into scores: the largest (0 for a row of -inf alone), the sum of the exponentials and 1 / sum.
 struct Norm {
-  float top, inv;
+  float top, sum, inv;
 };
-// exp(-x) overflows to Inf where the sigmoid is below 2^-126: 0.  1 - sigmoid(x) is sigmoid(-x), without cancellation.
+// exp(x), x <= 0, within 3 steps of 2^-24 however far below: the instruction's result for an argument that has been rounded,
+// t = x log2(e), times exp(r) = 1 + r, where r = x - t ln 2 (ln 2 in two parts) is what that rounding lost.  (Of -inf, r is NaN
+// and any number does for it.)  Below 2^-126 the instruction gives 0.
+__device__ __forceinline__ float exp32(float x) {
+  const float t = x * 0x1.715476p+0f, e = __builtin_amdgcn_exp2f(t);
+  const float r = __builtin_fmaf(t, 0x1.05c610p-29f, __builtin_fmaf(-t, 0x1.62e430p-1f, x));
+  return __builtin_fmaf(e, fminf(r, 1.0f), e);
+}
+// Scores in a row's sums and in keys, whose distance is looked at (kNear): an exponential without that correction is off by
+// 2 |x| steps of itself, which is less than one step of the row's largest.  exp(-x) overflows to Inf where the sigmoid is
+// below 2^-126: 0.
 __device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + __expf(-x)); }
+// The score of one logit, as weights have it, to a few steps.
 template <bool SIGMOID>
 __device__ __forceinline__ float score(float x, Norm n) {
-  if constexpr (SIGMOID) return sigmoid(x);
-  return __expf(x - n.top) * n.inv;
+  if constexpr (!SIGMOID) return exp32(x - n.top) / n.sum;
+  const float e = exp32(-fabsf(x));
+  return (x >= 0.f ? 1.0f : e) / (1.0f + e);
+}
+template <int L, int V>
+__device__ __forceinline__ float top_of(const float (&x)[V]) {
+  float top = x[0];
+#pragma unroll
+  for (int i = 1; i < V; ++i) top = fmaxf(top, x[i]);
+  top = max_of<L>(top);
+  return top == -INFINITY ? 0.f : top;
 }
 // A row's exponentials (a softmax is n.inv times them), or its sigmoids, for which n.inv is 1 / (their sum + 1e-20).
 template <int L, int V, bool SIGMOID>
 __device__ __forceinline__ Norm scores(const float (&x)[V], float (&p)[V]) {
-  Norm n{0.f, 0.f};
+  Norm n{0.f, 0.f, 0.f};
   float sum = 0.f;
   if constexpr (SIGMOID) {
 #pragma unroll
@@ -193,18 +213,48 @@ __device__ __forceinline__ Norm scores(const float (&x)[V], float (&p)[V]) {
     }
     n.inv = 1.0f / (sum_of<L>(sum) + kTiny);
   } else {
-    float top = x[0];
-#pragma unroll
-    for (int i = 1; i < V; ++i) top = fmaxf(top, x[i]);
-    top = max_of<L>(top);
-    n.top = top == -INFINITY ? 0.f : top;
+    n.top = top_of<L, V>(x);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       p[i] = __expf(x[i] - n.top);
       sum += p[i];
     }
-    sum = sum_of<L>(sum);
-    n.inv = sum == 0.f ? 0.f : 1.0f / sum;
+    n.sum = sum_of<L>(sum);
+    n.inv = n.sum == 0.f ? 0.f : 1.0f / n.sum;
+  }
+  return n;
+}
+
+// For the gradient, to a few steps each: a row's exponentials as above (for one that is rounded to BF16, 2^-8 of itself,
+// without the correction), or the slopes p (1 - p) of its sigmoids in their logits' place, and dot = the sum of g p over the
+// lane's.  With e = exp(-|x|) and r = 1 / (1 + e) (a Newton step on the
+// instruction's, with what the sum lost) a sigmoid is r or e r, its slope e r^2.
+template <int L, int V, bool BF16, bool SIGMOID>
+__device__ __forceinline__ Norm scores_for_gradient(float (&x)[V], float (&p)[V], const float (&g)[V], float& dot) {
+  if constexpr (!SIGMOID && BF16) return scores<L, V, false>(x, p);
+  Norm n{0.f, 0.f, 0.f};
+  float sum = 0.f;
+  if constexpr (SIGMOID) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float e = exp32(-fabsf(x[i])), d = 1.0f + e, lost = e - (d - 1.0f), r0 = __builtin_amdgcn_rcpf(d);
+      const float r = __builtin_fmaf(__builtin_fmaf(-lost, r0, __builtin_fmaf(-d, r0, 1.0f)), r0, r0), er = e * r;
+      const float v = x[i] >= 0.f ? r : er;
+      x[i] = er * r;
+      sum += v;
+      dot += g[i] * v;
+      asm volatile("" : "+v"(x[i]), "+v"(dot), "+v"(sum));  // now, not where the slopes are used: fewer registers are held
+    }
+    n.inv = 1.0f / (sum_of<L>(sum) + kTiny);
+  } else {
+    n.top = top_of<L, V>(x);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      p[i] = exp32(x[i] - n.top);
+      sum += p[i];
+    }
+    n.sum = sum_of<L>(sum);
+    n.inv = n.sum == 0.f ? 0.f : 1.0f / n.sum;
   }
   return n;
 }
@@ -441,7 +491,7 @@ __global__ void __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_e
       float xv = id >= 0 ? xs[id] : -INFINITY, bv = 0.f, v = xv;
       if (a.bias != nullptr && id >= 0) {
         bv = s_bias[id];
-        v = score<SIGMOID>(xv, n) + bv;
+        v = (SIGMOID ? sigmoid(xv) : __expf(xv - n.top) * n.inv) + bv;
       }
       for (int turn = 0; turn <= L; ++turn) {
         const float up = before<L>(v);
@@ -469,10 +519,10 @@ __global__ void __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_e
     }
     if (l >= a.k || !on) id = -1;
     const float w = id >= 0 ? score<SIGMOID>(xs[id], n) : 0.f;
-    const float f = a.normalize ? a.scale / (sum_of<L>(w) + kTiny) : a.scale;
+    const float chosen = a.normalize ? sum_of<L>(w) + kTiny : 1.0f;
     if (l < a.k && row < m) {
       a.ids[(int64_t)row * a.k + l] = id;
-      a.weights[(int64_t)row * a.k + l] = id >= 0 ? w * f : 0.f;  // (f may be Inf or NaN)
+      a.weights[(int64_t)row * a.k + l] = id >= 0 ? a.scale * w / chosen : 0.f;  // (the sum may be NaN)
     }
     if (stats && id >= 0) atomicAdd(&s_counts[id], 1u);
   }
@@ -652,31 +702,30 @@ __global__ void __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_e
     wave_sync();
 #pragma unroll
     for (int c = 0; c < V / 4; ++c) *reinterpret_cast<float4*>(ds + 4 * (l + L * c)) = make_float4(0.f, 0.f, 0.f, 0.f);
-    const Norm n = scores<L, V, SIGMOID>(x, p);
+    float dot = 0.f;
+    const Norm n = scores_for_gradient<L, V, BF16, SIGMOID>(x, p, g, dot);
     const bool on = any_of<L>(id >= 0, lane);
     if (a.normalize) {
       const float w = score<SIGMOID>(xv, n);  // 0 where there is no expert
-      const float r = 1.0f / (sum_of<L>(w) + kTiny);
-      d = (d - sum_of<L>(d * w) * r) * r;
+      const float chosen = sum_of<L>(w) + kTiny;
+      d = (d - sum_of<L>(d * w) / chosen) / chosen;
     }
     wave_sync();
     if (id >= 0) atomicAdd(&ds[id], d);
     wave_sync();
-    float dot = 0.f, dp[V];
+    float dp[V];
 #pragma unroll
     for (int c = 0; c < V / 4; ++c) {
       const float4 v = *reinterpret_cast<const float4*>(ds + 4 * (l + L * c));
       dp[4 * c] = v.x, dp[4 * c + 1] = v.y, dp[4 * c + 2] = v.z, dp[4 * c + 3] = v.w;
     }
     if constexpr (SIGMOID) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) dot += g[i] * p[i];
       // without the loss nothing depends on the row's sum, which may be NaN
       const float inv = a.counts != nullptr ? n.inv : 0.f;
       dot = a.counts != nullptr ? sum_of<L>(dot) * inv : 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        dp[i] = (dp[i] + (g[i] - dot) * inv) * p[i] * sigmoid(-x[i]);
+        dp[i] = (dp[i] + (g[i] - dot) * inv) * x[i];
       }
     } else {
 #pragma unroll
