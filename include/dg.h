@@ -532,7 +532,7 @@ dg_status dg_m_grouped_mxfp4_gemm_nt_masked(const void* a, const int32_t* sfa, i
  *               aligned, any contents; only where counts are asked for.
  * num_experts in [1, 1024], top_k in [1, min(64, num_experts)], else
  * DG_ERROR_NOT_SUPPORTED; scale >= 0.  m == 0 writes zeros to counts, prob_sum, loss.
- * The same bits every time.  Arithmetic is FP32: the weights' p, and p's slope in the
+ * The same bits every time.  Arithmetic is FP32: the weights' p, and p's slope in an FP32
  * gradient, are within 8 steps of 2^-24 of themselves however small (a softmax's up to
  * the common factor of its row's sum); p below 2^-126 is 0.  prob_sum adds a workgroup's
  * rows (1 in 1280 of a large batch) in FP32 and the workgroups' sums in FP64.

@@ -201,7 +201,7 @@ __device__ __forceinline__ float top_of(const float (&x)[V]) {
   return top == -INFINITY ? 0.f : top;
 }
 // A row's exponentials (a softmax is n.inv times them), or its sigmoids, for which n.inv is 1 / (their sum + 1e-20).
-template <int L, int V, bool SIGMOID>
+template <int L, int V, bool SIGMOID, bool CLOSE = false>
 __device__ __forceinline__ Norm scores(const float (&x)[V], float (&p)[V]) {
   Norm n{0.f, 0.f, 0.f};
   float sum = 0.f;
@@ -216,7 +216,7 @@ __device__ __forceinline__ Norm scores(const float (&x)[V], float (&p)[V]) {
     n.top = top_of<L, V>(x);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      p[i] = __expf(x[i] - n.top);
+      p[i] = CLOSE ? exp32(x[i] - n.top) : __expf(x[i] - n.top);
       sum += p[i];
     }
     n.sum = sum_of<L>(sum);
@@ -225,21 +225,21 @@ __device__ __forceinline__ Norm scores(const float (&x)[V], float (&p)[V]) {
   return n;
 }
 
-// For the gradient, to a few steps each: a row's exponentials as above (for one that is rounded to BF16, 2^-8 of itself,
-// without the correction), or the slopes p (1 - p) of its sigmoids in their logits' place, and dot = the sum of g p over the
-// lane's.  With e = exp(-|x|) and r = 1 / (1 + e) (a Newton step on the
-// instruction's, with what the sum lost) a sigmoid is r or e r, its slope e r^2.
+// For the gradient: a softmax's scores, or the slopes p (1 - p) of a row's sigmoids in their logits' place and dot = the sum of
+// g p over the lane's.  With e = exp(-|x|) and r = 1 / (1 + e) a sigmoid is r or e r, its slope e r^2.  FP32 gradients have them
+// to a few steps: the exponential with its correction, a Newton step on the reciprocal, with what 1 + e lost, and on the
+// quotient by a softmax's sum.  One that is rounded to BF16, 2^-9 of itself at most, does without: 2 |x| steps are 2^-16.
 template <int L, int V, bool BF16, bool SIGMOID>
 __device__ __forceinline__ Norm scores_for_gradient(float (&x)[V], float (&p)[V], const float (&g)[V], float& dot) {
-  if constexpr (!SIGMOID && BF16) return scores<L, V, false>(x, p);
   Norm n{0.f, 0.f, 0.f};
-  float sum = 0.f;
   if constexpr (SIGMOID) {
+    float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const float e = exp32(-fabsf(x[i])), d = 1.0f + e, lost = e - (d - 1.0f), r0 = __builtin_amdgcn_rcpf(d);
-      const float r = __builtin_fmaf(__builtin_fmaf(-lost, r0, __builtin_fmaf(-d, r0, 1.0f)), r0, r0), er = e * r;
-      const float v = x[i] >= 0.f ? r : er;
+      const float e = BF16 ? __expf(-fabsf(x[i])) : exp32(-fabsf(x[i])), d = 1.0f + e;
+      float r = __builtin_amdgcn_rcpf(d);
+      if (!BF16) r = __builtin_fmaf(__builtin_fmaf(d - 1.0f - e, r, __builtin_fmaf(-d, r, 1.0f)), r, r);
+      const float er = e * r, v = x[i] >= 0.f ? r : er;
       x[i] = er * r;
       sum += v;
       dot += g[i] * v;
@@ -247,14 +247,12 @@ __device__ __forceinline__ Norm scores_for_gradient(float (&x)[V], float (&p)[V]
     }
     n.inv = 1.0f / (sum_of<L>(sum) + kTiny);
   } else {
-    n.top = top_of<L, V>(x);
+    n = scores<L, V, false, !BF16>(x, p);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      p[i] = exp32(x[i] - n.top);
-      sum += p[i];
+      const float q = p[i] * n.inv;
+      p[i] = BF16 ? q : __builtin_fmaf(__builtin_fmaf(-q, n.sum, p[i]), n.inv, q);
     }
-    n.sum = sum_of<L>(sum);
-    n.inv = n.sum == 0.f ? 0.f : 1.0f / n.sum;
   }
   return n;
 }
@@ -730,7 +728,6 @@ __global__ void __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_e
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        p[i] *= n.inv;
         dp[i] += g[i];
         dot += dp[i] * p[i];
       }
