@@ -454,7 +454,9 @@ size_t dg_get_clip_workspace_size(void);
  *
  * dg_cast_to_mxfp4: the quantisation, for activations and weights alike.
  *   s = the smallest power of two with amax <= 6 s (1 for a block of zeros; never
- *   below 2^-127), code = E2M1(x / s) to nearest with ties to even.  A block that
+ *   below 2^-127), so that no value is clipped.  (The format's own conversion takes
+ *   floor(log2 amax) - 2 and clips what is past 6 s: its codes differ where amax is
+ *   between 1.5 and 2 times a power of two; either kind is read by the GEMMs.)  code = E2M1(x / s) to nearest with ties to even.  A block that
  *   holds an Inf or NaN gets the scale 255 and zero codes.
  *
  * x          [num_groups][m][k], BF16 or FP32, row stride ldx, 16-B aligned rows;
@@ -529,7 +531,8 @@ dg_status dg_m_grouped_mxfp4_gemm_nt_masked(const void* a, const int32_t* sfa, i
  * counts        optional int32 [num_experts] (masked_m of a masked GEMM).
  * prob_sum, loss  optional FP32 [num_experts], [1]; both or none, and with counts.
  * workspace     dg_get_moe_router_workspace_size(m, num_experts) bytes, 256-byte
- *               aligned, any contents; only where counts are asked for.
+ *               aligned, any contents; only where counts are asked for.  It is left with
+ *               others: clear it before a call that wants it zero-filled.
  * num_experts in [1, 1024], top_k in [1, min(64, num_experts)], else
  * DG_ERROR_NOT_SUPPORTED; scale >= 0.  m == 0 writes zeros to counts, prob_sum, loss.
  * The same bits every time.  Arithmetic is FP32: the weights' p, and p's slope in an FP32

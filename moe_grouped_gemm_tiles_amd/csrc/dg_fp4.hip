@@ -120,9 +120,9 @@ __device__ __forceinline__ bool live_tile(const LiveTiles& t, const dg::Params& 
 // are held back, so that after the slab's one barrier, placed between part 1 and part 2, the matrix cores run from registers
 // while the next slab's outer fragments are read and the loads of the slab after it go out.  Each step is two MFMAs on an
 // accumulator, the first halves of a fragment's products before the second ones, so that none waits for the one before.
-// Bound by the matrix cores' schedule: 4096 x 8192 x 16384 takes 230 us, 4.8 PFLOP/s, with them 0.53 busy at 1.98 GHz (the
-// power limit; the peak is 10 PFLOP/s at 2.4); contiguous 8 x 4096 x 7168 3.9 PFLOP/s, masked 16 x 4096 x 7168 with 103 rows a
-// group on average 68 us (its weights alone are 40 us of HBM).
+// Bound by the matrix cores' schedule: 4096 x 7168 x 16384 takes 218 us, 4.4 PFLOP/s, with them 0.53 busy at 1.98 GHz (the
+// power limit; the peak is 10 PFLOP/s at 2.4), 4096 x 8192 x 16384 240 us, 4.6 PFLOP/s; contiguous 8 x 4096 x 7168 3.9 PFLOP/s,
+// masked 16 x 4096 x 7168 with 103 rows a group on average 68 us (its weights alone are 40 us of HBM).
 template <int BM, int BN, int WM, int WN, int MODE, bool BF16_OUT, bool HAS_C>
 __global__ void __launch_bounds__(WM * WN * 64) gemm_kernel(const Params pp) {
   const dg::Params& p = pp.g;
@@ -748,12 +748,13 @@ struct Plan {
   size_t ws_bytes;  // 0: no split
 };
 
-// The configuration (and, for a dense call, the K split) with the least estimated time, in microseconds, fitted to sweeps of
-// 28 dense and 5 masked calls on MI355X (the choice within 10 % of the best candidate's time in all but two of them): 4 us from launch to the first slab and for
-// the last stores, 1 us a round of workgroups, the slabs at a rate of the tile's own (streaming tiles: 40 GB/s a CU), and not
-// less than the operands' bytes at 5.5 TB/s.  A split adds 1.2 us to publish and count partials, their bytes at 6 TB/s twice,
-// and the last workgroup's reading of a tile's at 85 GB/s.  rows: of A, or of a group's (masked: the expected number, taken
-// to be the mean of evenly spread ones, from 0 up to twice it, or of as wide a spread below most_rows).
+// The configuration (and, for a dense call, the K split) with the least estimated time, in microseconds, its constants set by
+// hand from timings on MI355X: 4 us from launch to the first slab and for the last stores, 1 us a round of workgroups, the slabs
+// at a rate of the tile's own (streaming tiles: 40 GB/s a CU), and not less than the operands' bytes at 5.5 TB/s.  A split adds
+// 1.2 us to publish and count partials, their bytes at 6 TB/s twice, and the last workgroup's reading of a tile's at 85 GB/s.
+// rows: of A, or of a group's (masked: the expected number, taken to be the mean of evenly spread ones, from 0 up to twice it,
+// or of as wide a spread below most_rows).  Against every configuration forced, the choice is within 15 % of the best one's time
+// in 30 dense calls (23 within 5 %) and in 9 of 12 masked ones (17, 23 and 33 % over it in the others).
 Plan plan(int mode, int64_t groups, int rows, int most_rows, int n, int k, int cus) {
   const int slabs = (k / 128 + 1) / 2;
   const bool masked = mode == dg::MODE_MASKED;

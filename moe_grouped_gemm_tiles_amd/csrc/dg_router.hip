@@ -14,11 +14,13 @@
 // largest head is taken top_k times.  Where the bits that the index pushed out, or FP32's errors in score + bias, leave the
 // order open, more are taken and sorted by full values, and at last all keys are compared in FP64 by the whole wave.
 // Sums of scores are held in FP32 registers per lane and expert (one rounding for each of the lane's rows, 20480 rows apart,
-// and for the workgroup's 16 lanes); each workgroup leaves one partial row, which a second kernel adds in FP64 in a fixed order (integer atomics would do for the counts, but FP ones would change the sums from run to run).
+// and for the 16 rows that a workgroup has at work); each workgroup leaves one partial row, which a second kernel adds in FP64
+// in a fixed order (integer atomics would do for the counts, but FP ones would change the sums from run to run).
 //
 // 33280 x 256 FP32, sigmoid, bias, mask, top 8, loss: 21 us and 7 us for the second kernel (a wave per row with FP64 keys: 258);
-// 34 MB of logits are 5 us of HBM, so the 700 vector instructions for four rows bound it (8 us of them issue alone).  Gradient,
-// BF16: 15 us (510 instructions for four rows).
+// 34 MB of logits are 5 us of HBM, so the 720 vector instructions for four rows bound it (8 us of them issue alone).  Gradient,
+// BF16: 15 us (530 instructions for four rows).  A batch of rows that all need the exact choice (with a bias, scores that
+// saturate or lie closer than kNear) takes up to four times as long: 33280 x 256 93 us sigmoid, 102 us softmax.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
