@@ -487,8 +487,9 @@ dg_status dg_cast_to_mxfp4(const void* x, int64_t ldx, dg_dtype x_dtype, void* q
  *              of 4, 16-B aligned.
  *   workspace  dg_get_mxfp4_workspace_size(m, n, k) bytes for the dense form, as
  *              described at the top.
- * Rows of 8 MiB or more (lda, ldb; also where k == 0), scale arrays of 2 GiB or more
- * and 2^29 or more rows or columns -> DG_ERROR_NOT_SUPPORTED.  A block whose scale is 255 makes its row of A (of B: its column of D) NaN.
+ * Rows of 8 MiB or more (lda, ldb; also where k == 0), scale arrays of 2 GiB or more,
+ * 2^29 or more rows or columns and more than 2^30 tiles of at least 32 x 128 (of all
+ * groups' m_max rows) -> DG_ERROR_NOT_SUPPORTED.  A block whose scale is 255 makes its row of A (of B: its column of D) NaN.
  * All of K accumulates in the matrix cores' FP32; C is added in FP32 and D rounded
  * once.  The same bits every time for a shape and CU count.
  */

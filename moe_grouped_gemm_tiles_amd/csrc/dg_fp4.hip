@@ -814,7 +814,7 @@ dg_status launch(fp4::Params& pp, const Plan& pl, dg_dtype t, int groups_for_til
   p.splits = pl.splits;
   p.slabs_per_split = pl.slabs_per_split;
   const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n * groups_for_tiles * pl.splits;
-  if (tiles > 0x7fffffff) return DG_ERROR_NOT_SUPPORTED;
+  if (tiles > (1 << 30)) return DG_ERROR_NOT_SUPPORTED;  // a tile's number and the grid's workgroups are added
   p.num_tiles = static_cast<int>(tiles);
   const int slots = cus * pl.cfg.per_cu;
   const int grid = p.num_tiles < slots ? p.num_tiles : slots;

@@ -56,3 +56,9 @@ def test_cast_past_its_limits(lib):
     for bad in (dict(k=(1 << 25) + 128, m=1), dict(k=128, m=1 << 29), dict(k=1 << 25, m=1 << 11), dict(k=512, m=1 << 27)):
         k = bad["k"]
         assert _cast(lib, ldx=k, ldq=k // 2, ld_sf=bad["m"], **bad) == UNSUPPORTED, bad
+
+
+def test_more_tiles_than_an_int_counts_with_the_grid(lib):
+    """Without K a masked call's groups are its output alone: one tile each here."""
+    for g in ((1 << 30) + 1, 2 ** 31 - 1):
+        assert _masked(lib, g=g, m=1, n=8, k=0, ld_sfa=4, ld_sfb=8) == UNSUPPORTED
