@@ -7,7 +7,8 @@ pytestmark = pytest.mark.gpu
 
 if torch.cuda.is_available():  # pragma: no cover - GPU only
     import moe_grouped_gemm_tiles_amd as dg
-    from tests._gpu_harness import DEV
+    from tests._gpu_harness import DEV, as_f64
+    from tests.test_gpu_router import DT, backward, check_backward, check_forward, forward
 
 
 @pytest.mark.parametrize("m", [(1 << 28) + 77, (1 << 31) - 5])
@@ -44,3 +45,19 @@ def test_router_of_as_many_rows_as_an_int_counts(m, stats):
         on, got = mask[at:at + (1 << 27)], dx[at:at + (1 << 27), 0]
         assert not got[~on].any()
         assert bool(((got[on].float() - want).abs() <= (2.0 ** -8 + 2.0 ** -18) * want).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("at,wide", [(1, 71), (1, 72), (2, 76), (3, 137)])
+@pytest.mark.parametrize("e", [60, 64])
+def test_rows_that_are_aligned_to_their_type_alone(e, at, wide, dtype):
+    m, k = 90, 5
+    x = torch.randn(m, wide, generator=torch.Generator().manual_seed(at)).to(DT[dtype]).to(DEV)[:, at:at + e]
+    for score in ("softmax", "sigmoid"):
+        f = forward(x, k, score=score)
+        check_forward(f, as_f64(x), k, score=score)
+        dw = torch.randn(m, k, generator=torch.Generator().manual_seed(2)).to(DEV)
+        stats = (f["counts"], f["prob_sum"], torch.tensor([50.0], device=DEV))
+        whole = torch.full((m, wide), 9.0, dtype=DT[dtype], device=DEV)
+        check_backward(backward(x, f["ids"], dw, stats, out=whole[:, at:at + e], score=score), x, f["ids"], dw, stats, dtype, score=score)
+        assert bool((whole[:, :at] == 9).all()) and bool((whole[:, at + e:] == 9).all())
